@@ -11,6 +11,10 @@
  *   kv_attn_decode_static        kv_attn_decode without a caller workspace (allocates nothing)
  *   kv_attn_verify, kv_verify_commit   speculative-decoding verify block and its commit
  *   lmhead_topk                  final RMSNorm + lm_head + the k best ids
+ *   lmhead_logprobs              log probabilities of given tokens, entropy, top alternatives
+ *   kv_cache_append_q4, kv_cache_expand_q4, kv_attn_decode_q4
+ *                                a cache held in 4 bits: its append, its read-back into a kva_cache
+ *                                and the attention of new tokens over it
  * plus workspace sizers (kva_workspace_size and the per-call ones), error strings, the
  * version, and the counter of in-kernel waits that gave up (kva_wait_timeouts).
  *
@@ -353,6 +357,115 @@ size_t kva_lmhead_workspace_size(int32_t B, int32_t H);
 size_t kva_lmhead_workspace_zero_bytes(int32_t B);
 
 /* ---------------------------------------------------------------------------------
+ * lmhead_logprobs  (log probabilities of given tokens, entropy and top alternatives)
+ *   z_b[v] = W[v] . h_b' for v < V, h' as in lmhead_topk (final RMSNorm when norm_w is given);
+ *     lse_b = log sum_v exp(z_b[v]);   logprob_b = z_b[targets[b]] - lse_b;
+ *     entropy_b = lse_b - sum_v exp(z_b[v] - lse_b) z_b[v]   (nats);
+ *     the top_k tokens of largest z_b with their log probabilities, equal logits toward the
+ *     lower id.
+ *   What a server returns beside a sampled token, what speculative sampling needs of its draft
+ *   tokens (B = sequences x block), and the scoring of a prompt (B = its tokens).  The logits
+ *   stay on the chip: a pass over the table keeps, per row, the running maximum, the sums and a
+ *   few more candidates than top_k; the target and the candidates are then scored again in
+ *   twice float32 precision, which fixes their order.
+ *  h            [B,H] of h_dtype (device);  norm_w [H] float32 or NULL;  W [V_rows,H] of w_dtype
+ *  targets      [B] int32 (device) or NULL: the given tokens.  A negative target means no token
+ *               (a padded row): its logprob is 0.  A target >= V has logprob NaN.
+ *  out_logprob  [B] float32 (needs targets);  out_entropy, out_lse [B] float32: each may be NULL
+ *  top_ids      [B,top_k] int32, top_logprobs [B,top_k] float32 or NULL; top_k = 0: neither read
+ *  workspace    kva_lmhead_logprobs_workspace_size(B, H, V, top_k) bytes, of any contents.  Calls
+ *               sharing one workspace must not overlap on the GPU.
+ *  0 <= top_k <= KVA_LOGPROBS_MAX_TOP and top_k <= V, else KVA_EINVAL.  NaN inputs are outside the
+ *  contract (a row with one gives NaN or id -1).  Errors as lmhead_topk.  B == 0 is a no-op. */
+#define KVA_LOGPROBS_MAX_TOP 24
+kva_status lmhead_logprobs(
+    const void* h, kva_dtype h_dtype, const float* norm_w, float eps, const void* W, kva_dtype w_dtype,
+    int32_t B, int32_t H, int32_t V, int32_t V_rows,
+    const int32_t* targets, float* out_logprob, float* out_entropy, float* out_lse,
+    int32_t top_k, int32_t* top_ids, float* top_logprobs,
+    void* workspace, size_t workspace_bytes, kva_stream stream);
+size_t kva_lmhead_logprobs_workspace_size(int32_t B, int32_t H, int32_t V, int32_t top_k);
+
+/* ---------------------------------------------------------------------------------
+ * A cache held in 4 bits
+ *   A row (one slot of one KV head) of D values is cut into G = D/64 groups of 64.  A group holds
+ *   a scale and a midpoint, both bf16, and 64 codes u in 0..15, and stands for the values
+ *     scale * (u - 8) + mid.
+ *   The append chooses scale = (max - min) / 15 rounded up to bf16, mid = min + 8 scale rounded to
+ *   bf16 and u = 8 + (x - mid) / scale rounded (half to even) into -8..7, so that a value is off
+ *   by at most scale / 2 plus half a bf16 step of mid.  A group of equal values has scale 0 and
+ *   stands for their bf16 rounding; a group with a NaN, an infinity or a spread beyond float32
+ *   stands for NaN throughout.  A row takes D/2 + 4G bytes: 72 for D = 128 (256 in bf16).
+ *  Layout (KV head g, slot s: row g * capacity + s of its instance)
+ *     k, v              codes: D/8 little-endian 32-bit words a row, 8 codes each, lowest dim in the
+ *                       lowest 4 bits; word w holds dims 64 * (w % G) + 8 * (w / G) + 0..7
+ *     k_scale, v_scale  bf16 pairs (scale, mid), G a row
+ *  Instance i starts inst_rows rows after instance i - 1 in all four arrays (0: n_kv_heads *
+ *  capacity).  head_dim and head_dim_v (0: head_dim) are multiples of 64 up to 256, capacity is a
+ *  multiple of 4 (else KVA_EALIGN), pointers are 16-byte aligned, inst_rows is a multiple of 4. */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t capacity;
+  int32_t head_dim_v;
+  int64_t inst_rows;
+} kva_cache_q4;
+
+/* kv_cache_append_q4: kv_cache_append_rope_qknorm into a 4-bit cache; arguments, conventions and
+ *   errors as there, and
+ *  - q and q_out may both be NULL: K and V only;
+ *  - a slot may be written once per instance and call (a row's codes and scales are separate
+ *    writes): slots that repeat within an instance are refused with KVA_EINVAL;
+ *  - values are quantised from float32, after QK-Norm and RoPE. */
+kva_status kv_cache_append_q4(
+    const void* q, const void* k, const void* v, kva_dtype in_dtype,
+    int32_t N, int32_t T, int32_t n_q_heads,
+    const int32_t* pos, int64_t pos_inst_stride,
+    const int32_t* slot, int64_t slot_inst_stride, const int32_t* slot_host,
+    kva_qknorm norm, kva_rope rope,
+    void* q_out, kva_dtype q_out_dtype,
+    kva_cache_q4 cache, kva_stream stream);
+
+/* kv_cache_expand_q4: the values of slots of a 4-bit cache, rounded to the dtype of `dst`:
+ *     dst_n[g, dst_first + i, :] = value(cache_n[g, slot[n,i], :])     i < T
+ *   For kv_attn_prefill and kv_attn_verify over a prefix held in 4 bits, and for moving slots.
+ *  slot    [.., T] int32 source slots (device; instance n reads slot + n*slot_inst_stride), with
+ *          host mirror slot_host; a slot may repeat.  dst: a kva_cache with the same KV heads and
+ *          head dims.
+ *  Errors: KVA_EINVAL, KVA_ECAPACITY (a source slot outside the cache, dst_first + T beyond dst),
+ *          KVA_EALIGN, KVA_ECUDA.  N == 0 or T == 0 is a no-op. */
+kva_status kv_cache_expand_q4(
+    kva_cache_q4 cache, const int32_t* slot, int64_t slot_inst_stride, const int32_t* slot_host,
+    int32_t N, int32_t T, kva_cache dst, int32_t dst_first, kva_stream stream);
+
+/* kv_attn_decode_q4: attention of the last T tokens of each instance over its 4-bit cache (T = 1:
+ *   a decode step; T > 1: a draft block or the end of a prompt).  The tokens already sit in slots
+ *   L-T .. L-1; token i attends to slots 0 .. L-T+i:
+ *     o = softmax(q K^T * scale) V over those slots' values.
+ *  q          [B,T,Hq,Dk] of q_dtype (device);  out [B,T,Hq,Dv] float32 (device)
+ *  lengths    [B] valid slots, 0 <= L <= capacity (device) + lengths_host (host mirror or an upper
+ *             bound: validation and planning).  A token that sees no slot (L - T + i < 0: a padding
+ *             instance with L = 0, or a block longer than its sequence) gives a row of zeros.
+ *  Probabilities meet the codes as two bf16 halves (about 17 significant bits), a float32 q as
+ *  two halves likewise; all sums are float32.  Slots at or beyond L are never used, whatever they
+ *  hold.  Any Hq/Hkv.  1 <= T <= KVA_DECODE_Q4_MAX_BLOCK.
+ *  workspace  as for kv_attn_decode, sized by kva_decode_q4_workspace_size; zero before the first
+ *             call (its first kva_decode_q4_workspace_zero_bytes bytes), left so by every call.
+ *  Built for (Dk, Dv) = (64, 64), (128, 128) and (192, 128).  Errors as kv_attn_decode. */
+#define KVA_DECODE_Q4_MAX_BLOCK 64
+kva_status kv_attn_decode_q4(
+    const void* q, kva_dtype q_dtype, kva_cache_q4 cache,
+    const int32_t* lengths, const int32_t* lengths_host, int32_t B, int32_t T, int32_t n_q_heads,
+    float scale, float* out, void* workspace, size_t workspace_bytes, kva_stream stream);
+size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T,
+                                    int32_t max_len, int32_t head_dim_v);
+size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T);
+
+/* ---------------------------------------------------------------------------------
  * kva_workspace_size
  *   One sizer for every call that takes a workspace (the boundary lists a single
  *   kva_workspace_size(which, ...)); it returns what the per-call sizer above returns for
@@ -362,13 +475,18 @@ size_t kva_lmhead_workspace_zero_bytes(int32_t B);
  *     KVA_WS_VERIFY        kv_attn_verify: the same plus block (k)
  *     KVA_WS_LMHEAD        lmhead_argmax: B, hidden
  *     KVA_WS_LMHEAD_TOPK   lmhead_topk: B, hidden, vocab, block (top_k)
+ *     KVA_WS_DECODE_Q4     kv_attn_decode_q4: B, n_kv_heads, n_q_heads, max_len, head_dim (Dv),
+ *                          block (T)
+ *     KVA_WS_LMHEAD_LOGPROBS  lmhead_logprobs: B, hidden, vocab, block (top_k, 0 allowed)
  *   Fields a kind does not read are ignored.  Returns 0 for an unknown kind, a NULL `dims` or
  *   a dimension that is not positive. */
 typedef enum {
   KVA_WS_DECODE = 0,
   KVA_WS_VERIFY = 1,
   KVA_WS_LMHEAD = 2,
-  KVA_WS_LMHEAD_TOPK = 3
+  KVA_WS_LMHEAD_TOPK = 3,
+  KVA_WS_DECODE_Q4 = 4,
+  KVA_WS_LMHEAD_LOGPROBS = 5
 } kva_workspace_kind;
 
 typedef struct {
@@ -379,7 +497,7 @@ typedef struct {
   int32_t head_dim;  /* value head width Dv of the attention output */
   int32_t hidden;    /* lm_head hidden size H */
   int32_t vocab;     /* lm_head candidate rows V */
-  int32_t block;     /* verify block length k, or top_k */
+  int32_t block;     /* verify block length k, decode_q4 block T, or top_k */
 } kva_workspace_dims;
 
 size_t kva_workspace_size(int32_t which, const kva_workspace_dims* dims);

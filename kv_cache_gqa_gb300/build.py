@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkv_attn.so")
-SOURCES = ["kv_attn_api.cu", "append.cu", "append_general.cu", "decode.cu", "decode_mma.cu", "decode_static.cu", "lmhead.cu", "lmhead_tc.cu", "lmhead_topk.cu",
-           "prefill_simt.cu", "prefill_tc.cu", "verify_mma.cu", "verify_tc.cu"]
+SOURCES = ["kv_attn_api.cu", "append.cu", "append_general.cu", "append_q4.cu", "decode.cu", "decode_mma.cu", "decode_q4.cu",
+           "decode_static.cu", "lmhead.cu", "lmhead_tc.cu", "lmhead_topk.cu", "logprobs.cu", "prefill_simt.cu", "prefill_tc.cu", "verify_mma.cu", "verify_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -185,6 +185,61 @@ size_t decode_ws_bytes(int B, int Hkv, int Hq, int max_chunks, int D) {
          sizeof(float) * (size_t)B * Hq * max_chunks * D;
 }
 
+// Checks a 4-bit cache and resolves its defaults in place (head_dim_v, inst_rows).
+kva_status check_cache_q4(kva_cache_q4& c, int n_instances) {
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return fail(KVA_EINVAL, "4-bit cache: a pointer is NULL");
+  if (c.head_dim_v < 0 || c.inst_rows < 0) return fail(KVA_EINVAL, "negative head_dim_v or inst_rows");
+  if (c.n_kv_heads <= 0 || c.head_dim <= 0 || c.capacity <= 0)
+    return fail(KVA_EINVAL, "4-bit cache shape must be positive (Hkv=%d D=%d capacity=%d)", c.n_kv_heads, c.head_dim,
+                c.capacity);
+  if (c.head_dim_v == 0) c.head_dim_v = c.head_dim;
+  const int64_t rows = (int64_t)c.n_kv_heads * c.capacity;
+  if (c.inst_rows == 0) c.inst_rows = rows;
+  if (n_instances > 1 && c.inst_rows < rows)
+    return fail(KVA_EINVAL, "4-bit cache inst_rows %lld < Hkv*capacity = %lld", (long long)c.inst_rows, (long long)rows);
+  if (c.head_dim % Q4_GROUP != 0 || c.head_dim_v % Q4_GROUP != 0)
+    return fail(KVA_EALIGN, "4-bit cache: head dims %d/%d are not multiples of %d", c.head_dim, c.head_dim_v, Q4_GROUP);
+  if (c.head_dim > 256 || c.head_dim_v > 256)
+    return fail(KVA_EUNSUPPORTED, "4-bit cache: head dims %d/%d above 256", c.head_dim, c.head_dim_v);
+  if (c.capacity % 4 != 0 || c.inst_rows % 4 != 0)
+    return fail(KVA_EALIGN, "4-bit cache: capacity %d and inst_rows %lld must be multiples of 4", c.capacity,
+                (long long)c.inst_rows);
+  if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k_scale) || !aligned16(c.v_scale))
+    return fail(KVA_EALIGN, "4-bit cache pointers must be 16-byte aligned");
+  if (c.n_kv_heads > 65535) return fail(KVA_EUNSUPPORTED, "4-bit cache: more than 65535 KV heads");
+  return KVA_OK;
+}
+
+Q4Cache q4_args(const kva_cache_q4& c) {
+  Q4Cache a{};
+  a.k = static_cast<uint32_t*>(c.k); a.v = static_cast<uint32_t*>(c.v);
+  a.ks = static_cast<uint32_t*>(c.k_scale); a.vs = static_cast<uint32_t*>(c.v_scale);
+  a.Hkv = c.n_kv_heads; a.capacity = c.capacity; a.Dk = c.head_dim; a.Dv = c.head_dim_v;
+  a.inst_rows = c.inst_rows;
+  return a;
+}
+
+// Slots of one instance: inside the cache and, when `once`, none of them twice.
+kva_status check_slots(const int32_t* slots, int n, int T, int capacity, bool once) {
+  bool ascending = true;
+  for (int t = 0; t < T; ++t) {
+    if (slots[t] < 0 || slots[t] >= capacity)
+      return fail(KVA_ECAPACITY, "slot %d of instance %d token %d outside [0, %d)", slots[t], n, t, capacity);
+    if (t > 0 && slots[t] <= slots[t - 1]) ascending = false;
+  }
+  if (!once || ascending) return KVA_OK;
+  try {
+    std::vector<int32_t> sorted(slots, slots + T);
+    std::sort(sorted.begin(), sorted.end());
+    for (int t = 1; t < T; ++t)
+      if (sorted[t] == sorted[t - 1])
+        return fail(KVA_EINVAL, "slot %d of instance %d is written twice in one call", sorted[t], n);
+  } catch (...) {
+    return fail(KVA_EINVAL, "no host memory to check %d slots", T);
+  }
+  return KVA_OK;
+}
+
 int decode_max_chunks_bound(int max_len) {
   return std::max(1, std::min(DECODE_MAX_CHUNKS, (max_len + DECODE_CHUNK_ALIGN - 1) / DECODE_CHUNK_ALIGN));
 }
@@ -309,6 +364,9 @@ size_t kva_workspace_size(int32_t which, const kva_workspace_dims* d) {
       return kva_verify_workspace_size(d->B, d->n_kv_heads, d->n_q_heads, d->block, d->max_len, d->head_dim);
     case KVA_WS_LMHEAD: return kva_lmhead_workspace_size(d->B, d->hidden);
     case KVA_WS_LMHEAD_TOPK: return kva_lmhead_topk_workspace_size(d->B, d->hidden, d->vocab, d->block);
+    case KVA_WS_DECODE_Q4:
+      return kva_decode_q4_workspace_size(d->B, d->n_kv_heads, d->n_q_heads, d->block, d->max_len, d->head_dim);
+    case KVA_WS_LMHEAD_LOGPROBS: return kva_lmhead_logprobs_workspace_size(d->B, d->hidden, d->vocab, d->block);
   }
   return 0;
 }
@@ -734,6 +792,218 @@ kva_status lmhead_topk(
   }
   if (e == cudaSuccess) count_launches(n_launch);
   return cuda_status(e, "lm_head top-k launch");
+}
+
+size_t kva_lmhead_logprobs_workspace_size(int32_t B, int32_t H, int32_t V, int32_t top_k) {
+  if (B <= 0 || H <= 0 || V <= 0 || top_k < 0 || top_k > LOGPROB_TOP_MAX) return 0;
+  return logprob_workspace_bytes(B, H, V, top_k);
+}
+
+kva_status lmhead_logprobs(
+    const void* h, kva_dtype h_dtype, const float* norm_w, float eps, const void* W, kva_dtype w_dtype,
+    int32_t B, int32_t H, int32_t V, int32_t V_rows,
+    const int32_t* targets, float* out_logprob, float* out_entropy, float* out_lse,
+    int32_t top_k, int32_t* top_ids, float* top_logprobs,
+    void* workspace, size_t workspace_bytes, kva_stream stream) {
+  if (B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", B);
+  if (B == 0) return KVA_OK;
+  if (top_k < 0 || top_k > LOGPROB_TOP_MAX) return fail(KVA_EINVAL, "top_k=%d outside [0, %d]", top_k, LOGPROB_TOP_MAX);
+  if (!valid_dtype(h_dtype) || !valid_dtype(w_dtype)) return fail(KVA_EINVAL, "unknown dtype");
+  if (H <= 0 || V <= 0 || V_rows <= 0) return fail(KVA_EINVAL, "H, V, V_rows must be positive");
+  if (V > V_rows) return fail(KVA_EINVAL, "vocab V=%d exceeds the table's %d rows", V, V_rows);
+  if (top_k > V) return fail(KVA_EINVAL, "top_k=%d exceeds the vocab %d", top_k, V);
+  if (norm_w && !(eps >= 0.f)) return fail(KVA_EINVAL, "final-norm eps must be >= 0");
+  if (H % 8 != 0) return fail(KVA_EALIGN, "hidden %d is not a multiple of 8", H);
+  if (H > lmhead_max_hidden()) return fail(KVA_EUNSUPPORTED, "hidden %d > %d", H, lmhead_max_hidden());
+  if (!h || !W) return fail(KVA_EINVAL, "NULL h/W");
+  if ((targets != nullptr) != (out_logprob != nullptr))
+    return fail(KVA_EINVAL, "targets and out_logprob must both be given or both be NULL");
+  if (top_k > 0 && !top_ids) return fail(KVA_EINVAL, "top_k=%d needs top_ids", top_k);
+  if (!out_logprob && !out_entropy && !out_lse && top_k == 0) return fail(KVA_EINVAL, "no output asked for");
+  if (!aligned16(h) || !aligned16(W) || (norm_w && !aligned16(norm_w)))
+    return fail(KVA_EALIGN, "h, W and norm_w must be 16-byte aligned");
+  if (B > 65535) return fail(KVA_EUNSUPPORTED, "lm_head log probabilities: B=%d > 65535", B);
+  if (!workspace) return fail(KVA_EWORKSPACE, "lm_head: workspace is NULL");
+  if (!aligned16(workspace)) return fail(KVA_EALIGN, "workspace must be 16-byte aligned");
+  const size_t need = logprob_workspace_bytes(B, H, V, top_k);
+  if (workspace_bytes < need)
+    return fail(KVA_EWORKSPACE, "lm_head log-probability workspace %zu bytes < %zu needed", workspace_bytes, need);
+  LogprobArgs a{};
+  a.h = h; a.h_dtype = (int)h_dtype; a.norm_w = norm_w; a.eps = eps; a.W = W;
+  a.B = B; a.H = H; a.V = V;
+  a.targets = targets; a.out_logprob = out_logprob; a.out_entropy = out_entropy; a.out_lse = out_lse;
+  a.top_k = top_k; a.top_ids = top_ids; a.top_logprobs = top_logprobs;
+  unsigned n_launch = 0;
+  const cudaError_t e = launch_logprobs(a, w_dtype, workspace, (cudaStream_t)stream, &n_launch);
+  if (e == cudaSuccess) count_launches(n_launch);
+  return cuda_status(e, "lm_head log-probability launch");
+}
+
+kva_status kv_cache_append_q4(
+    const void* q, const void* k, const void* v, kva_dtype in_dtype,
+    int32_t N, int32_t T, int32_t n_q_heads,
+    const int32_t* pos, int64_t pos_inst_stride,
+    const int32_t* slot, int64_t slot_inst_stride, const int32_t* slot_host,
+    kva_qknorm norm, kva_rope rope,
+    void* q_out, kva_dtype q_out_dtype,
+    kva_cache_q4 cache, kva_stream stream) {
+  if (N < 0 || T < 0) return fail(KVA_EINVAL, "N=%d T=%d must be >= 0", N, T);
+  if (N == 0 || T == 0) return KVA_OK;
+  if (!valid_dtype(in_dtype) || (q && !valid_dtype(q_out_dtype))) return fail(KVA_EINVAL, "unknown dtype");
+  kva_status st = check_cache_q4(cache, N);
+  if (st != KVA_OK) return st;
+  const int Dk = cache.head_dim, Hkv = cache.n_kv_heads;
+  if ((q != nullptr) != (q_out != nullptr)) return fail(KVA_EINVAL, "q and q_out must both be given or both be NULL");
+  if (q && (n_q_heads <= 0 || n_q_heads % Hkv != 0))
+    return fail(KVA_EINVAL, "n_q_heads %d must be a positive multiple of n_kv_heads %d", n_q_heads, Hkv);
+  if (!k || !v || !slot || !slot_host) return fail(KVA_EINVAL, "NULL k/v/slot");
+  if (rope.kind != KVA_ROPE_NONE && !pos) return fail(KVA_EINVAL, "RoPE needs positions");
+  if (pos_inst_stride < 0 || slot_inst_stride < 0) return fail(KVA_EINVAL, "negative instance stride");
+  if ((norm.q_w == nullptr) != (norm.k_w == nullptr))
+    return fail(KVA_EINVAL, "q and k norm weights must both be given or both be NULL");
+  if (norm.q_w && (!(norm.eps >= 0.f) || norm.inst_stride < 0))
+    return fail(KVA_EINVAL, "QK-Norm eps must be >= 0 and inst_stride >= 0");
+  int rot_off = 0, rot_w = Dk;
+  if (rope.kind != KVA_ROPE_NONE && (st = rope_range(rope, Dk, &rot_off, &rot_w)) != KVA_OK) return st;
+  if (N > 65535) return fail(KVA_EUNSUPPORTED, "append: N=%d > 65535", N);
+  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))))
+    return fail(KVA_EALIGN, "q/k/v/q_out must be 16-byte aligned");
+  if (norm.q_w && (!aligned16(norm.q_w) || !aligned16(norm.k_w) || (norm.inst_stride * 4) % 16 != 0))
+    return fail(KVA_EALIGN, "norm weights must be 16-byte aligned with a 16-byte instance stride");
+  AppendQ4Args a{};
+  if ((st = build_rope_table(rope, rot_w, &a.rope)) != KVA_OK) return st;
+  for (int n = 0; n < N; ++n) {
+    if (n > 0 && slot_inst_stride == 0) break;             // one list for every instance
+    if ((st = check_slots(slot_host + (int64_t)n * slot_inst_stride, n, T, cache.capacity, true)) != KVA_OK) return st;
+  }
+  a.q = q; a.k = k; a.v = v; a.q_out = q_out;
+  a.pos = pos; a.pos_stride = pos_inst_stride; a.slot = slot; a.slot_stride = slot_inst_stride;
+  a.q_w = norm.q_w; a.k_w = norm.k_w; a.w_stride = norm.inst_stride; a.eps = norm.eps;
+  a.after_rope = norm.after_rope ? 1 : 0;
+  a.N = N; a.T = T; a.Hq = q ? n_q_heads : 0;
+  a.rot_offset = rot_off; a.rot_dim = rot_w;
+  a.c = q4_args(cache);
+  const cudaError_t e = launch_append_q4(a, in_dtype, q ? q_out_dtype : KVA_F32, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "4-bit append launch");
+}
+
+kva_status kv_cache_expand_q4(
+    kva_cache_q4 cache, const int32_t* slot, int64_t slot_inst_stride, const int32_t* slot_host,
+    int32_t N, int32_t T, kva_cache dst, int32_t dst_first, kva_stream stream) {
+  if (N < 0 || T < 0) return fail(KVA_EINVAL, "N=%d T=%d must be >= 0", N, T);
+  if (N == 0 || T == 0) return KVA_OK;
+  kva_status st = check_cache_q4(cache, N);
+  if (st != KVA_OK) return st;
+  if ((st = check_cache(dst, N)) != KVA_OK) return st;
+  if (dst.n_kv_heads != cache.n_kv_heads || dst.head_dim != cache.head_dim || dst.head_dim_v != cache.head_dim_v)
+    return fail(KVA_EINVAL, "expand: destination heads %d x %d/%d differ from the source's %d x %d/%d", dst.n_kv_heads,
+                dst.head_dim, dst.head_dim_v, cache.n_kv_heads, cache.head_dim, cache.head_dim_v);
+  if (!slot || !slot_host) return fail(KVA_EINVAL, "NULL slot");
+  if (slot_inst_stride < 0) return fail(KVA_EINVAL, "negative instance stride");
+  if (dst_first < 0 || (int64_t)dst_first + T > dst.capacity)
+    return fail(KVA_ECAPACITY, "expand: slots [%d, %d + %d) outside the destination's %d", dst_first, dst_first, T,
+                dst.capacity);
+  if (N > 65535) return fail(KVA_EUNSUPPORTED, "expand: N=%d > 65535", N);
+  for (int n = 0; n < N; ++n) {
+    if (n > 0 && slot_inst_stride == 0) break;
+    if ((st = check_slots(slot_host + (int64_t)n * slot_inst_stride, n, T, cache.capacity, false)) != KVA_OK) return st;
+  }
+  ExpandQ4Args a{};
+  a.c = q4_args(cache);
+  a.slot = slot; a.slot_stride = slot_inst_stride;
+  a.dk = dst.k; a.dv = dst.v; a.d_stride = dst.inst_stride; a.d_stride_v = dst.inst_stride_v;
+  a.N = N; a.T = T; a.d_capacity = dst.capacity; a.d_first = dst_first;
+  const cudaError_t e = launch_expand_q4(a, dst.dtype, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "4-bit expand launch");
+}
+
+// Work units of kv_attn_decode_q4 per instance: (KV head, tile of query rows).
+static int64_t decode_q4_units(int Hkv, int Hq, int T, int* tile, int64_t* row_tiles) {
+  const int64_t rows = (int64_t)(Hq / Hkv) * T;
+  *tile = decode_q4_row_tile((int)std::min<int64_t>(rows, 1 << 20));
+  *row_tiles = (rows + *tile - 1) / *tile;
+  return (int64_t)Hkv * *row_tiles;
+}
+// Most chunks an instance is cut into: enough CTAs to fill the GPU some times over, and at least
+// 8, so that one long sequence among many short ones is still spread.
+static int decode_q4_max_chunks(int64_t instances_units, int max_len) {
+  const int64_t cap = std::min<int64_t>(DECODE_MAX_CHUNKS, std::max<int64_t>(8, 8192 / std::max<int64_t>(1, instances_units)));
+  return (int)std::min<int64_t>(cap, decode_max_chunks_bound(max_len));
+}
+static size_t decode_q4_zero_bytes(int64_t counters) { return round_up(sizeof(unsigned) * (size_t)counters, 256); }
+
+size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T) {
+  if (B <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || T <= 0 || n_q_heads % n_kv_heads != 0) return 0;
+  int tile;
+  int64_t rt;
+  return decode_q4_zero_bytes((int64_t)B * decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt));
+}
+
+size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T, int32_t max_len,
+                                    int32_t head_dim_v) {
+  if (B <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || T <= 0 || max_len <= 0 || head_dim_v <= 0 ||
+      n_q_heads % n_kv_heads != 0)
+    return 0;
+  int tile;
+  int64_t rt;
+  const int64_t units = (int64_t)B * decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt);
+  const size_t rows = (size_t)units * tile * decode_q4_max_chunks(units, max_len);
+  return decode_q4_zero_bytes(units) + round_up(sizeof(float) * rows * 2, 256) + sizeof(float) * rows * head_dim_v;
+}
+
+kva_status kv_attn_decode_q4(
+    const void* q, kva_dtype q_dtype, kva_cache_q4 cache,
+    const int32_t* lengths, const int32_t* lengths_host, int32_t B, int32_t T, int32_t n_q_heads,
+    float scale, float* out, void* workspace, size_t workspace_bytes, kva_stream stream) {
+  if (B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", B);
+  if (B == 0) return KVA_OK;
+  if (T < 1 || T > KVA_DECODE_Q4_MAX_BLOCK) return fail(KVA_EINVAL, "block T=%d outside [1, %d]", T, KVA_DECODE_Q4_MAX_BLOCK);
+  if (!valid_dtype(q_dtype)) return fail(KVA_EINVAL, "unknown q dtype");
+  kva_status st = check_cache_q4(cache, B);
+  if (st != KVA_OK) return st;
+  const int Dk = cache.head_dim, Dv = cache.head_dim_v, Hkv = cache.n_kv_heads;
+  if (n_q_heads <= 0 || n_q_heads % Hkv != 0)
+    return fail(KVA_EINVAL, "n_q_heads %d must be a positive multiple of n_kv_heads %d", n_q_heads, Hkv);
+  if (!decode_q4_supports(Dk, Dv))
+    return fail(KVA_EUNSUPPORTED, "4-bit decode: head dims %d/%d (built: 64/64, 128/128, 192/128)", Dk, Dv);
+  if (!q || !out || !lengths || !lengths_host) return fail(KVA_EINVAL, "NULL q/out/lengths");
+  if (!aligned16(q) || !aligned16(out)) return fail(KVA_EALIGN, "q/out must be 16-byte aligned");
+  int tile;
+  int64_t rt;
+  const int64_t units = decode_q4_units(Hkv, n_q_heads, T, &tile, &rt);
+  if (B > 65535 || units > 65535) return fail(KVA_EUNSUPPORTED, "4-bit decode: B or Hkv * row tiles > 65535");
+  if (!workspace) return fail(KVA_EWORKSPACE, "4-bit decode: workspace is NULL");
+  if (!aligned16(workspace)) return fail(KVA_EALIGN, "workspace must be 16-byte aligned");
+  int max_len = 0;
+  for (int b = 0; b < B; ++b) {
+    const int L = lengths_host[b];
+    if (L < 0 || L > cache.capacity)
+      return fail(KVA_ECAPACITY, "length %d of instance %d outside [0, %d]", L, b, cache.capacity);
+    max_len = std::max(max_len, L);
+  }
+  max_len = std::max(max_len, 1);
+  const int max_chunks = decode_q4_max_chunks((int64_t)B * units, max_len);
+  const int chunk = decode_q4_plan_chunk(lengths_host, B, (int)units, max_len, max_chunks);
+  const int chunks = (max_len + chunk - 1) / chunk;
+  const size_t rows = (size_t)B * units * tile * chunks;
+  const size_t zero = decode_q4_zero_bytes(B * units), ml = round_up(sizeof(float) * rows * 2, 256);
+  const size_t need = zero + ml + sizeof(float) * rows * Dv;
+  if (workspace_bytes < need)
+    return fail(KVA_EWORKSPACE, "4-bit decode workspace %zu bytes < %zu needed", workspace_bytes, need);
+  DecodeQ4Args a{};
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.counters = reinterpret_cast<unsigned*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + zero);
+  a.part_acc = reinterpret_cast<float*>(ws + zero + ml);
+  a.q = q; a.c = q4_args(cache); a.lengths = lengths; a.out = out;
+  a.B = B; a.T = T; a.Hq = n_q_heads; a.RT = (int)rt; a.chunk = chunk; a.max_chunks = chunks;
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)Dk);
+  a.scale_log2 = sc * 1.4426950408889634f;
+  const cudaError_t e = launch_decode_q4(a, q_dtype, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "4-bit decode launch");
 }
 
 }  // extern "C"

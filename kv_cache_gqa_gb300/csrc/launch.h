@@ -216,6 +216,89 @@ struct PrefillArgs {
 int lmhead_max_hidden();
 cudaError_t launch_prefill(const PrefillArgs& a, kva_dtype dtype, cudaStream_t s);
 
+// ---------------------------------------------------------------------------------
+// The 4-bit cache (layout: kva_cache_q4 in kv_attn.h).
+constexpr int Q4_GROUP = 64;          // values sharing a scale and a midpoint
+struct Q4Cache {
+  uint32_t* k;                        // [rows, Dk/8] words of 8 codes
+  uint32_t* v;
+  uint32_t* ks;                       // [rows, Dk/64] bf16 pairs (scale low, mid high)
+  uint32_t* vs;
+  int Hkv, capacity, Dk, Dv;
+  int64_t inst_rows;
+};
+struct AppendQ4Args {
+  const void* q;                      // null: no queries
+  const void* k;
+  const void* v;
+  void* q_out;
+  const int32_t* pos;
+  int64_t pos_stride;
+  const int32_t* slot;
+  int64_t slot_stride;
+  const float* q_w;
+  const float* k_w;
+  int64_t w_stride;
+  float eps;
+  int after_rope;
+  int N, T, Hq;
+  int rot_offset, rot_dim;
+  Q4Cache c;
+  RopeTable rope;
+};
+cudaError_t launch_append_q4(const AppendQ4Args& a, kva_dtype in_dtype, kva_dtype q_out_dtype, cudaStream_t s);
+struct ExpandQ4Args {
+  Q4Cache c;
+  const int32_t* slot;
+  int64_t slot_stride;
+  void* dk;                           // destination caches of the same heads and head dims
+  void* dv;
+  int64_t d_stride, d_stride_v;       // elements between destination instances
+  int N, T, d_capacity, d_first;
+};
+cudaError_t launch_expand_q4(const ExpandQ4Args& a, kva_dtype dst_dtype, cudaStream_t s);
+struct DecodeQ4Args {
+  const void* q;                      // [B, T, Hq, Dk]
+  Q4Cache c;
+  const int32_t* lengths;             // [B]
+  float* out;                         // [B, T, Hq, Dv]
+  unsigned int* counters;             // [B, Hkv, RT] zero on entry, zero on exit
+  float* part_acc;                    // [B, Hkv, RT, rows, max_chunks, Dv]
+  float* part_ml;                     // [B, Hkv, RT, rows, max_chunks, 2]
+  int B, T, Hq, RT, chunk, max_chunks;
+  float scale_log2;
+};
+bool decode_q4_supports(int Dk, int Dv);
+int decode_q4_row_tile(int rows);     // query rows (G * T) per CTA
+// Keys per CTA: the longest instance is cut into at most max_chunks chunks.
+int decode_q4_plan_chunk(const int32_t* lengths_host, int B, int units, int max_len, int max_chunks);
+cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------
+struct LogprobArgs {
+  const void* h;                      // [B, H]
+  int h_dtype;                        // kva_dtype
+  const float* norm_w;
+  float eps;
+  const void* W;                      // [V_rows, H]
+  int B, H, V;
+  const int32_t* targets;
+  float* out_logprob;
+  float* out_entropy;
+  float* out_lse;
+  int top_k;
+  int32_t* top_ids;
+  float* top_logprobs;
+  float* hn;                          // [B, H] normalised rows (norm_w given)
+  uint16_t* hb;                       // bf16 halves of the rows (tensor-core form)
+  float* part_stat;                   // [B, splits, 4]: max, sum, weighted sum
+  unsigned long long* part_key;       // [B, splits, TK]
+  int splits;
+};
+constexpr int LOGPROB_TOP_MAX = KVA_LOGPROBS_MAX_TOP;
+size_t logprob_workspace_bytes(int B, int H, int V, int top_k);
+cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, cudaStream_t s, unsigned* n_launches);
+
 // Launch `kern` with programmatic stream serialization: its set-up overlaps the tail of the
 // kernel before it on the stream.  The kernel must call griddep_wait() before its first global
 // memory access.  A kernel that allocates tensor memory must do so before it calls
