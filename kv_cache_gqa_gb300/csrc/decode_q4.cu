@@ -1,5 +1,37 @@
-// Attention of new tokens over a 4-bit cache (kv_attn_decode_q4): one warp per query row.  A lane
-// scores one key of a 32-key tile, then the lanes turn to the value dims.
+// Attention of new tokens over a 4-bit cache (kv_attn_decode_q4): split-KV, the codes fed to the
+// tensor cores as they are.
+//
+// Work unit = (chunk c, KV head g and tile of query rows, instance b).  The query rows of a group
+// are (token i, head j) -> i * G + j, 4, 8 or 16 a CTA.  A CTA's 4 warps are independent: warp w takes
+// the 32-key stages w, w+4, ... of the chunk through a private ring, filled by 1-D bulk copies (a
+// head's codes and scales are contiguous in the cache).  Per 16 keys:
+//   S^T = K q^T   keys are the 16 rows of the MMA, query rows its 8 columns.  A 4-bit code u taken
+//                 out of a word by one AND is the float16 subnormal u 2^-24 (or u 2^-20 for the odd
+//                 nibble; V shifts every code there), so K needs 5 instructions per 8 codes; q is scaled by a power of two per
+//                 row so that its float16 (two halves for float32 q) loses nothing.  Scale and
+//                 midpoint of a group enter in float32 after the product:
+//                   s = sum_g scale_g (u . q)_g + (mid_g - 8 scale_g) sum(q)_g.
+//   softmax       online, against a reference maximum that moves only when a score exceeds it by
+//                 more than 2^8, float32
+//   O^T += V^T P  value dims are the MMA's rows, keys its K axis.  The weights p * scale_g, two
+//                 float16 halves (22 bits) against a power of two that follows the largest scale,
+//                 turn from S^T's layout to the operand layout with movmatrix.  The codes' centre
+//                 (u - 8) is taken off by a second product with a constant -8, or in the operand:
+//                 without it O would be the small difference of sums of positive codes.
+//                 mid enters as sum p mid_g in float32.
+// With at most 4 query rows the two halves of the weights (and of q) share the 8 columns.  The
+// contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
+// a lane's codes of K, and of V, are adjacent bytes.
+//
+// Bound: HBM, 144 bytes per key and KV head at D = 128; issue slots come second (about 250 warp
+// instructions per 16 keys, 65% of the slots at full bandwidth), then mma.sync (24 per 16 keys; a
+// measured 1.05 ns each per SM, half of the time).
+//
+// Method: attention over the valid prefix of the cache (Youtu-VL-4B ncnn port, step 8), GQA grouping
+// (Penguin-VL ncnn port, section 3), softmax as max/subtract/exp/sum/divide (Youtu-VL-4B ncnn port,
+// implementation difficulty 3); the 4-bit cache has no counterpart on the pages.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -9,66 +41,550 @@ namespace kva {
 
 namespace {
 
-__device__ __forceinline__ float code_value(uint32_t w, int i, uint32_t par) {
-  return fmaf(bf16_lo(par), (float)((int)((w >> (4 * i)) & 15u) - 8), bf16_hi(par));
-}
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int SK = 32;                          // keys per stage
+constexpr int NS = 3;                           // ring stages per warp
+constexpr float RESCALE_LOG2 = 8.0f;            // a row's reference max lags its true max by <= 2^8
+constexpr float M_NONE = -3.0e38f;              // reference max of a row that has seen no key
 
-template <typename QT, int DK, int DV>
-__global__ void __launch_bounds__(32)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held as one register a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// (lo, hi) - its float16 rounding h, as float16
+__device__ __forceinline__ uint32_t residual_f16x2(float lo, float hi, uint32_t h) {
+  const float2 f = unpack_f16x2(h);
+  return pack_f16x2(lo - f.x, hi - f.y);
+}
+__device__ __forceinline__ float pow2(int biased) { return __uint_as_float((uint32_t)biased << 23); }
+__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u); }
+
+template <int DK, int DV, int MODE>
+struct Shape {
+  static constexpr int GK = DK / Q4_GROUP, GV = DV / Q4_GROUP;
+  static constexpr int NB = MODE == 2 ? 2 : 1;              // 8-column blocks of query rows
+  static constexpr int ROWS = MODE == 0 ? 4 : 8 * NB;
+  static constexpr int KC = SK * DK / 2, VC = SK * DV / 2, KP = SK * GK * 4, VP = SK * GV * 4;
+  static constexpr int STAGE = KC + VC + KP + VP;
+  static constexpr int RING = NS * STAGE;
+  static constexpr int MERGE = WARPS * ROWS * (DV + 2) * 4;
+  static constexpr int SMEM = (WARPS * RING > MERGE ? WARPS * RING : MERGE) + WARPS * NS * 8;
+  static constexpr int CTAS = MODE == 2 ? 3 : 4;            // resident per SM
+};
+
+// MODE 0: up to 4 rows, halves side by side in the 8 columns; 1: 8 rows; 2: 16 rows.
+// SPLITQ: float32 queries (two halves); else bf16 (exact in one).
+template <int DK, int DV, int MODE, bool SPLITQ>
+__global__ void __launch_bounds__(THREADS, (Shape<DK, DV, MODE>::CTAS))
 decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
-  constexpr int GK = DK / Q4_GROUP, GV = DV / Q4_GROUP, WK = DK / 8, WV = DV / 8, PER = DV / 32;
-  __shared__ float s_q[DK];
-  const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z, lane = threadIdx.x;
-  const int g = h / (a.Hq / a.c.Hkv);
-  griddep_wait();
-  const int64_t qrow = ((int64_t)b * a.T + t) * a.Hq + h;
-  for (int i = lane; i < DK; i += 32) s_q[i] = load1(reinterpret_cast<const QT*>(a.q) + qrow * DK + i) * a.scale_log2;
+  using S = Shape<DK, DV, MODE>;
+  constexpr int GK = S::GK, GV = S::GV, NB = S::NB, ROWS = S::ROWS;
+  constexpr int QP = MODE != 0 && SPLITQ ? 2 : 1;           // products per K fragment and block
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float s_M[ROWS], s_L[ROWS];
+  __shared__ int s_last;
+  const int c = blockIdx.x, g = blockIdx.y / a.RT, rt = blockIdx.y % a.RT, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
+  const int G = a.Hq / a.c.Hkv, n_rows = G * a.T;
+  unsigned char* ring = smem + warp * S::RING;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::SMEM - WARPS * NS * 8) + warp * NS;
+  if (lane == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(&bar[s], 1);
+    fence_mbar_init();
+  }
   __syncwarp();
-  const int L = min(max(a.lengths[b], 0), a.c.capacity) - a.T + t + 1;      // visible slots
+  griddep_wait();                               // inputs of this launch are complete from here on
+  griddep_launch_dependents();
+
+  // ---- the chunk: keys [k0, k1) of the slots that the tile's last token sees ----
+  const int L = min(max(a.lengths[b], 0), a.c.capacity);
+  const int row_end = min(n_rows, (rt + 1) * ROWS);
+  const int end = max(0, L - a.T + (row_end - 1) / G + 1);
+  const int stages = (end + SK - 1) / SK;
+  const int n_chunks = min(a.max_chunks, (end + a.chunk - 1) / a.chunk);
+  auto out_row = [&](int row) {                 // row of the tile -> its output
+    const int rr = rt * ROWS + row;
+    return a.out + (((int64_t)b * a.T + rr / G) * a.Hq + g * G + rr % G) * DV;
+  };
+  if (c >= max(n_chunks, 1)) return;
+  if (n_chunks == 0) {                          // nothing visible: zeros
+    for (int i = tid; i < (row_end - rt * ROWS) * DV; i += THREADS) out_row(i / DV)[i % DV] = 0.f;
+    return;
+  }
+  const int st0 = (int)((int64_t)stages * c / n_chunks), st1 = (int)((int64_t)stages * (c + 1) / n_chunks);
+  const int k1 = min(end, st1 * SK);
+  const int n_mine = st1 - st0 > warp ? (st1 - st0 - 1 - warp) / WARPS + 1 : 0;
   const int64_t row0 = (int64_t)b * a.c.inst_rows + (int64_t)g * a.c.capacity;
-  float m = -INFINITY, l = 0.f, o[PER];
+  auto issue = [&](int u) {                     // lane 0: stage u of this warp
+    const int ks = (st0 + warp + u * WARPS) * SK;
+    const int n = min(SK, (k1 - ks + 3) & ~3);  // whole 16-byte pieces of the scales; capacity is a multiple of 4
+    unsigned char* dst = ring + (u % NS) * S::STAGE;
+    uint64_t* bb = &bar[u % NS];
+    const int64_t row = row0 + ks;
+    mbar_arrive_expect_tx(bb, (uint32_t)n * (DK / 2 + DV / 2 + GK * 4 + GV * 4));
+    bulk_g2s(dst, a.c.k + row * (DK / 8), (uint32_t)n * (DK / 2), bb);
+    bulk_g2s(dst + S::KC + S::VC, a.c.ks + row * GK, (uint32_t)n * (GK * 4), bb);
+    bulk_g2s(dst + S::KC, a.c.v + row * (DV / 8), (uint32_t)n * (DV / 2), bb);
+    bulk_g2s(dst + S::KC + S::VC + S::KP, a.c.vs + row * GV, (uint32_t)n * (GV * 4), bb);
+  };
+  if (lane == 0)
+    for (int u = 0; u < NS && u < n_mine; ++u) issue(u);
+  __syncwarp();
+
+  // ---- query fragments: column r of block nb, dims 64 gk + 16 t + 0..15 ----
+  // word j (8 dims) of group gk gives two MMAs h = 0, 1 with b0 = dims (2h, 2h + 4), b1 = (2h + 1, 2h + 5)
+  uint32_t qf[NB][QP][GK][2][2][2];
+  float qs[NB][GK][2], qf_scale[NB][2];         // of the S^T columns 2t, 2t + 1
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  for (int k0 = 0; k0 < L; k0 += 32) {
-    float x = -INFINITY;
-    if (k0 + lane < L) {
-      x = 0.f;
-      const int64_t row = row0 + k0 + lane;
-      for (int w = 0; w < WK; ++w) {
-        const uint32_t code = a.c.k[row * WK + w], par = a.c.ks[row * GK + w % GK];
-        for (int i = 0; i < 8; ++i) x = fmaf(s_q[64 * (w % GK) + 8 * (w / GK) + i], code_value(code, i, par), x);
+  for (int nb = 0; nb < NB; ++nb) {
+    const int col = MODE == 0 ? (r & 3) : 8 * nb + r;
+    const int rr = rt * ROWS + col;
+    const bool on = rr < n_rows;
+    const int64_t qrow = (((int64_t)b * a.T + (on ? rr / G : 0)) * a.Hq + g * G + (on ? rr % G : 0)) * DK;
+    float x[GK][16], big = 0.f, sum[GK];
+#pragma unroll
+    for (int gk = 0; gk < GK; ++gk) {
+      const int64_t o = qrow + 64 * gk + 16 * t;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float y[8];
+        if constexpr (SPLITQ) load8(reinterpret_cast<const float*>(a.q) + o + 8 * j, y);
+        else load8(reinterpret_cast<const bf16_t*>(a.q) + o + 8 * j, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[gk][8 * j + i] = on ? y[i] : 0.f;
       }
+      sum[gk] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) { big = fmaxf(big, fabsf(x[gk][i])); sum[gk] += x[gk][i]; }
+      sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 1);
+      sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 2);
     }
-    float mt = x;
+    big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 2));
+    // the row's largest element becomes 2^13 .. 2^14
+    const int e = min(max(exponent(big), 20), 240);
+    const float up = pow2(267 - e), down = pow2(e + 11) * a.scale_log2;   // 2^(13-(e-127)); 2^24 / up
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, s));
-    mt = fmaxf(mt, m);
-    const float p = exp2f(x - mt), alpha = exp2f(m - mt);
-    m = mt;
-    l = l * alpha + p;
+    for (int gk = 0; gk < GK; ++gk)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= alpha;
-    for (int j = 0; j < 32 && k0 + j < L; ++j) {
-      const float pj = __shfl_sync(FULL_MASK, p, j);
-      const int64_t row = row0 + k0 + j;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int d = lane + 32 * i, gr = d / 64, w = (d % 64 / 8) * GV + gr;
-        o[i] = fmaf(pj, code_value(a.c.v[row * WV + w], d & 7, a.c.vs[row * GV + gr]), o[i]);
-      }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {         // the odd nibble counts 16 times the even one
+            const int d = 8 * j + 2 * h + o;
+            const float f = o ? up * 0.0625f : up;
+            const float y0 = x[gk][d] * f, y1 = x[gk][d + 4] * f;
+            const uint32_t hi = pack_f16x2(y0, y1);
+            if constexpr (MODE == 0) {
+              qf[nb][0][gk][j][h][o] = SPLITQ && r >= 4 ? residual_f16x2(y0, y1, hi) : hi;
+            } else {
+              qf[nb][0][gk][j][h][o] = hi;
+              if constexpr (SPLITQ) qf[nb][1][gk][j][h][o] = residual_f16x2(y0, y1, hi);
+            }
+          }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int src = 4 * (2 * t + i);          // any lane of column 2t + i
+      qf_scale[nb][i] = __shfl_sync(FULL_MASK, down, src);
+#pragma unroll
+      for (int gk = 0; gk < GK; ++gk)           // in units of the product (2^-24 up)
+        qs[nb][gk][i] = __shfl_sync(FULL_MASK, sum[gk] * (up * 5.9604644775390625e-8f), src);
     }
   }
+
+  int lim[NB][2];                               // slots that the columns' tokens see
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(FULL_MASK, l, s);
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-  for (int i = 0; i < PER; ++i) a.out[qrow * DV + lane + 32 * i] = L > 0 ? o[i] / l : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int col = MODE == 0 ? ((2 * t + i) & 3) : 8 * nb + 2 * t + i;
+      lim[nb][i] = min(L - a.T + min(rt * ROWS + col, n_rows - 1) / G + 1, k1);
+    }
+  const int lim_all = min(L - a.T + (rt * ROWS) / G + 1, k1);   // slots that every column sees
+
+  float o[NB][GV][4][4];                        // value dims 64 gv + 8 r + i (and + 4), columns 2t, 2t + 1
+  float om[NB][GV][2], m[NB][2], l[NB][2], vtop[GV], vmul[GV];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int gv = 0; gv < GV; ++gv) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[nb][gv][i][0] = o[nb][gv][i][1] = o[nb][gv][i][2] = o[nb][gv][i][3] = 0.f;
+      om[nb][gv][0] = om[nb][gv][1] = 0.f;
+    }
+    m[nb][0] = m[nb][1] = M_NONE;
+    l[nb][0] = l[nb][1] = 0.f;
+  }
+#pragma unroll
+  for (int gv = 0; gv < GV; ++gv) { vtop[gv] = 0.f; vmul[gv] = 0.f; }
+  bool ok = true;
+  int done = 0;                                 // stages consumed
+
+  // key order inside a 16-key tile: MMA row (and K index) j holds key sigma(j); adjacent rows and
+  // every second row alternate between even and odd keys, which spreads the 64-byte rows over the
+  // shared-memory banks
+  const int kr = r ^ ((r >> 1) & 1);            // sigma(r); rows r + 8: + 8
+  const int kv0 = (2 * t) ^ (t & 1), kv1 = (2 * t + 1) ^ (t & 1);
+
+  for (int u = 0; u < n_mine; done = ++u) {
+    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[u % NS], (uint32_t)((u / NS) & 1)))) { ok = false; break; }
+    const unsigned char* stg = ring + (u % NS) * S::STAGE;
+    const int ks = (st0 + warp + u * WARPS) * SK;
+#pragma unroll 1
+    for (int tt = 0; tt < SK / 16; ++tt) {
+      const int kb = ks + 16 * tt;
+      if (kb >= k1) break;                      // warp-uniform
+      // ---- S^T ----
+      float d[NB][GK][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk) d[nb][gk][0] = d[nb][gk][1] = d[nb][gk][2] = d[nb][gk][3] = 0.f;
+      const unsigned char* pk = stg + (16 * tt + kr) * (DK / 2) + t * (DK / 8);
+      uint32_t wk[2][2 * GK];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        if constexpr (GK == 2) {
+          const uint4 q4 = *reinterpret_cast<const uint4*>(pk + hh * 8 * (DK / 2));
+          wk[hh][0] = q4.x; wk[hh][1] = q4.y; wk[hh][2] = q4.z; wk[hh][3] = q4.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < GK; ++i) {
+            const uint2 q2 = *reinterpret_cast<const uint2*>(pk + hh * 8 * (DK / 2) + 8 * i);
+            wk[hh][2 * i] = q2.x; wk[hh][2 * i + 1] = q2.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int gk = 0; gk < GK; ++gk) {
+          uint32_t x = wk[0][j * GK + gk], y = wk[1][j * GK + gk];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = x & 0x000f000fu, a1 = y & 0x000f000fu, a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int p = 0; p < QP; ++p) mma16816(d[nb][gk], a0, a1, a2, a3, qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
+            x >>= 8; y >>= 8;
+          }
+        }
+      // ---- scale and midpoint of keys kr (i = 0, 1) and kr + 8 (i = 2, 3); columns 2t, 2t + 1 ----
+      float s[NB][4];
+      {
+        float sp[NB][4], sc[NB][4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t* pp = reinterpret_cast<const uint32_t*>(stg + S::KC + S::VC) + (16 * tt + kr + 8 * hh) * GK;
+#pragma unroll
+          for (int gk = 0; gk < GK; ++gk) {
+            const uint32_t w = pp[gk];
+            const float scale = bf16_lo(w), off = fmaf(-8.f, scale, bf16_hi(w));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int e = 2 * hh + i;
+                sp[nb][e] = gk == 0 ? scale * d[nb][gk][e] : fmaf(scale, d[nb][gk][e], sp[nb][e]);
+                sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
+              }
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
+            s[nb][e] = (sp[nb][e] + sc[nb][e]) * qf_scale[nb][e & 1];
+          }
+      }
+      const bool tail = kb + 16 > lim_all;
+      if (tail) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (kb + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[nb][e] = -INFINITY;
+      }
+      // ---- online softmax ----
+      bool grow = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) grow |= fmaxf(s[nb][i], s[nb][2 + i]) > m[nb][i] + RESCALE_LOG2;
+      if (__any_sync(FULL_MASK, grow)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mt = fmaxf(s[nb][i], s[nb][2 + i]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
+            if (mt > m[nb][i] + RESCALE_LOG2) {           // uniform over the column's lanes
+              const float alpha = ex2(m[nb][i] - mt);
+              m[nb][i] = mt;
+              l[nb][i] *= alpha;
+#pragma unroll
+              for (int gv = 0; gv < GV; ++gv) {
+                om[nb][gv][i] *= alpha;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) { o[nb][gv][k][i] *= alpha; o[nb][gv][k][2 + i] *= alpha; }
+              }
+            }
+          }
+      }
+      float p[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[nb][e] = ex2(s[nb][e] - m[nb][e & 1]);
+          l[nb][e & 1] += p[nb][e];
+        }
+      // ---- weights p * scale of V, per group ----
+      float vs[GV][2], vm[GV][2];
+      bool wide = false;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint32_t* pp = reinterpret_cast<const uint32_t*>(stg + S::KC + S::VC + S::KP) + (16 * tt + kr + 8 * hh) * GV;
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv) {
+          uint32_t w = pp[gv];
+          if (tail && kb + kr + 8 * hh >= k1) w = 0u;     // slots past the chunk may hold anything
+          vs[gv][hh] = bf16_lo(w); vm[gv][hh] = bf16_hi(w);
+          wide |= vs[gv][hh] > vtop[gv];
+        }
+      }
+      if (__any_sync(FULL_MASK, wide)) {                  // a larger scale than any before: follow it
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv) {
+          float top = fmaxf(vs[gv][0], vs[gv][1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
+          if (top > vtop[gv]) {
+            const int e = max(exponent(top) + 1, 40);     // top < 2^(e-127) (or tiny)
+            vtop[gv] = pow2(min(e, 254));
+            const float now = pow2(127 - (e - 127) + 6);  // weights reach 2^8 * 2^6
+            const float ratio = vmul[gv] == 0.f ? 0.f : now / vmul[gv];
+            vmul[gv] = now;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[nb][gv][k][x] *= ratio;
+          }
+        }
+      }
+      uint32_t bh[NB][GV][2], bl[NB][GV][2];              // operand fragments: keys 2t, 2t + 1 (and + 8), column r
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float mul = vs[gv][hh] * vmul[gv];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float w0 = p[nb][2 * hh] * mul, w1 = p[nb][2 * hh + 1] * mul;
+            float z0 = p[nb][2 * hh] * vm[gv][hh], z1 = p[nb][2 * hh + 1] * vm[gv][hh];
+            if (tail) {                                   // a hidden key's values may be NaN: no 0 * NaN
+              if (s[nb][2 * hh] == -INFINITY) w0 = z0 = 0.f;
+              if (s[nb][2 * hh + 1] == -INFINITY) w1 = z1 = 0.f;
+            }
+            om[nb][gv][0] += z0;
+            om[nb][gv][1] += z1;
+            const uint32_t hi = pack_f16x2(w0, w1), lo = residual_f16x2(w0, w1, hi);
+            if constexpr (MODE == 0) {
+              bh[nb][gv][hh] = transpose8x8(t >= 2 ? lo : hi);
+            } else {
+              bh[nb][gv][hh] = transpose8x8(hi);
+              bl[nb][gv][hh] = transpose8x8(lo);
+            }
+          }
+        }
+      // ---- O^T += V^T P ----
+      const unsigned char* pv = stg + S::KC + 16 * tt * (DV / 2) + r * (GV * 4);
+      uint32_t wv[4][GV];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned char* q = pv + ((k & 1 ? kv1 : kv0) + (k & 2 ? 8 : 0)) * (DV / 2);
+        if constexpr (GV == 2) {
+          const uint2 q2 = *reinterpret_cast<const uint2*>(q);
+          wv[k][0] = q2.x; wv[k][1] = q2.y;
+        } else {
+          wv[k][0] = *reinterpret_cast<const uint32_t*>(q);
+        }
+      }
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv) {
+        const uint32_t x0 = __byte_perm(wv[0][gv], wv[1][gv], 0x5410), y0 = __byte_perm(wv[0][gv], wv[1][gv], 0x7632);
+        const uint32_t x1 = __byte_perm(wv[2][gv], wv[3][gv], 0x5410), y1 = __byte_perm(wv[2][gv], wv[3][gv], 0x7632);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
+          // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
+          auto code = [&](uint32_t v) { return (i == 0 ? v << 4 : v >> (4 * (i > 0 ? i - 1 : 0))) & 0x00f000f0u; };
+          constexpr uint32_t eight = 0x80808080u;                     // -8 2^-20, twice
+          uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
+          if constexpr (MODE == 0) {
+            mma16816(o[0][gv][i], a0, a1, a2, a3, bh[0][gv][0], bh[0][gv][1]);
+            mma16816(o[0][gv][i], eight, eight, eight, eight, bh[0][gv][0], bh[0][gv][1]);
+          } else {
+            const __half2 e2 = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));
+            auto centre = [&](uint32_t v) {
+              const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), e2);
+              return *reinterpret_cast<const uint32_t*>(&z);
+            };
+            a0 = centre(a0); a1 = centre(a1); a2 = centre(a2); a3 = centre(a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
+              mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();                               // all lanes are done with this stage
+    if (lane == 0 && u + NS < n_mine) issue(u + NS);
+  }
+  if (!ok)                                      // gave up: the copies still in flight land first (bounded)
+    for (int u = done; u < n_mine && u < done + NS; ++u) (void)mbar_wait_bounded(&bar[u % NS], (uint32_t)((u / NS) & 1));
+
+  // ---- merge the warps ----
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[nb][i] += __shfl_xor_sync(FULL_MASK, l[nb][i], x);
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv) om[nb][gv][i] += __shfl_xor_sync(FULL_MASK, om[nb][gv][i], x);
+      }
+  __syncthreads();                              // rings drained: reuse them
+  float* sm_m = reinterpret_cast<float*>(smem);                 // [WARPS][ROWS]
+  float* sm_l = sm_m + WARPS * ROWS;
+  float* sm_o = sm_l + WARPS * ROWS;                            // [WARPS][ROWS][DV]
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 8 * nb + 2 * t + i;       // MODE 0: rows 0..3 in lanes t < 2
+      if (r == 0 && row < ROWS) {
+        sm_m[warp * ROWS + row] = ok ? m[nb][i] : NAN;
+        sm_l[warp * ROWS + row] = ok ? l[nb][i] : NAN;
+      }
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv) {
+        const float inv = vmul[gv] == 0.f ? 0.f : 1.0f / vmul[gv];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          constexpr float unit = 1048576.f;                     // 1 / the code's subnormal step
+          float lo = o[nb][gv][k][i], hi = o[nb][gv][k][2 + i];
+          if constexpr (MODE == 0) {
+            lo += __shfl_xor_sync(FULL_MASK, lo, 2);
+            hi += __shfl_xor_sync(FULL_MASK, hi, 2);
+          }
+          if (row < ROWS) {
+            float* dst = sm_o + (warp * ROWS + row) * DV + 64 * gv + 8 * r + k;
+            dst[0] = fmaf(lo * unit, inv, om[nb][gv][i]);
+            dst[4] = fmaf(hi * unit, inv, om[nb][gv][i]);
+          }
+        }
+      }
+    }
+  __syncthreads();
+  if (tid < ROWS) {
+    float M = M_NONE, Ls = 0.f;
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
+    for (int w = 0; w < WARPS; ++w) Ls += ex2(sm_m[w * ROWS + tid] - M) * sm_l[w * ROWS + tid];
+    s_M[tid] = M; s_L[tid] = Ls;
+  }
+  __syncthreads();
+  const bool single = n_chunks == 1;
+  const int rows_here = row_end - rt * ROWS;
+  const int64_t unit0 = ((int64_t)b * gridDim.y + blockIdx.y) * ROWS;
+  for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
+    const int row = idx / DV, dd = idx % DV;
+    float tot = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) tot += ex2(sm_m[w * ROWS + row] - s_M[row]) * sm_o[(w * ROWS + row) * DV + dd];
+    if (single) {
+      out_row(row)[dd] = s_L[row] == 0.f ? 0.f : tot / s_L[row];
+    } else {
+      const int64_t pi = (unit0 + row) * a.max_chunks + c;
+      a.part_acc[pi * DV + dd] = tot;
+      if (dd == 0) { a.part_ml[2 * pi] = s_M[row]; a.part_ml[2 * pi + 1] = s_L[row]; }
+    }
+  }
+  if (single) return;
+
+  __threadfence();
+  __syncthreads();
+  unsigned* counter = a.counters + (int64_t)b * gridDim.y + blockIdx.y;
+  if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(n_chunks - 1);
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
+    const int row = idx / DV, dd = idx % DV;
+    const int64_t p0 = (unit0 + row) * a.max_chunks;
+    float M = M_NONE;
+    for (int cc = 0; cc < n_chunks; ++cc) M = fmaxf(M, __ldcg(&a.part_ml[2 * (p0 + cc)]));
+    float num = 0.f, den = 0.f;
+    for (int cc = 0; cc < n_chunks; ++cc) {
+      const float w = ex2(__ldcg(&a.part_ml[2 * (p0 + cc)]) - M);
+      num = fmaf(w, __ldcg(&a.part_acc[(p0 + cc) * DV + dd]), num);
+      den = fmaf(w, __ldcg(&a.part_ml[2 * (p0 + cc) + 1]), den);
+    }
+    out_row(row)[dd] = den == 0.f ? 0.f : num / den;
+  }
+  if (tid == 0) *counter = 0u;
+}
+
+template <int DK, int DV, int MODE, bool SPLITQ>
+cudaError_t launch_m(const DecodeQ4Args& a, cudaStream_t s) {
+  constexpr int smem = Shape<DK, DV, MODE>::SMEM;
+  static DeviceOnce configured;
+  if (!configured.done()) {
+    cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<DK, DV, MODE, SPLITQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.mark();
+  }
+  return launch_pdl(decode_q4_kernel<DK, DV, MODE, SPLITQ>, dim3(a.max_chunks, a.c.Hkv * a.RT, a.B), dim3(THREADS), smem, s, a);
 }
 
 template <int DK, int DV>
 cudaError_t launch_d(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s) {
-  const dim3 grid(a.Hq, a.T, a.B);
-  if (q_dtype == KVA_BF16) return launch_pdl(decode_q4_kernel<bf16_t, DK, DV>, grid, dim3(32), 0, s, a);
-  return launch_pdl(decode_q4_kernel<float, DK, DV>, grid, dim3(32), 0, s, a);
+  const bool split = q_dtype == KVA_F32;
+  switch (decode_q4_row_tile(a.Hq / a.c.Hkv * a.T)) {
+    case 4: return split ? launch_m<DK, DV, 0, true>(a, s) : launch_m<DK, DV, 0, false>(a, s);
+    case 8: return split ? launch_m<DK, DV, 1, true>(a, s) : launch_m<DK, DV, 1, false>(a, s);
+    default: return split ? launch_m<DK, DV, 2, true>(a, s) : launch_m<DK, DV, 2, false>(a, s);
+  }
 }
 
 }  // namespace
@@ -79,7 +595,25 @@ bool decode_q4_supports(int Dk, int Dv) {
 
 int decode_q4_row_tile(int rows) { return rows <= 4 ? 4 : (rows <= 8 ? 8 : 16); }
 
-int decode_q4_plan_chunk(const int32_t*, int, int, int max_len, int) { return max_len; }
+// Chunks of at most 1024 keys (many waves: the last wave's tail is one such chunk), or, when all the
+// work fits the GPU at once, the smallest chunk that keeps it to one wave; at least 128 keys (one
+// stage per warp).
+int decode_q4_plan_chunk(const int32_t* lengths, int B, int units, int max_len, int max_chunks) {
+  constexpr int STEP = WARPS * SK;
+  const int64_t slots = 152 * 4;
+  int64_t keys = 0;
+  for (int b = 0; b < B; ++b) keys += lengths[b];
+  const int floor_chunk = (max_len + max_chunks - 1) / max_chunks;
+  int64_t chunk = std::max<int64_t>(floor_chunk, keys * units / slots);
+  chunk = std::min<int64_t>(std::max<int64_t>((chunk + STEP - 1) / STEP, 1) * STEP, std::max(1024, (floor_chunk + STEP - 1) / STEP * STEP));
+  while (chunk < 1024) {
+    int64_t ctas = 0;
+    for (int b = 0; b < B; ++b) ctas += (lengths[b] + chunk - 1) / chunk;
+    if (ctas * units <= slots) break;
+    chunk += STEP;
+  }
+  return (int)chunk;
+}
 
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s) {
   if (a.c.Dk == 64) return launch_d<64, 64>(a, q_dtype, s);
