@@ -1,5 +1,15 @@
-// Log probabilities over the vocabulary (lmhead_logprobs): a streaming form for any table, and the
-// merge that ends every form.
+// Log probabilities over the vocabulary (lmhead_logprobs): a tcgen05 form for bf16 tables, a
+// streaming form for the others, and the merge that ends both.
+//
+// tcgen05 form (H a multiple of 64): D[128 batch rows x N vocabulary rows] = h W^T with the batch on the
+// TMEM lanes, so that an epilogue thread owns a batch row and every sum over the vocabulary is a sum
+// along its own columns.  A float32 (or normalised) row is two bf16 halves, h = hi + lo (about 17
+// significant bits): two products into the same accumulator; a bf16 row is one.  Persistent CTAs
+// walk vocabulary tiles for one block of 128 rows: warp 0 loads (TMA, 128-byte swizzle, a ring of
+// 64-wide K chunks), warp 1 issues the MMAs into one of two accumulators, warps 2-5 read the other one
+// and keep, per row, the maximum, the two sums and a list of candidates.  With fewer than 128 rows only
+// those are loaded: the MMA reads whatever follows them in shared memory into lanes that nobody
+// reads.  Up to 8 row blocks run side by side, so that a table tile is read from HBM once per 8.
 //
 // Streaming form: grid (vocabulary split p, block of 8 batch rows).  The 8 warps of a CTA dot 4
 // table rows each with the 8 hidden rows (staged in shared memory) and leave 32 x 8 logits in
@@ -13,14 +23,18 @@
 // float32 (or two-bf16-halves) logits, whose rounding may exchange neighbours, while the second
 // scoring carries each product and sum with its rounding error (compensated dot product: Ogita,
 // Rump and Oishi, "Accurate sum and dot product"), about twice float32 precision, and orders them.
-// entropy = log s - u / s and lse = m + log s need no cancellation against m.
+// entropy = log s - u / s and lse = m + log s need no cancellation against m.  The candidates' terms
+// of s and u are exchanged for those of the second scoring: the tensor core drops a little of every
+// sum that it adds to (6e-6 of a logit at H = 4096), and the largest logits lose and weigh most.
 //
 // Method: the lm_head over the whole tied table and the pick of tokens after the final RMSNorm
 // (Youtu-VL-4B ncnn port, step 6 and "decoding and sampling").
 #include <algorithm>
 
-#include "common.cuh"
+#include <mutex>
+
 #include "launch.h"
+#include "tc.cuh"
 
 namespace kva {
 
@@ -94,9 +108,9 @@ __device__ __forceinline__ Stat stat_warp(Stat a) {
   return a;
 }
 
-// One CTA per row: the final RMSNorm in float32.
+// One CTA per row: the final RMSNorm in float32 (norm_w given) and the two bf16 halves (hb given).
 __global__ void __launch_bounds__(THREADS)
-logprob_norm_kernel(const __grid_constant__ LogprobArgs a) {
+logprob_prep_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ float s_part[WARPS];
   const int b = blockIdx.x, tid = threadIdx.x;
   griddep_wait();
@@ -106,17 +120,28 @@ logprob_norm_kernel(const __grid_constant__ LogprobArgs a) {
     return a.h_dtype == KVA_BF16 ? load1(reinterpret_cast<const bf16_t*>(a.h) + row + k)
                                  : reinterpret_cast<const float*>(a.h)[row + k];
   };
-  float ss = 0.f;
-  for (int k = tid; k < a.H; k += THREADS) { const float x = at(k); ss = fmaf(x, x, ss); }
+  float r = 1.f;
+  if (a.norm_w) {
+    float ss = 0.f;
+    for (int k = tid; k < a.H; k += THREADS) { const float x = at(k); ss = fmaf(x, x, ss); }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
-  if ((tid & 31) == 0) s_part[tid >> 5] = ss;
-  __syncthreads();
-  float tot = 0.f;
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
+    if ((tid & 31) == 0) s_part[tid >> 5] = ss;
+    __syncthreads();
+    float tot = 0.f;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) tot += s_part[w];
-  const float r = 1.0f / sqrtf(tot / (float)a.H + a.eps);
-  for (int k = tid; k < a.H; k += THREADS) a.hn[row + k] = at(k) * r * a.norm_w[k];
+    for (int w = 0; w < WARPS; ++w) tot += s_part[w];
+    r = 1.0f / sqrtf(tot / (float)a.H + a.eps);
+  }
+  for (int k = tid; k < a.H; k += THREADS) {
+    float x = at(k);
+    if (a.norm_w) a.hn[row + k] = x = x * r * a.norm_w[k];
+    if (a.hb) {
+      const uint32_t hi = f32_to_bf16_rne(x);
+      a.hb[row + k] = (uint16_t)hi;
+      a.hb[(int64_t)a.B * a.H + row + k] = (uint16_t)f32_to_bf16_rne(x - __uint_as_float(hi << 16));
+    }
+  }
 }
 
 // The row that the table meets: normalised (float32), or h itself.
@@ -130,7 +155,7 @@ __global__ void __launch_bounds__(THREADS)
 logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
   extern __shared__ __align__(16) float sh[];   // [nb][H]
   __shared__ float s_z[BG][ROWS + 1];
-  __shared__ u64 s_list[WARPS][TK > 0 ? TK : 1];
+  __shared__ u64 s_list[WARPS][TK];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b0 = blockIdx.y * BG, nb = min(BG, a.B - b0), H = a.H;
   griddep_wait();
@@ -139,9 +164,9 @@ logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
   __syncthreads();
 
   Stat st{-INFINITY, 0.f, 0.f};
-  u64 L[TK > 0 ? TK : 1];
+  u64 L[TK];
 #pragma unroll
-  for (int i = 0; i < (TK > 0 ? TK : 1); ++i) L[i] = 0ull;
+  for (int i = 0; i < TK; ++i) L[i] = 0ull;
   const int n_steps = (a.V + ROWS - 1) / ROWS;
   for (int step = blockIdx.x; step < n_steps; step += a.splits) {
     for (int r = 0; r < ROWS / WARPS; ++r) {
@@ -178,7 +203,7 @@ logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
     if (v < a.V && warp < nb) {
       const float z = s_z[warp][lane];
       stat_add(st, z);
-      if constexpr (TK > 0) list_insert<TK>(L, argmax_key(z, (uint32_t)v));
+      list_insert<TK>(L, argmax_key(z, (uint32_t)v));
     }
     __syncthreads();
   }
@@ -189,11 +214,240 @@ logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
     float* p = a.part_stat + slot * 4;
     p[0] = st.m; p[1] = st.s; p[2] = st.u;
   }
-  if constexpr (TK > 0) {
-    warp_merge<TK>(L, s_list[warp]);
-    __syncwarp();
-    for (int i = lane; i < TK; i += 32) a.part_key[slot * TK + i] = s_list[warp][i];
+  warp_merge<TK>(L, s_list[warp]);
+  __syncwarp();
+  for (int i = lane; i < TK; i += 32) a.part_key[slot * TK + i] = s_list[warp][i];
+}
+
+// ---------------------------------------------------------------------------------
+// tcgen05 form
+// ---------------------------------------------------------------------------------
+constexpr int TC_THREADS = 192;
+constexpr int KCH = 64;                       // K elements per chunk (one 128-byte swizzle row)
+constexpr int MROWS = 128;                    // batch rows per block (TMEM lanes)
+constexpr int MAX_N = 256;                    // vocabulary rows per tile
+constexpr int MAX_STAGES = 8;
+constexpr int Z_LD = 33;                      // padded row of the candidate buffer
+constexpr int TC_FIXED = 1024 + MROWS * Z_LD * 4 + 256;   // alignment slack, candidate buffer, barriers
+
+struct TcPlan {
+  int N;                                      // vocabulary rows per tile
+  int blocks, group, passes;                  // row blocks; side by side; one after the other
+  int splits;                                 // CTAs that share a row block's vocabulary
+  int parts, a_rows, stages;                  // bf16 parts of h, rows loaded per part, ring depth
+};
+
+template <int TK>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__ TcPlan p,
+                  const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH) {
+  constexpr uint64_t DESC = tc::desc_template(16, 1024, tc::SWIZZLE_128B);
+  constexpr uint32_t TMEM_COLS = 2 * MAX_N;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
+  __shared__ uint32_t s_taddr;
+  __shared__ int s_err;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int w_bytes = p.N * 128, a_bytes = p.a_rows * 128;
+  const int stage = w_bytes + p.parts * a_bytes;
+  // the MMA reads MROWS rows of h whatever a_rows: past the last stage's rows it meets this buffer
+  static_assert(Z_LD * 4 >= 128, "operand reads stay inside shared memory");
+  float* s_z = reinterpret_cast<float*>(sm + p.stages * stage);
+  const int rb0 = blockIdx.x % p.group, split = blockIdx.x / p.group;
+  const int n_tiles = (a.V + p.N - 1) / p.N, kchunks = a.H / KCH;
+  const int tiles = split < n_tiles ? (n_tiles - 1 - split) / p.splits + 1 : 0;
+  const int my_passes = rb0 < p.blocks ? (p.blocks - 1 - rb0) / p.group + 1 : 0;
+  const int items = tiles * my_passes;        // (pass, tile) in order
+
+  if (warp == 1) tc::tmem_alloc(&s_taddr, TMEM_COLS);
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+    s_err = 0;
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_taddr;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tc::tma_prefetch_desc(&tmW);
+      tc::tma_prefetch_desc(&tmH);
+      const int total = items * kchunks;
+      int it = 0;
+      for (; it < total; ++it) {
+        const int s = it % p.stages, item = it / kchunks, c = it - item * kchunks;
+        if (it >= p.stages && !mbar_wait_bounded(&empty[s], ((it / p.stages) + 1) & 1)) { s_err = 1; break; }
+        const int tile = split + (item % tiles) * p.splits, rb = rb0 + (item / tiles) * p.group;
+        uint8_t* dst = sm + s * stage;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)stage);
+        tc::tma_load_4d(dst, &tmW, c * KCH, tile * p.N, 0, 0, &full[s]);
+        for (int h = 0; h < p.parts; ++h)
+          tc::tma_load_4d(dst + w_bytes + h * a_bytes, &tmH, c * KCH, rb * MROWS, h, 0, &full[s]);
+      }
+      if (it < total)                         // gave up: the copies in flight land first (bounded)
+        for (int j = max(0, it - p.stages); j < it; ++j) (void)mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_bf16(MROWS, p.N, 0, 0);
+      int it = 0;
+      bool ok = true;
+      for (int item = 0; item < items && ok; ++item) {
+        const int ab = item & 1;
+        if (item >= 2 && !mbar_wait_bounded(&acc_empty[ab], ((item >> 1) + 1) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        for (int c = 0; c < kchunks; ++c, ++it) {
+          const int s = it % p.stages;
+          if (!mbar_wait_bounded(&full[s], (it / p.stages) & 1)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint32_t w_addr = smem_u32(sm + s * stage), h_addr = w_addr + w_bytes;
+          for (int h = 0; h < p.parts; ++h)
+#pragma unroll
+            for (int k = 0; k < KCH / 16; ++k)
+              tc::mma_ss(tmem + ab * MAX_N, tc::desc_at(DESC, h_addr + h * a_bytes + k * 32), tc::desc_at(DESC, w_addr + k * 32),
+                         idesc, (c > 0 || k > 0 || h > 0));
+          tc::mma_commit(&empty[s]);
+        }
+        if (ok) tc::mma_commit(&acc_full[ab]);
+      }
+      if (!ok) {                              // gave up: the products in flight end first (bounded)
+        s_err = 1;
+        tc::mma_commit(&drain);
+        (void)mbar_wait_bounded(&drain, 0);
+      }
+    }
+  } else {
+    const int q = warp & 3, row = q * 32 + lane;          // TMEM lane = row of the block
+    float* zrow = s_z + row * Z_LD;
+    Stat st{-INFINITY, 0.f, 0.f};
+    u64 L[TK];
+    float thr = -INFINITY;                                // logit of the list's last candidate
+#pragma unroll
+    for (int i = 0; i < TK; ++i) L[i] = 0ull;
+    bool ok = true;
+    for (int item = 0; item < items; ++item) {
+      const int ab = item & 1, tile = split + (item % tiles) * p.splits, rb = rb0 + (item / tiles) * p.group;
+      const int b = rb * MROWS + row;
+      if (!__all_sync(FULL_MASK, mbar_wait_bounded(&acc_full[ab], (item >> 1) & 1))) { ok = false; break; }
+      tc::fence_after_sync();
+      const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + ab * MAX_N;
+      if (rb * MROWS + q * 32 < a.B) {                    // a warp with rows (warp-uniform)
+        for (int c0 = 0; c0 < p.N; c0 += 32) {
+          uint32_t raw[32];
+          tc::tmem_ld32(base + c0, raw);
+          tc::tmem_wait_ld();
+          const int v0 = tile * p.N + c0, nv = a.V - v0;  // columns of this piece inside the vocabulary
+          if (nv <= 0) continue;
+          float z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = j < nv ? __uint_as_float(raw[j]) : -INFINITY;
+          float top = z[0];
+#pragma unroll
+          for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j]);
+          if (top > st.m) {
+            const float d = st.m - top, e = __expf(d);    // -inf on the first piece, whose sums are 0
+            st.u = st.s == 0.f ? 0.f : e * fmaf(st.s, d, st.u);
+            st.s *= e;
+            st.m = top;
+          }
+          float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float d0 = z[j] - st.m, d1 = z[j + 1] - st.m;
+            const float e0 = __expf(d0), e1 = __expf(d1);
+            s0 += e0; s1 += e1;
+            u0 = fmaf(e0, fmaxf(d0, -1000.f), u0);        // a masked column: 0 * -1000
+            u1 = fmaf(e1, fmaxf(d1, -1000.f), u1);
+          }
+          st.s += s0 + s1;
+          st.u += u0 + u1;
+          if (top > thr && b < a.B) {
+            uint32_t cand = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              zrow[j] = z[j];
+              if (z[j] > thr) cand |= 1u << j;
+            }
+            while (cand) {                                // ids ascend: an equal logit keeps the lower id
+              const int j = __ffs(cand) - 1;
+              cand &= cand - 1;
+              const float x = zrow[j];
+              if (x > thr) {
+                list_insert<TK>(L, argmax_key(x, (uint32_t)(v0 + j)));
+                if (L[TK - 1]) thr = float_from_order_bits((uint32_t)(L[TK - 1] >> 32));
+              }
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      if ((item + 1) % tiles == 0) {                      // the row block's vocabulary is done
+        if (b < a.B) {
+          const int64_t slot = (int64_t)b * p.splits + split;
+          *reinterpret_cast<float4*>(a.part_stat + slot * 4) = make_float4(st.m, st.s, st.u, 0.f);
+#pragma unroll
+          for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = L[i];
+        }
+        st = Stat{-INFINITY, 0.f, 0.f};
+        thr = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < TK; ++i) L[i] = 0ull;
+      }
+    }
+    if (!ok) {                                            // gave up: the rows of every pass are void
+      s_err = 1;
+      for (int ps = 0; ps < my_passes; ++ps) {
+        const int b = (rb0 + ps * p.group) * MROWS + row;
+        if (b >= a.B) continue;
+        const int64_t slot = (int64_t)b * p.splits + split;
+        a.part_stat[slot * 4] = a.part_stat[slot * 4 + 1] = a.part_stat[slot * 4 + 2] = __uint_as_float(0x7fc00000u);
+        for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = 0ull;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, TMEM_COLS);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn_lp() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// bf16 map [parts, rows, H], box [box_rows x 64]; rows past the end read as zeros.
+cudaError_t make_map(CUtensorMap* m, const void* base, int H, int rows, int parts, int box_rows) {
+  EncodeTiledFn fn = encode_fn_lp();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {(cuuint64_t)H, (cuuint64_t)rows, (cuuint64_t)parts, 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)H * 2, (cuuint64_t)H * 2 * rows, (cuuint64_t)H * 2 * rows * parts};
+  const cuuint32_t box[4] = {KCH, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // s + p with its rounding error added to c.
@@ -227,77 +481,85 @@ __device__ __forceinline__ double dot_again(const LogprobArgs& a, int b, int v) 
 template <typename WT, int TK>
 __global__ void __launch_bounds__(MERGE_THREADS)
 logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
-  constexpr int TL = TK > 0 ? TK : 1;
-  __shared__ u64 s_w[MERGE_WARPS][TL];
-  __shared__ u64 s_top[TL];
-  __shared__ double s_val[TL + 1];
+  static_assert(TK <= 32, "one lane per candidate");
+  __shared__ u64 s_w[MERGE_WARPS][TK];
+  __shared__ u64 s_top[TK];
+  __shared__ double s_val[TK + 1];
   __shared__ Stat s_stat[MERGE_WARPS];
   __shared__ double s_lse;
-  __shared__ int s_rank[TL];                            // candidate of each rank, -1: none
+  __shared__ int s_rank[TK];                            // candidate of each rank, -1: none
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
   griddep_launch_dependents();
   Stat st{-INFINITY, 0.f, 0.f};
-  u64 L[TL];
+  u64 L[TK];
 #pragma unroll
-  for (int i = 0; i < TL; ++i) L[i] = 0ull;
+  for (int i = 0; i < TK; ++i) L[i] = 0ull;
   for (int p = tid; p < a.splits; p += MERGE_THREADS) {
     const int64_t slot = (int64_t)b * a.splits + p;
     const float4 q = *reinterpret_cast<const float4*>(a.part_stat + slot * 4);
     st = stat_join(st, Stat{q.x, q.y, q.z});
-    if constexpr (TK > 0)
-      for (int i = 0; i < TK; ++i) {
-        const u64 key = a.part_key[slot * TK + i];
-        if (key <= L[TK - 1]) break;                    // lists are sorted
-        list_insert<TK>(L, key);
-      }
+    for (int i = 0; i < TK; ++i) {
+      const u64 key = a.part_key[slot * TK + i];
+      if (key <= L[TK - 1]) break;                      // lists are sorted
+      list_insert<TK>(L, key);
+    }
   }
   st = stat_warp(st);
   if (lane == 0) s_stat[warp] = st;
-  if constexpr (TK > 0) warp_merge<TK>(L, s_w[warp]);
+  warp_merge<TK>(L, s_w[warp]);
   __syncthreads();
   if (warp == 0) {
-    if constexpr (TK > 0) {
 #pragma unroll
-      for (int i = 0; i < TK; ++i) L[i] = lane < MERGE_WARPS ? s_w[lane][i] : 0ull;
-      warp_merge<TK>(L, s_top);
-    }
-    Stat all = s_stat[0];
-    for (int w = 1; w < MERGE_WARPS; ++w) all = stat_join(all, s_stat[w]);
-    if (lane == 0) {
-      const double ls = log((double)all.s);
-      s_lse = (double)all.m + ls;
-      if (a.out_lse) a.out_lse[b] = (float)s_lse;
-      if (a.out_entropy) a.out_entropy[b] = (float)(ls - (double)all.u / (double)all.s);
-    }
+    for (int i = 0; i < TK; ++i) L[i] = lane < MERGE_WARPS ? s_w[lane][i] : 0ull;
+    warp_merge<TK>(L, s_top);
   }
   __syncthreads();
+  auto id_of = [&](int c) { return (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)); };
   const int target = a.targets ? a.targets[b] : -1;
   for (int c = warp; c <= TK; c += MERGE_WARPS) {       // candidate TK is the given token
-    int v = target;
-    if (c < TK) v = s_top[c] ? (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)) : -1;
+    const int v = c == TK ? target : (s_top[c] ? id_of(c) : -1);
     const double d = v >= 0 && v < a.V ? dot_again<WT>(a, b, v) : 0.0;
     if (lane == 0) s_val[c] = d;
   }
-  if (tid < TL) s_rank[tid] = -1;
+  if (tid < TK) s_rank[tid] = -1;
+  __syncthreads();
+  if (warp == 0) {
+    Stat all = s_stat[0];
+    for (int w = 1; w < MERGE_WARPS; ++w) all = stat_join(all, s_stat[w]);
+    // the candidates carry most of the sums: exchange their logits for the ones scored again
+    double ds = 0.0, du = 0.0;
+    if (lane < TK && s_top[lane]) {
+      const double x = s_val[lane] - (double)all.m, y = (double)float_from_order_bits((uint32_t)(s_top[lane] >> 32)) - (double)all.m;
+      const double ex = exp(x), ey = exp(y);
+      ds = ex - ey;
+      du = ex * x - ey * y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ds += __shfl_xor_sync(FULL_MASK, ds, o);
+      du += __shfl_xor_sync(FULL_MASK, du, o);
+    }
+    if (lane == 0) {
+      const double sum = (double)all.s + ds, ls = log(sum);
+      s_lse = (double)all.m + ls;
+      if (a.out_lse) a.out_lse[b] = (float)s_lse;
+      if (a.out_entropy) a.out_entropy[b] = (float)(ls - ((double)all.u + du) / sum);
+    }
+    if (lane < TK && s_top[lane]) {
+      int rank = 0;
+      for (int c = 0; c < TK; ++c)
+        if (s_top[c] && (s_val[c] > s_val[lane] || (s_val[c] == s_val[lane] && id_of(c) < id_of(lane)))) ++rank;
+      s_rank[rank] = lane;
+    }
+  }
   __syncthreads();
   if (tid == 0 && a.targets)
     a.out_logprob[b] = target < 0 ? 0.f : (target < a.V ? (float)(s_val[TK] - s_lse) : __uint_as_float(0x7fc00000u));
-  if (tid < TK) {
-    const u64 key = s_top[tid];
-    const uint32_t id = 0xffffffffu - (uint32_t)(key & 0xffffffffull);
-    int rank = 0;
-    for (int c = 0; c < TK; ++c) {
-      const uint32_t other = 0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull);
-      if (s_top[c] && (s_val[c] > s_val[tid] || (s_val[c] == s_val[tid] && other < id))) ++rank;
-    }
-    if (key) s_rank[rank] = tid;
-  }
-  __syncthreads();
   if (tid < a.top_k) {
     const int c = s_rank[tid];
     const int64_t o = (int64_t)b * a.top_k + tid;
-    a.top_ids[o] = c < 0 ? -1 : (int32_t)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull));
+    a.top_ids[o] = c < 0 ? -1 : id_of(c);
     if (a.top_logprobs) a.top_logprobs[o] = c < 0 ? __uint_as_float(0x7fc00000u) : (float)(s_val[c] - s_lse);
   }
 }
@@ -305,12 +567,53 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Candidates kept for top_k alternatives: the rest is room for neighbours that rounding exchanges.
-int list_len(int top_k) { return top_k == 0 ? 0 : (top_k <= 4 ? 8 : (top_k <= 10 ? 16 : 32)); }
+int list_len(int top_k) { return top_k <= 4 ? 8 : (top_k <= 10 ? 16 : 32); }
 
-constexpr int CTAS = 152 * 2;
+constexpr int SMS = 152;                      // grids are sized for the whole GPU; fewer SMs only take longer
 int stream_splits(int B, int V) {
-  const int groups = (B + BG - 1) / BG;
-  return std::max(1, std::min((V + ROWS - 1) / ROWS, CTAS / std::min(groups, CTAS)));
+  const int groups = (B + BG - 1) / BG, ctas = 2 * SMS;
+  return std::max(1, std::min((V + ROWS - 1) / ROWS, ctas / std::min(groups, ctas)));
+}
+
+bool tc_supports(int H) { return H % KCH == 0; }
+
+// At most 8 row blocks side by side.  The tile width is the one whose rounds of tiles cost least, a tile
+// costing its columns and a fixed part worth about 32 of them.
+TcPlan tc_plan(int B, int V, int parts) {
+  TcPlan p{};
+  p.blocks = (B + MROWS - 1) / MROWS;
+  p.passes = (p.blocks + 7) / 8;
+  p.group = (p.blocks + p.passes - 1) / p.passes;
+  const int most = SMS / p.group;
+  int64_t best = 0;
+  for (int N = MAX_N; N >= 64; N /= 2) {
+    const int tiles = (V + N - 1) / N;
+    const int64_t cost = (int64_t)((tiles + most - 1) / most) * (N + 32);
+    if (best == 0 || cost < best) { best = cost; p.N = N; p.splits = std::min(tiles, most); }
+  }
+  p.parts = parts;
+  p.a_rows = std::min(MROWS, (B + 7) / 8 * 8);
+  const int stage = p.N * 128 + parts * p.a_rows * 128;
+  p.stages = std::min(MAX_STAGES, (232448 - 2048 - TC_FIXED) / stage);
+  return p;
+}
+
+template <int TK>
+cudaError_t launch_tc(const LogprobArgs& a, const TcPlan& p, cudaStream_t s) {
+  constexpr int smem = 232448 - 2048;         // everything but the static barriers: one CTA per SM
+  static DeviceOnce configured;
+  if (!configured.done()) {
+    cudaError_t e = cudaFuncSetAttribute(logprob_tc_kernel<TK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.mark();
+  }
+  CUtensorMap mw, mh;
+  cudaError_t e = make_map(&mw, a.W, a.H, a.V, 1, p.N);
+  if (e != cudaSuccess) return e;
+  if ((e = make_map(&mh, p.parts == 2 ? (const void*)a.hb : a.h, a.H, a.B, p.parts, p.a_rows)) != cudaSuccess) return e;
+  if ((e = launch_pdl(logprob_tc_kernel<TK>, dim3(p.group * p.splits), dim3(TC_THREADS), smem, s, a, p, mw, mh)) != cudaSuccess)
+    return e;
+  return launch_pdl(logprob_merge_kernel<bf16_t, TK>, dim3(a.B), dim3(MERGE_THREADS), 0, s, a);
 }
 
 template <typename WT, int TK>
@@ -328,38 +631,46 @@ cudaError_t launch_stream(const LogprobArgs& a, cudaStream_t s) {
   return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(MERGE_THREADS), 0, s, a);
 }
 
-template <typename WT>
-cudaError_t launch_w(const LogprobArgs& a, cudaStream_t s) {
-  switch (list_len(a.top_k)) {
-    case 0: return launch_stream<WT, 0>(a, s);
-    case 8: return launch_stream<WT, 8>(a, s);
-    case 16: return launch_stream<WT, 16>(a, s);
-    default: return launch_stream<WT, 32>(a, s);
-  }
+template <int TK>
+cudaError_t launch_k(const LogprobArgs& a, kva_dtype w_dtype, const TcPlan* p, cudaStream_t s) {
+  if (p) return launch_tc<TK>(a, *p, s);
+  return w_dtype == KVA_BF16 ? launch_stream<bf16_t, TK>(a, s) : launch_stream<float, TK>(a, s);
 }
 
 }  // namespace
 
-// Workspace: [normalised rows, float32][partial statistics][partial lists]
+// Workspace: [normalised rows, float32][bf16 halves][partial statistics][partial lists]
 size_t logprob_workspace_bytes(int B, int H, int V, int top_k) {
-  const size_t parts = (size_t)B * stream_splits(B, V);
-  return up256(sizeof(float) * (size_t)B * H) + up256(parts * 16) + up256(parts * 8 * list_len(top_k));
+  int splits = stream_splits(B, V);
+  if (tc_supports(H)) splits = std::max(splits, tc_plan(B, V, 2).splits);
+  const size_t parts = (size_t)B * splits;
+  return 2 * up256(sizeof(float) * (size_t)B * H) + up256(parts * 16) + up256(parts * 8 * list_len(top_k));
 }
 
 cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, cudaStream_t s, unsigned* n_launches) {
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  *n_launches = 2;
-  a.splits = stream_splits(a.B, a.V);
+  const bool tc = w_dtype == KVA_BF16 && tc_supports(a.H) && encode_fn_lp() != nullptr;
+  const bool split = a.h_dtype == KVA_F32 || a.norm_w;    // rows that need two bf16 halves
+  TcPlan p{};
+  if (tc) p = tc_plan(a.B, a.V, split ? 2 : 1);
+  a.splits = tc ? p.splits : stream_splits(a.B, a.V);
   a.hn = reinterpret_cast<float*>(ws);
+  ws += up256(sizeof(float) * (size_t)a.B * a.H);
+  a.hb = tc && split ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   ws += up256(sizeof(float) * (size_t)a.B * a.H);
   a.part_stat = reinterpret_cast<float*>(ws);
   a.part_key = reinterpret_cast<u64*>(ws + up256((size_t)a.B * a.splits * 16));
-  if (a.norm_w) {
-    cudaError_t e = launch_pdl(logprob_norm_kernel, dim3(a.B), dim3(THREADS), 0, s, a);
+  *n_launches = 2;
+  if (a.norm_w || a.hb) {
+    cudaError_t e = launch_pdl(logprob_prep_kernel, dim3(a.B), dim3(THREADS), 0, s, a);
     if (e != cudaSuccess) return e;
     *n_launches = 3;
   }
-  return w_dtype == KVA_BF16 ? launch_w<bf16_t>(a, s) : launch_w<float>(a, s);
+  switch (list_len(a.top_k)) {
+    case 8: return launch_k<8>(a, w_dtype, tc ? &p : nullptr, s);
+    case 16: return launch_k<16>(a, w_dtype, tc ? &p : nullptr, s);
+    default: return launch_k<32>(a, w_dtype, tc ? &p : nullptr, s);
+  }
 }
 
 }  // namespace kva
