@@ -44,8 +44,8 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int BG = 8;                         // batch rows per CTA (one per warp)
 constexpr int ROWS = 32;                      // vocabulary rows per step (one per lane)
-constexpr int MERGE_THREADS = 128;
-constexpr int MERGE_WARPS = MERGE_THREADS / 32;
+constexpr int MERGE_MAX = 320;                // threads of a merge CTA: at least one per split
+constexpr int MERGE_MAX_WARPS = MERGE_MAX / 32;
 
 using u64 = unsigned long long;
 
@@ -57,17 +57,15 @@ __device__ __forceinline__ void list_insert(u64 (&L)[TK], u64 key) {
   for (int i = TK - 1; i > 0; --i) L[i] = key > L[i - 1] ? L[i - 1] : (key > L[i] ? key : L[i]);
   L[0] = key > L[0] ? key : L[0];
 }
-// The TK best of the warp's 32 lists, into out[] (lane 0 writes).
+// The TK best of the warp's 32 lists, into out[] (lane 0 writes).  The maximum of the list heads is
+// found in two 32-bit steps, logit bits and then ids.
 template <int TK>
 __device__ __forceinline__ void warp_merge(u64 (&L)[TK], u64* out) {
   const int lane = threadIdx.x & 31;
   for (int r = 0; r < TK; ++r) {
-    u64 best = L[0];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const u64 other = __shfl_xor_sync(FULL_MASK, best, o);
-      best = other > best ? other : best;
-    }
+    const uint32_t hi = (uint32_t)(L[0] >> 32), top = __reduce_max_sync(FULL_MASK, hi);
+    const uint32_t id = __reduce_max_sync(FULL_MASK, hi == top ? (uint32_t)L[0] : 0u);
+    const u64 best = ((u64)top << 32) | id;
     if (lane == 0) out[r] = best;
     if (best != 0ull && L[0] == best) {       // keys are unique: one lane pops
 #pragma unroll
@@ -116,30 +114,53 @@ logprob_prep_kernel(const __grid_constant__ LogprobArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t row = (int64_t)b * a.H;
-  auto at = [&](int k) {
-    return a.h_dtype == KVA_BF16 ? load1(reinterpret_cast<const bf16_t*>(a.h) + row + k)
-                                 : reinterpret_cast<const float*>(a.h)[row + k];
-  };
+  constexpr int MAX_PER = 4096 / THREADS / 4;             // pieces of 4 a thread holds (H <= 4096)
+  float x[MAX_PER][4], w[MAX_PER][4];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < MAX_PER; ++j) {
+    const int k = 4 * (tid + j * THREADS);
+    if (k >= a.H) continue;
+    if (a.h_dtype == KVA_BF16) {
+      const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.h) + row + k);
+      x[j][0] = bf16_lo(u.x); x[j][1] = bf16_hi(u.x); x[j][2] = bf16_lo(u.y); x[j][3] = bf16_hi(u.y);
+    } else {
+      const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.h) + row + k);
+      x[j][0] = u.x; x[j][1] = u.y; x[j][2] = u.z; x[j][3] = u.w;
+    }
+    if (a.norm_w) {
+      const float4 u = *reinterpret_cast<const float4*>(a.norm_w + k);
+      w[j][0] = u.x; w[j][1] = u.y; w[j][2] = u.z; w[j][3] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+  }
   float r = 1.f;
   if (a.norm_w) {
-    float ss = 0.f;
-    for (int k = tid; k < a.H; k += THREADS) { const float x = at(k); ss = fmaf(x, x, ss); }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL_MASK, ss, o);
     if ((tid & 31) == 0) s_part[tid >> 5] = ss;
     __syncthreads();
     float tot = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) tot += s_part[w];
+    for (int v = 0; v < WARPS; ++v) tot += s_part[v];
     r = 1.0f / sqrtf(tot / (float)a.H + a.eps);
   }
-  for (int k = tid; k < a.H; k += THREADS) {
-    float x = at(k);
-    if (a.norm_w) a.hn[row + k] = x = x * r * a.norm_w[k];
+#pragma unroll
+  for (int j = 0; j < MAX_PER; ++j) {
+    const int k = 4 * (tid + j * THREADS);
+    if (k >= a.H) continue;
+    if (a.norm_w) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[j][i] = x[j][i] * r * w[j][i];
+      *reinterpret_cast<float4*>(a.hn + row + k) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+    }
     if (a.hb) {
-      const uint32_t hi = f32_to_bf16_rne(x);
-      a.hb[row + k] = (uint16_t)hi;
-      a.hb[(int64_t)a.B * a.H + row + k] = (uint16_t)f32_to_bf16_rne(x - __uint_as_float(hi << 16));
+      const uint32_t h01 = pack_bf16x2(x[j][0], x[j][1]), h23 = pack_bf16x2(x[j][2], x[j][3]);
+      *reinterpret_cast<uint2*>(a.hb + row + k) = make_uint2(h01, h23);
+      *reinterpret_cast<uint2*>(a.hb + (int64_t)a.B * a.H + row + k) =
+          make_uint2(pack_bf16x2(x[j][0] - bf16_lo(h01), x[j][1] - bf16_hi(h01)),
+                     pack_bf16x2(x[j][2] - bf16_lo(h23), x[j][3] - bf16_hi(h23)));
     }
   }
 }
@@ -148,6 +169,12 @@ logprob_prep_kernel(const __grid_constant__ LogprobArgs a) {
 __device__ __forceinline__ float hidden_at(const LogprobArgs& a, int64_t i) {
   if (a.norm_w) return a.hn[i];
   return a.h_dtype == KVA_BF16 ? load1(reinterpret_cast<const bf16_t*>(a.h) + i) : reinterpret_cast<const float*>(a.h)[i];
+}
+
+__device__ __forceinline__ void hidden8(const LogprobArgs& a, int64_t i, float (&y)[8]) {
+  if (a.norm_w) load8(a.hn + i, y);
+  else if (a.h_dtype == KVA_BF16) load8(reinterpret_cast<const bf16_t*>(a.h) + i, y);
+  else load8(reinterpret_cast<const float*>(a.h) + i, y);
 }
 
 template <typename WT, int TK>
@@ -275,53 +302,57 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
   griddep_wait();
   griddep_launch_dependents();
 
+  // Ring positions advance by counting: a division by a run-time ring depth or tile count costs the one
+  // issuing thread about 60 ns, several of them a chunk cost more than the chunk's products.
   if (warp == 0) {
     if (lane == 0) {
       tc::tma_prefetch_desc(&tmW);
       tc::tma_prefetch_desc(&tmH);
-      const int total = items * kchunks;
-      int it = 0;
-      for (; it < total; ++it) {
-        const int s = it % p.stages, item = it / kchunks, c = it - item * kchunks;
-        if (it >= p.stages && !mbar_wait_bounded(&empty[s], ((it / p.stages) + 1) & 1)) { s_err = 1; break; }
-        const int tile = split + (item % tiles) * p.splits, rb = rb0 + (item / tiles) * p.group;
-        uint8_t* dst = sm + s * stage;
-        mbar_arrive_expect_tx(&full[s], (uint32_t)stage);
-        tc::tma_load_4d(dst, &tmW, c * KCH, tile * p.N, 0, 0, &full[s]);
-        for (int h = 0; h < p.parts; ++h)
-          tc::tma_load_4d(dst + w_bytes + h * a_bytes, &tmH, c * KCH, rb * MROWS, h, 0, &full[s]);
-      }
-      if (it < total)                         // gave up: the copies in flight land first (bounded)
+      int s = 0, it = 0;
+      uint32_t phase = 1;                     // of empty[s]: the first round finds it free
+      bool ok = true;
+      for (int ps = 0, rb = rb0; ps < my_passes && ok; ++ps, rb += p.group)
+        for (int tl = 0, tile = split; tl < tiles && ok; ++tl, tile += p.splits)
+          for (int c = 0; c < kchunks; ++c, ++it) {
+            if (it >= p.stages && !mbar_wait_bounded(&empty[s], phase)) { ok = false; break; }
+            uint8_t* dst = sm + s * stage;
+            mbar_arrive_expect_tx(&full[s], (uint32_t)stage);
+            tc::tma_load_4d(dst, &tmW, c * KCH, tile * p.N, 0, 0, &full[s]);
+            for (int h = 0; h < p.parts; ++h)
+              tc::tma_load_4d(dst + w_bytes + h * a_bytes, &tmH, c * KCH, rb * MROWS, h, 0, &full[s]);
+            if (++s == p.stages) { s = 0; phase ^= 1; }
+          }
+      if (!ok) {                              // gave up: the copies in flight land first (bounded)
+        s_err = 1;
         for (int j = max(0, it - p.stages); j < it; ++j) (void)mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1);
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = tc::idesc_bf16(MROWS, p.N, 0, 0);
-      int it = 0;
-      bool ok = true;
-      for (int item = 0; item < items && ok; ++item) {
-        const int ab = item & 1;
-        if (item >= 2 && !mbar_wait_bounded(&acc_empty[ab], ((item >> 1) + 1) & 1)) { ok = false; break; }
+    const uint32_t idesc = tc::idesc_bf16(MROWS, p.N, 0, 0);
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int item = 0; item < items && ok; ++item) {
+      const int ab = item & 1;
+      if (item >= 2) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&acc_empty[ab], ((item >> 1) + 1) & 1));
+      tc::fence_after_sync();
+      for (int c = 0; c < kchunks && ok; ++c) {
+        ok = __all_sync(FULL_MASK, mbar_wait_bounded(&full[s], phase));
+        if (!ok) break;
         tc::fence_after_sync();
-        for (int c = 0; c < kchunks; ++c, ++it) {
-          const int s = it % p.stages;
-          if (!mbar_wait_bounded(&full[s], (it / p.stages) & 1)) { ok = false; break; }
-          tc::fence_after_sync();
-          const uint32_t w_addr = smem_u32(sm + s * stage), h_addr = w_addr + w_bytes;
-          for (int h = 0; h < p.parts; ++h)
-#pragma unroll
-            for (int k = 0; k < KCH / 16; ++k)
-              tc::mma_ss(tmem + ab * MAX_N, tc::desc_at(DESC, h_addr + h * a_bytes + k * 32), tc::desc_at(DESC, w_addr + k * 32),
-                         idesc, (c > 0 || k > 0 || h > 0));
-          tc::mma_commit(&empty[s]);
-        }
-        if (ok) tc::mma_commit(&acc_full[ab]);
+        const uint32_t w_addr = smem_u32(sm + s * stage), h_addr = w_addr + w_bytes;
+        for (int h = 0; h < p.parts; ++h)
+          tc::mma_ss_x4_elect(tmem + ab * MAX_N, tc::desc_at(DESC, h_addr + h * a_bytes), tc::desc_at(DESC, w_addr), idesc,
+                              c > 0 || h > 0);
+        tc::mma_commit_elect(&empty[s]);
+        if (++s == p.stages) { s = 0; phase ^= 1; }
       }
-      if (!ok) {                              // gave up: the products in flight end first (bounded)
-        s_err = 1;
-        tc::mma_commit(&drain);
-        (void)mbar_wait_bounded(&drain, 0);
-      }
+      if (ok) tc::mma_commit_elect(&acc_full[ab]);
+    }
+    if (!ok) {                                // gave up: the products in flight end first (bounded)
+      s_err = 1;
+      tc::mma_commit_elect(&drain);
+      (void)mbar_wait_bounded(&drain, 0);
     }
   } else {
     const int q = warp & 3, row = q * 32 + lane;          // TMEM lane = row of the block
@@ -332,9 +363,9 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
 #pragma unroll
     for (int i = 0; i < TK; ++i) L[i] = 0ull;
     bool ok = true;
+    int tile = split, rb = rb0;
     for (int item = 0; item < items; ++item) {
-      const int ab = item & 1, tile = split + (item % tiles) * p.splits, rb = rb0 + (item / tiles) * p.group;
-      const int b = rb * MROWS + row;
+      const int ab = item & 1, b = rb * MROWS + row;
       if (!__all_sync(FULL_MASK, mbar_wait_bounded(&acc_full[ab], (item >> 1) & 1))) { ok = false; break; }
       tc::fence_after_sync();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + ab * MAX_N;
@@ -390,13 +421,16 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
-      if ((item + 1) % tiles == 0) {                      // the row block's vocabulary is done
+      tile += p.splits;
+      if (tile >= n_tiles) {                              // the row block's vocabulary is done
         if (b < a.B) {
           const int64_t slot = (int64_t)b * p.splits + split;
           *reinterpret_cast<float4*>(a.part_stat + slot * 4) = make_float4(st.m, st.s, st.u, 0.f);
 #pragma unroll
           for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = L[i];
         }
+        tile = split;
+        rb += p.group;
         st = Stat{-INFINITY, 0.f, 0.f};
         thr = -INFINITY;
 #pragma unroll
@@ -456,84 +490,105 @@ __device__ __forceinline__ void sum_two(float& s, float& c, float p) {
   c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z)));
   s = t;
 }
-// W[v] . h_b in about twice float32 precision (a warp; every lane gets the result).
+// W[v] . h_b in about twice float32 precision (a warp; every lane gets the result).  The lanes join in
+// pairs of floats too: the GPU's float64 units are few.
 template <typename WT>
 __device__ __forceinline__ double dot_again(const LogprobArgs& a, int b, int v) {
   const WT* w = reinterpret_cast<const WT*>(a.W) + (int64_t)v * a.H;
+  const int64_t hrow = (int64_t)b * a.H;
   float s = 0.f, c = 0.f;
-  for (int k = (threadIdx.x & 31) * 8; k < a.H; k += 256) {
-    float x[8];
-    load8(w + k, x);
+  constexpr int AHEAD = 4;                                // 8-element pieces loaded before any is used
+  for (int k0 = (threadIdx.x & 31) * 8; k0 < a.H; k0 += 256 * AHEAD) {
+    float x[AHEAD][8], y[AHEAD][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = hidden_at(a, (int64_t)b * a.H + k + i);
-      const float p = __fmul_rn(x[i], y);
-      c = __fadd_rn(c, __fmaf_rn(x[i], y, -p));
-      sum_two(s, c, p);
-    }
+    for (int j = 0; j < AHEAD; ++j)
+      if (k0 + 256 * j < a.H) {
+        load8(w + k0 + 256 * j, x[j]);
+        hidden8(a, hrow + k0 + 256 * j, y[j]);
+      }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (k0 + 256 * j < a.H) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = __fmul_rn(x[j][i], y[j][i]);
+          c = __fadd_rn(c, __fmaf_rn(x[j][i], y[j][i], -p));
+          sum_two(s, c, p);
+        }
+      }
   }
-  double d = (double)s + (double)c;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(FULL_MASK, d, o);
-  return d;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float s2 = __shfl_xor_sync(FULL_MASK, s, o), c2 = __shfl_xor_sync(FULL_MASK, c, o);
+    const float lo = fminf(s, s2), hi = fmaxf(s, s2);   // both lanes of a pair add in one order
+    s = hi;
+    c = __fadd_rn(c, c2);
+    sum_two(s, c, lo);
+  }
+  return (double)s + (double)c;
 }
 
 template <typename WT, int TK>
-__global__ void __launch_bounds__(MERGE_THREADS)
+__global__ void __launch_bounds__(MERGE_MAX)
 logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   static_assert(TK <= 32, "one lane per candidate");
-  __shared__ u64 s_w[MERGE_WARPS][TK];
+  __shared__ u64 s_w[MERGE_MAX_WARPS][TK];
   __shared__ u64 s_top[TK];
   __shared__ double s_val[TK + 1];
-  __shared__ Stat s_stat[MERGE_WARPS];
+  __shared__ Stat s_stat[MERGE_MAX_WARPS];
   __shared__ double s_lse;
   __shared__ int s_rank[TK];                            // candidate of each rank, -1: none
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
   Stat st{-INFINITY, 0.f, 0.f};
   u64 L[TK];
 #pragma unroll
   for (int i = 0; i < TK; ++i) L[i] = 0ull;
-  for (int p = tid; p < a.splits; p += MERGE_THREADS) {
-    const int64_t slot = (int64_t)b * a.splits + p;
+  if (tid < a.splits) {                                 // one split per thread: its list is sorted
+    const int64_t slot = (int64_t)b * a.splits + tid;
     const float4 q = *reinterpret_cast<const float4*>(a.part_stat + slot * 4);
-    st = stat_join(st, Stat{q.x, q.y, q.z});
-    for (int i = 0; i < TK; ++i) {
-      const u64 key = a.part_key[slot * TK + i];
-      if (key <= L[TK - 1]) break;                      // lists are sorted
-      list_insert<TK>(L, key);
+    st = Stat{q.x, q.y, q.z};
+    const ulonglong2* keys = reinterpret_cast<const ulonglong2*>(a.part_key + slot * TK);
+#pragma unroll
+    for (int i = 0; i < TK / 2; ++i) {
+      const ulonglong2 two = keys[i];
+      L[2 * i] = two.x; L[2 * i + 1] = two.y;
     }
   }
   st = stat_warp(st);
   if (lane == 0) s_stat[warp] = st;
   warp_merge<TK>(L, s_w[warp]);
+  const int target = a.targets ? a.targets[b] : -1;
+  if (warp == warps - 1) {                              // the given token waits for no list
+    const double d = target >= 0 && target < a.V ? dot_again<WT>(a, b, target) : 0.0;
+    if (lane == 0) s_val[TK] = d;
+  }
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int i = 0; i < TK; ++i) L[i] = lane < MERGE_WARPS ? s_w[lane][i] : 0ull;
+    for (int i = 0; i < TK; ++i) L[i] = lane < warps ? s_w[lane][i] : 0ull;
     warp_merge<TK>(L, s_top);
   }
   __syncthreads();
   auto id_of = [&](int c) { return (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)); };
-  const int target = a.targets ? a.targets[b] : -1;
-  for (int c = warp; c <= TK; c += MERGE_WARPS) {       // candidate TK is the given token
-    const int v = c == TK ? target : (s_top[c] ? id_of(c) : -1);
-    const double d = v >= 0 && v < a.V ? dot_again<WT>(a, b, v) : 0.0;
+  for (int c = warp; c < TK; c += warps) {
+    const double d = s_top[c] ? dot_again<WT>(a, b, id_of(c)) : 0.0;
     if (lane == 0) s_val[c] = d;
   }
   if (tid < TK) s_rank[tid] = -1;
   __syncthreads();
   if (warp == 0) {
     Stat all = s_stat[0];
-    for (int w = 1; w < MERGE_WARPS; ++w) all = stat_join(all, s_stat[w]);
-    // the candidates carry most of the sums: exchange their logits for the ones scored again
-    double ds = 0.0, du = 0.0;
+    for (int w = 1; w < warps; ++w) all = stat_join(all, s_stat[w]);
+    // the candidates carry most of the sums: exchange their logits y for the ones scored again,
+    // x = y + d with a small d, so exp(x) - exp(y) = exp(y) (d + d^2 / 2)
+    float ds = 0.f, du = 0.f;
     if (lane < TK && s_top[lane]) {
-      const double x = s_val[lane] - (double)all.m, y = (double)float_from_order_bits((uint32_t)(s_top[lane] >> 32)) - (double)all.m;
-      const double ex = exp(x), ey = exp(y);
-      ds = ex - ey;
-      du = ex * x - ey * y;
+      const float z = float_from_order_bits((uint32_t)(s_top[lane] >> 32)), y = z - all.m;
+      const float d = (float)(s_val[lane] - (double)z), g = fmaf(0.5f * d, d, d), e = __expf(y);
+      ds = e * g;
+      du = e * fmaf(g, y + d, d);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -541,10 +596,10 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
       du += __shfl_xor_sync(FULL_MASK, du, o);
     }
     if (lane == 0) {
-      const double sum = (double)all.s + ds, ls = log(sum);
-      s_lse = (double)all.m + ls;
+      const float sum = all.s + ds, ls = logf(sum);
+      s_lse = (double)all.m + (double)ls;
       if (a.out_lse) a.out_lse[b] = (float)s_lse;
-      if (a.out_entropy) a.out_entropy[b] = (float)(ls - ((double)all.u + du) / sum);
+      if (a.out_entropy) a.out_entropy[b] = ls - (all.u + du) / sum;
     }
     if (lane < TK && s_top[lane]) {
       int rank = 0;
@@ -598,6 +653,11 @@ TcPlan tc_plan(int B, int V, int parts) {
   return p;
 }
 
+// One thread per split, at least 4 warps to share the second scoring (8 while the rows do not fill the GPU).
+int merge_threads(const LogprobArgs& a) {
+  return std::max((a.splits + 31) / 32 * 32, a.B <= 4 * SMS ? 256 : 128);
+}
+
 template <int TK>
 cudaError_t launch_tc(const LogprobArgs& a, const TcPlan& p, cudaStream_t s) {
   constexpr int smem = 232448 - 2048;         // everything but the static barriers: one CTA per SM
@@ -613,7 +673,7 @@ cudaError_t launch_tc(const LogprobArgs& a, const TcPlan& p, cudaStream_t s) {
   if ((e = make_map(&mh, p.parts == 2 ? (const void*)a.hb : a.h, a.H, a.B, p.parts, p.a_rows)) != cudaSuccess) return e;
   if ((e = launch_pdl(logprob_tc_kernel<TK>, dim3(p.group * p.splits), dim3(TC_THREADS), smem, s, a, p, mw, mh)) != cudaSuccess)
     return e;
-  return launch_pdl(logprob_merge_kernel<bf16_t, TK>, dim3(a.B), dim3(MERGE_THREADS), 0, s, a);
+  return launch_pdl(logprob_merge_kernel<bf16_t, TK>, dim3(a.B), dim3(merge_threads(a)), 0, s, a);
 }
 
 template <typename WT, int TK>
@@ -628,7 +688,7 @@ cudaError_t launch_stream(const LogprobArgs& a, cudaStream_t s) {
   }
   cudaError_t e = launch_pdl(logprob_stream_kernel<WT, TK>, dim3(a.splits, (a.B + BG - 1) / BG), dim3(THREADS), smem, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(MERGE_THREADS), 0, s, a);
+  return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(merge_threads(a)), 0, s, a);
 }
 
 template <int TK>

@@ -91,6 +91,28 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
                " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
                :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
+// Four products over adjacent 16-wide K slices of two K-major 128-byte-swizzled operands (32 bytes, 2
+// descriptor units, apart), issued by one elected lane of a converged warp.  From a converged warp
+// 128 x 256 x 16 products issue back to back at the tensor pipe's rate (65 ns each over all SMs);
+// from a branch that one lane takes they take 84 ns and more.  `accumulate` holds for the first one.
+__device__ __forceinline__ void mma_ss_x4_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %9, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %10, p;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %4, %10, 1;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %10, 1;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %10, 1;\n}\n"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "l"(a_desc + 2), "l"(b_desc + 2), "l"(a_desc + 4), "l"(b_desc + 4),
+         "l"(a_desc + 6), "l"(b_desc + 6), "r"(accumulate), "r"(idesc) : "memory");
+}
+// mma_commit by the lane that mma_ss_x4_elect elects.
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+      :: "r"(smem_u32(bar)) : "memory");
+}
 // Arrive on `bar` once every tcgen05.mma previously issued by this thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
