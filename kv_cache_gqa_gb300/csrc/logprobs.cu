@@ -6,8 +6,8 @@
 // along its own columns.  A float32 (or normalised) row is two bf16 halves, h = hi + lo (about 17
 // significant bits): two products into the same accumulator; a bf16 row is one.  Persistent CTAs
 // walk vocabulary tiles for one block of 128 rows: warp 0 loads (TMA, 128-byte swizzle, a ring of
-// 64-wide K chunks), warp 1 issues the MMAs into one of two accumulators, warps 2-5 read the other one
-// and keep, per row, the maximum, the two sums and a list of candidates.  With fewer than 128 rows only
+// 64-wide K chunks), warp 1 issues the MMAs into one of two accumulators, warps 2-9 read the other one
+// (a thread: one row, half of the columns) and keep, per row, the maximum, the two sums and a list of candidates.  With fewer than 128 rows only
 // those are loaded: the MMA reads whatever follows them in shared memory into lanes that nobody
 // reads.  Up to 8 row blocks run side by side, so that a table tile is read from HBM once per 8.
 //
@@ -44,8 +44,8 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int BG = 8;                         // batch rows per CTA (one per warp)
 constexpr int ROWS = 32;                      // vocabulary rows per step (one per lane)
-constexpr int MERGE_MAX = 320;                // threads of a merge CTA: at least one per split
-constexpr int MERGE_MAX_WARPS = MERGE_MAX / 32;
+// Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per token scored again.
+__host__ __device__ constexpr int merge_max(int TK) { return TK <= 16 ? 544 : 320; }
 
 using u64 = unsigned long long;
 
@@ -90,19 +90,22 @@ __device__ __forceinline__ void stat_add(Stat& a, float z) {
     if (e > 0.f) a.u = fmaf(e, d, a.u);
   }
 }
-__device__ __forceinline__ Stat stat_join(const Stat& a, const Stat& b) {
-  const float m = fmaxf(a.m, b.m);
-  Stat r{m, 0.f, 0.f};
-  if (a.s != 0.f) { const float d = a.m - m, e = __expf(d); r.s += a.s * e; r.u += e * fmaf(a.s, d, a.u); }
-  if (b.s != 0.f) { const float d = b.m - m, e = __expf(d); r.s += b.s * e; r.u += e * fmaf(b.s, d, b.u); }
-  return r;
-}
+// The union of the warp's 32 sets, in every lane.
 __device__ __forceinline__ Stat stat_warp(Stat a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+  if (a.s != 0.f) {                           // an empty set has m = -inf
+    const float d = a.m - m, e = __expf(d);
+    a.u = e * fmaf(a.s, d, a.u);
+    a.s *= e;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Stat b{__shfl_xor_sync(FULL_MASK, a.m, o), __shfl_xor_sync(FULL_MASK, a.s, o), __shfl_xor_sync(FULL_MASK, a.u, o)};
-    a = stat_join(a, b);
+    a.s += __shfl_xor_sync(FULL_MASK, a.s, o);
+    a.u += __shfl_xor_sync(FULL_MASK, a.u, o);
   }
+  a.m = m;
   return a;
 }
 
@@ -169,12 +172,6 @@ logprob_prep_kernel(const __grid_constant__ LogprobArgs a) {
 __device__ __forceinline__ float hidden_at(const LogprobArgs& a, int64_t i) {
   if (a.norm_w) return a.hn[i];
   return a.h_dtype == KVA_BF16 ? load1(reinterpret_cast<const bf16_t*>(a.h) + i) : reinterpret_cast<const float*>(a.h)[i];
-}
-
-__device__ __forceinline__ void hidden8(const LogprobArgs& a, int64_t i, float (&y)[8]) {
-  if (a.norm_w) load8(a.hn + i, y);
-  else if (a.h_dtype == KVA_BF16) load8(reinterpret_cast<const bf16_t*>(a.h) + i, y);
-  else load8(reinterpret_cast<const float*>(a.h) + i, y);
 }
 
 template <typename WT, int TK>
@@ -249,13 +246,65 @@ logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
 // ---------------------------------------------------------------------------------
 // tcgen05 form
 // ---------------------------------------------------------------------------------
-constexpr int TC_THREADS = 192;
+constexpr int EPI_WARPS = 8;                  // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int KCH = 64;                       // K elements per chunk (one 128-byte swizzle row)
 constexpr int MROWS = 128;                    // batch rows per block (TMEM lanes)
 constexpr int MAX_N = 256;                    // vocabulary rows per tile
 constexpr int MAX_STAGES = 8;
-constexpr int Z_LD = 33;                      // padded row of the candidate buffer
-constexpr int TC_FIXED = 1024 + MROWS * Z_LD * 4 + 256;   // alignment slack, candidate buffer, barriers
+constexpr int Z_LD = 17;                      // padded row of the candidate buffer: 16 logits a thread
+constexpr int Z_BYTES = 32 * EPI_WARPS * Z_LD * 4;
+constexpr int TC_FIXED = 1024 + Z_BYTES;      // alignment slack, candidate buffer
+
+// Sorted list of a row's TK best logits; larger first, equal ones in the order of insertion.
+template <int TK>
+struct TopList {
+  float v[TK];
+  int id[TK];                                 // -1: none yet
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < TK; ++i) { v[i] = -INFINITY; id[i] = -1; }
+  }
+  // x takes its place and moves the rest down: v[i] becomes the middle one of v[i - 1], v[i] and x
+  __device__ __forceinline__ void insert(float x, int token) {
+    bool above[TK];                           // x goes before entry i
+#pragma unroll
+    for (int i = 0; i < TK; ++i) above[i] = x > v[i];
+#pragma unroll
+    for (int i = TK - 1; i > 0; --i) {
+      id[i] = above[i - 1] ? id[i - 1] : (above[i] ? token : id[i]);
+      v[i] = fminf(v[i - 1], fmaxf(v[i], x));
+    }
+    id[0] = above[0] ? token : id[0];
+    v[0] = fmaxf(v[0], x);
+  }
+  __device__ __forceinline__ u64 key(int i) const { return id[i] < 0 ? 0ull : argmax_key(v[i], (uint32_t)id[i]); }
+};
+
+// Two float32 operations an instruction.
+__device__ __forceinline__ u64 pack_f32x2(float lo, float hi) {
+  return ((u64)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ u64 add_f32x2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 mul_f32x2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 fma_f32x2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 struct TcPlan {
   int N;                                      // vocabulary rows per tile
@@ -279,7 +328,7 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
   const int w_bytes = p.N * 128, a_bytes = p.a_rows * 128;
   const int stage = w_bytes + p.parts * a_bytes;
   // the MMA reads MROWS rows of h whatever a_rows: past the last stage's rows it meets this buffer
-  static_assert(Z_LD * 4 >= 128, "operand reads stay inside shared memory");
+  static_assert(Z_BYTES >= MROWS * 128, "operand reads stay inside shared memory");
   float* s_z = reinterpret_cast<float*>(sm + p.stages * stage);
   const int rb0 = blockIdx.x % p.group, split = blockIdx.x / p.group;
   const int n_tiles = (a.V + p.N - 1) / p.N, kchunks = a.H / KCH;
@@ -290,7 +339,7 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
   if (warp == 1) tc::tmem_alloc(&s_taddr, TMEM_COLS);
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], EPI_WARPS); }
     mbar_init(&drain, 1);
     fence_mbar_init();
     s_err = 0;
@@ -356,66 +405,80 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
     }
   } else {
     const int q = warp & 3, row = q * 32 + lane;          // TMEM lane = row of the block
-    float* zrow = s_z + row * Z_LD;
+    const int side = (warp - 2) >> 2, cols = p.N / 2;     // the warp's half of the columns
+    float* zrow = s_z + (tid - 64) * Z_LD;
     Stat st{-INFINITY, 0.f, 0.f};
-    u64 L[TK];
-    float thr = -INFINITY;                                // logit of the list's last candidate
-#pragma unroll
-    for (int i = 0; i < TK; ++i) L[i] = 0ull;
+    TopList<TK> list;
+    list.clear();
     bool ok = true;
     int tile = split, rb = rb0;
     for (int item = 0; item < items; ++item) {
       const int ab = item & 1, b = rb * MROWS + row;
       if (!__all_sync(FULL_MASK, mbar_wait_bounded(&acc_full[ab], (item >> 1) & 1))) { ok = false; break; }
       tc::fence_after_sync();
-      const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + ab * MAX_N;
-      if (rb * MROWS + q * 32 < a.B) {                    // a warp with rows (warp-uniform)
-        for (int c0 = 0; c0 < p.N; c0 += 32) {
-          uint32_t raw[32];
-          tc::tmem_ld32(base + c0, raw);
-          tc::tmem_wait_ld();
-          const int v0 = tile * p.N + c0, nv = a.V - v0;  // columns of this piece inside the vocabulary
-          if (nv <= 0) continue;
-          float z[32];
+      const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + ab * MAX_N + side * cols;
+      // 32 columns z of the tile: they begin at vocabulary row v0
+      auto piece = [&](uint32_t (&z)[32], int v0) {
+        const int nv = a.V - v0;
+        if (nv <= 0) return;
+        if (nv < 32) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = j < nv ? __uint_as_float(raw[j]) : -INFINITY;
-          float top = z[0];
+          for (int j = 0; j < 32; ++j)
+            if (j >= nv) z[j] = __float_as_uint(-1e30f);  // adds nothing to the sums
+        }
+        float top = __uint_as_float(z[0]);
 #pragma unroll
-          for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j]);
-          if (top > st.m) {
-            const float d = st.m - top, e = __expf(d);    // -inf on the first piece, whose sums are 0
-            st.u = st.s == 0.f ? 0.f : e * fmaf(st.s, d, st.u);
-            st.s *= e;
-            st.m = top;
-          }
-          float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+        for (int j = 1; j < 31; j += 2) top = fmaxf(fmaxf(top, __uint_as_float(z[j])), __uint_as_float(z[j + 1]));
+        top = fmaxf(top, __uint_as_float(z[31]));
+        if (top > st.m) {
+          const float d = st.m - top, e = __expf(d);      // -inf on the first piece, whose sums are 0
+          st.u = st.s == 0.f ? 0.f : e * fmaf(st.s, d, st.u);
+          st.s *= e;
+          st.m = top;
+        }
+        const u64 minus_m = pack_f32x2(-st.m, -st.m), log2e = pack_f32x2(LOG2E, LOG2E);
+        u64 s2 = 0ull, u2 = 0ull;                         // pairs of zeros
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float d0 = z[j] - st.m, d1 = z[j + 1] - st.m;
-            const float e0 = __expf(d0), e1 = __expf(d1);
-            s0 += e0; s1 += e1;
-            u0 = fmaf(e0, fmaxf(d0, -1000.f), u0);        // a masked column: 0 * -1000
-            u1 = fmaf(e1, fmaxf(d1, -1000.f), u1);
-          }
-          st.s += s0 + s1;
-          st.u += u0 + u1;
-          if (top > thr && b < a.B) {
+        for (int j = 0; j < 32; j += 2) {
+          const u64 d = add_f32x2(((u64)z[j + 1] << 32) | z[j], minus_m), t = mul_f32x2(d, log2e);
+          const u64 e = pack_f32x2(ex2(__uint_as_float((uint32_t)t)), ex2(__uint_as_float((uint32_t)(t >> 32))));
+          s2 = add_f32x2(s2, e);
+          u2 = fma_f32x2(e, d, u2);
+        }
+        st.s += __uint_as_float((uint32_t)s2) + __uint_as_float((uint32_t)(s2 >> 32));
+        st.u += __uint_as_float((uint32_t)u2) + __uint_as_float((uint32_t)(u2 >> 32));
+        if (top > list.v[TK - 1] && b < a.B) {
+#pragma unroll
+          for (int j0 = 0; j0 < 32; j0 += 16) {
             uint32_t cand = 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              zrow[j] = z[j];
-              if (z[j] > thr) cand |= 1u << j;
+            for (int j = 0; j < 16; ++j) {
+              zrow[j] = __uint_as_float(z[j0 + j]);
+              if (__uint_as_float(z[j0 + j]) > list.v[TK - 1]) cand |= 1u << j;
             }
+            if (nv < j0 + 16) cand &= nv > j0 ? (1u << (nv - j0)) - 1 : 0u;
             while (cand) {                                // ids ascend: an equal logit keeps the lower id
               const int j = __ffs(cand) - 1;
               cand &= cand - 1;
-              const float x = zrow[j];
-              if (x > thr) {
-                list_insert<TK>(L, argmax_key(x, (uint32_t)(v0 + j)));
-                if (L[TK - 1]) thr = float_from_order_bits((uint32_t)(L[TK - 1] >> 32));
-              }
+              list.insert(zrow[j], v0 + j0 + j);
             }
           }
+        }
+      };
+      if (rb * MROWS + q * 32 < a.B) {                    // a warp with rows (warp-uniform)
+        // the next 32 columns are on their way while these are worked on
+        uint32_t z0[32], z1[32];
+        const int first = tile * p.N + side * cols;
+        tc::tmem_ld32(base, z0);
+        for (int c0 = 0;; c0 += 64) {
+          tc::tmem_wait_ld();
+          if (c0 + 32 < cols) tc::tmem_ld32(base + c0 + 32, z1);
+          piece(z0, first + c0);
+          if (c0 + 32 >= cols) break;
+          tc::tmem_wait_ld();
+          if (c0 + 64 < cols) tc::tmem_ld32(base + c0 + 64, z0);
+          piece(z1, first + c0 + 32);
+          if (c0 + 64 >= cols) break;
         }
       }
       tc::fence_before_sync();
@@ -424,17 +487,15 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
       tile += p.splits;
       if (tile >= n_tiles) {                              // the row block's vocabulary is done
         if (b < a.B) {
-          const int64_t slot = (int64_t)b * p.splits + split;
+          const int64_t slot = (int64_t)b * a.splits + 2 * split + side;
           *reinterpret_cast<float4*>(a.part_stat + slot * 4) = make_float4(st.m, st.s, st.u, 0.f);
 #pragma unroll
-          for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = L[i];
+          for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = list.key(i);
         }
         tile = split;
         rb += p.group;
         st = Stat{-INFINITY, 0.f, 0.f};
-        thr = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < TK; ++i) L[i] = 0ull;
+        list.clear();
       }
     }
     if (!ok) {                                            // gave up: the rows of every pass are void
@@ -442,7 +503,7 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
       for (int ps = 0; ps < my_passes; ++ps) {
         const int b = (rb0 + ps * p.group) * MROWS + row;
         if (b >= a.B) continue;
-        const int64_t slot = (int64_t)b * p.splits + split;
+        const int64_t slot = (int64_t)b * a.splits + 2 * split + side;
         a.part_stat[slot * 4] = a.part_stat[slot * 4 + 1] = a.part_stat[slot * 4 + 2] = __uint_as_float(0x7fc00000u);
         for (int i = 0; i < TK; ++i) a.part_key[slot * TK + i] = 0ull;
       }
@@ -490,29 +551,28 @@ __device__ __forceinline__ void sum_two(float& s, float& c, float p) {
   c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z)));
   s = t;
 }
-// W[v] . h_b in about twice float32 precision (a warp; every lane gets the result).  The lanes join in
-// pairs of floats too: the GPU's float64 units are few.
+// W[v] . h in about twice float32 precision, as a pair (hi, lo) in every lane of the warp; h in shared
+// memory.  (The GPU has few float64 units: one row's sums in float64 took longer than its lists.)
 template <typename WT>
-__device__ __forceinline__ double dot_again(const LogprobArgs& a, int b, int v) {
+__device__ __forceinline__ float2 dot_again(const LogprobArgs& a, const float* h, int v) {
   const WT* w = reinterpret_cast<const WT*>(a.W) + (int64_t)v * a.H;
-  const int64_t hrow = (int64_t)b * a.H;
   float s = 0.f, c = 0.f;
   constexpr int AHEAD = 4;                                // 8-element pieces loaded before any is used
+#pragma unroll 1
   for (int k0 = (threadIdx.x & 31) * 8; k0 < a.H; k0 += 256 * AHEAD) {
-    float x[AHEAD][8], y[AHEAD][8];
+    float x[AHEAD][8];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (k0 + 256 * j < a.H) load8(w + k0 + 256 * j, x[j]);
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j)
       if (k0 + 256 * j < a.H) {
-        load8(w + k0 + 256 * j, x[j]);
-        hidden8(a, hrow + k0 + 256 * j, y[j]);
-      }
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (k0 + 256 * j < a.H) {
+        const float4 y0 = *reinterpret_cast<const float4*>(h + k0 + 256 * j), y1 = *reinterpret_cast<const float4*>(h + k0 + 256 * j + 4);
+        const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p = __fmul_rn(x[j][i], y[j][i]);
-          c = __fadd_rn(c, __fmaf_rn(x[j][i], y[j][i], -p));
+          const float p = __fmul_rn(x[j][i], y[i]);
+          c = __fadd_rn(c, __fmaf_rn(x[j][i], y[i], -p));
           sum_two(s, c, p);
         }
       }
@@ -520,27 +580,29 @@ __device__ __forceinline__ double dot_again(const LogprobArgs& a, int b, int v) 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float s2 = __shfl_xor_sync(FULL_MASK, s, o), c2 = __shfl_xor_sync(FULL_MASK, c, o);
-    const float lo = fminf(s, s2), hi = fmaxf(s, s2);   // both lanes of a pair add in one order
-    s = hi;
+    const float lo = fminf(s, s2);
+    s = fmaxf(s, s2);                                     // both lanes of a pair add in one order
     c = __fadd_rn(c, c2);
     sum_two(s, c, lo);
   }
-  return (double)s + (double)c;
+  const float hi = __fadd_rn(s, c);                       // |c| is far below |s|, or the sum is small: exact enough
+  return make_float2(hi, __fadd_rn(__fsub_rn(s, hi), c));
 }
 
 template <typename WT, int TK>
-__global__ void __launch_bounds__(MERGE_MAX)
+__global__ void __launch_bounds__(merge_max(TK))
 logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   static_assert(TK <= 32, "one lane per candidate");
-  __shared__ u64 s_w[MERGE_MAX_WARPS][TK];
+  extern __shared__ __align__(16) float s_h[];          // [H]
+  __shared__ u64 s_w[merge_max(TK) / 32][TK];
   __shared__ u64 s_top[TK];
-  __shared__ double s_val[TK + 1];
-  __shared__ Stat s_stat[MERGE_MAX_WARPS];
-  __shared__ double s_lse;
+  __shared__ float2 s_val[TK + 1];                      // logits scored again; [TK]: the given token's
+  __shared__ Stat s_stat[merge_max(TK) / 32];
   __shared__ int s_rank[TK];                            // candidate of each rank, -1: none
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
+  const int target = a.targets ? a.targets[b] : -1;
   Stat st{-INFINITY, 0.f, 0.f};
   u64 L[TK];
 #pragma unroll
@@ -556,73 +618,85 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
       L[2 * i] = two.x; L[2 * i + 1] = two.y;
     }
   }
-  st = stat_warp(st);
-  if (lane == 0) s_stat[warp] = st;
-  warp_merge<TK>(L, s_w[warp]);
-  const int target = a.targets ? a.targets[b] : -1;
-  if (warp == warps - 1) {                              // the given token waits for no list
-    const double d = target >= 0 && target < a.V ? dot_again<WT>(a, b, target) : 0.0;
-    if (lane == 0) s_val[TK] = d;
-  }
-  __syncthreads();
-  if (warp == 0) {
+  for (int k = tid; k < a.H; k += blockDim.x) s_h[k] = hidden_at(a, (int64_t)b * a.H + k);
+  // lists and statistics: within the warps, then (second round) those of the warps in warp 0
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    if (round == 1) {
+      if (warp == 0) {
 #pragma unroll
-    for (int i = 0; i < TK; ++i) L[i] = lane < warps ? s_w[lane][i] : 0ull;
-    warp_merge<TK>(L, s_top);
+        for (int i = 0; i < TK; ++i) L[i] = lane < warps ? s_w[lane][i] : 0ull;
+        st = lane < warps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f};
+      }
+    }
+    if (round == 0 || warp == 0) {
+      if (round == 1 || warp * 32 < a.splits) {
+        st = stat_warp(st);
+        warp_merge<TK>(L, round == 0 ? s_w[warp] : s_top);
+      } else if (lane < TK) {                           // a warp without splits
+        s_w[warp][lane] = 0ull;
+      }
+      if (round == 0 && lane == 0) s_stat[warp] = st;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   auto id_of = [&](int c) { return (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)); };
-  for (int c = warp; c < TK; c += warps) {
-    const double d = s_top[c] ? dot_again<WT>(a, b, id_of(c)) : 0.0;
+#pragma unroll 1
+  for (int c = warp; c <= TK; c += warps) {
+    const int v = c == TK ? target : (s_top[c] ? id_of(c) : -1);
+    float2 d = make_float2(0.f, 0.f);
+    if (v >= 0 && v < a.V) d = dot_again<WT>(a, s_h, v);
     if (lane == 0) s_val[c] = d;
   }
   if (tid < TK) s_rank[tid] = -1;
   __syncthreads();
   if (warp == 0) {
-    Stat all = s_stat[0];
-    for (int w = 1; w < warps; ++w) all = stat_join(all, s_stat[w]);
     // the candidates carry most of the sums: exchange their logits y for the ones scored again,
     // x = y + d with a small d, so exp(x) - exp(y) = exp(y) (d + d^2 / 2)
     float ds = 0.f, du = 0.f;
     if (lane < TK && s_top[lane]) {
-      const float z = float_from_order_bits((uint32_t)(s_top[lane] >> 32)), y = z - all.m;
-      const float d = (float)(s_val[lane] - (double)z), g = fmaf(0.5f * d, d, d), e = __expf(y);
+      const float z = float_from_order_bits((uint32_t)(s_top[lane] >> 32)), y = z - st.m;
+      const float2 x = s_val[lane];
+      const float d = (x.x - z) + x.y, g = fmaf(0.5f * d, d, d), e = __expf(y);
       ds = e * g;
       du = e * fmaf(g, y + d, d);
+      int rank = 0;
+#pragma unroll 4
+      for (int c = 0; c < TK; ++c) {
+        const float2 o = s_val[c];
+        const u64 key = s_top[c];
+        const bool above = o.x > x.x || (o.x == x.x && (o.y > x.y || (o.y == x.y && (uint32_t)key > (uint32_t)s_top[lane])));
+        rank += key != 0ull && above;
+      }
+      s_rank[rank] = lane;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       ds += __shfl_xor_sync(FULL_MASK, ds, o);
       du += __shfl_xor_sync(FULL_MASK, du, o);
     }
+    const float sum = st.s + ds, ls = logf(sum);
+    __syncwarp();
+    auto logprob = [&](float2 z) { return ((z.x - st.m) + z.y) - ls; };
     if (lane == 0) {
-      const float sum = all.s + ds, ls = logf(sum);
-      s_lse = (double)all.m + (double)ls;
-      if (a.out_lse) a.out_lse[b] = (float)s_lse;
-      if (a.out_entropy) a.out_entropy[b] = ls - (all.u + du) / sum;
+      if (a.out_lse) a.out_lse[b] = st.m + ls;
+      if (a.out_entropy) a.out_entropy[b] = ls - (st.u + du) / sum;
+      if (a.targets)
+        a.out_logprob[b] = target < 0 ? 0.f : (target < a.V ? logprob(s_val[TK]) : __uint_as_float(0x7fc00000u));
     }
-    if (lane < TK && s_top[lane]) {
-      int rank = 0;
-      for (int c = 0; c < TK; ++c)
-        if (s_top[c] && (s_val[c] > s_val[lane] || (s_val[c] == s_val[lane] && id_of(c) < id_of(lane)))) ++rank;
-      s_rank[rank] = lane;
+    if (lane < a.top_k) {
+      const int c = s_rank[lane];
+      const int64_t o = (int64_t)b * a.top_k + lane;
+      a.top_ids[o] = c < 0 ? -1 : id_of(c);
+      if (a.top_logprobs) a.top_logprobs[o] = c < 0 ? __uint_as_float(0x7fc00000u) : logprob(s_val[c]);
     }
-  }
-  __syncthreads();
-  if (tid == 0 && a.targets)
-    a.out_logprob[b] = target < 0 ? 0.f : (target < a.V ? (float)(s_val[TK] - s_lse) : __uint_as_float(0x7fc00000u));
-  if (tid < a.top_k) {
-    const int c = s_rank[tid];
-    const int64_t o = (int64_t)b * a.top_k + tid;
-    a.top_ids[o] = c < 0 ? -1 : id_of(c);
-    if (a.top_logprobs) a.top_logprobs[o] = c < 0 ? __uint_as_float(0x7fc00000u) : (float)(s_val[c] - s_lse);
   }
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Candidates kept for top_k alternatives: the rest is room for neighbours that rounding exchanges.
-int list_len(int top_k) { return top_k <= 4 ? 8 : (top_k <= 10 ? 16 : 32); }
+int list_len(int top_k) { return top_k <= 5 ? 8 : (top_k <= 8 ? 12 : (top_k <= 12 ? 16 : 32)); }
 
 constexpr int SMS = 152;                      // grids are sized for the whole GPU; fewer SMs only take longer
 int stream_splits(int B, int V) {
@@ -653,9 +727,11 @@ TcPlan tc_plan(int B, int V, int parts) {
   return p;
 }
 
-// One thread per split, at least 4 warps to share the second scoring (8 while the rows do not fill the GPU).
-int merge_threads(const LogprobArgs& a) {
-  return std::max((a.splits + 31) / 32 * 32, a.B <= 4 * SMS ? 256 : 128);
+// One thread per split; a warp for each token scored again while the rows do not fill the GPU, else 4.
+template <typename WT, int TK>
+cudaError_t launch_merge(const LogprobArgs& a, cudaStream_t s) {
+  const int threads = std::max((a.splits + 31) / 32 * 32, a.B <= SMS ? std::min(32 * (TK + 1), merge_max(TK)) : 128);
+  return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(threads), sizeof(float) * a.H, s, a);
 }
 
 template <int TK>
@@ -673,7 +749,7 @@ cudaError_t launch_tc(const LogprobArgs& a, const TcPlan& p, cudaStream_t s) {
   if ((e = make_map(&mh, p.parts == 2 ? (const void*)a.hb : a.h, a.H, a.B, p.parts, p.a_rows)) != cudaSuccess) return e;
   if ((e = launch_pdl(logprob_tc_kernel<TK>, dim3(p.group * p.splits), dim3(TC_THREADS), smem, s, a, p, mw, mh)) != cudaSuccess)
     return e;
-  return launch_pdl(logprob_merge_kernel<bf16_t, TK>, dim3(a.B), dim3(merge_threads(a)), 0, s, a);
+  return launch_merge<bf16_t, TK>(a, s);
 }
 
 template <typename WT, int TK>
@@ -688,7 +764,7 @@ cudaError_t launch_stream(const LogprobArgs& a, cudaStream_t s) {
   }
   cudaError_t e = launch_pdl(logprob_stream_kernel<WT, TK>, dim3(a.splits, (a.B + BG - 1) / BG), dim3(THREADS), smem, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(merge_threads(a)), 0, s, a);
+  return launch_merge<WT, TK>(a, s);
 }
 
 template <int TK>
@@ -702,7 +778,7 @@ cudaError_t launch_k(const LogprobArgs& a, kva_dtype w_dtype, const TcPlan* p, c
 // Workspace: [normalised rows, float32][bf16 halves][partial statistics][partial lists]
 size_t logprob_workspace_bytes(int B, int H, int V, int top_k) {
   int splits = stream_splits(B, V);
-  if (tc_supports(H)) splits = std::max(splits, tc_plan(B, V, 2).splits);
+  if (tc_supports(H)) splits = std::max(splits, 2 * tc_plan(B, V, 2).splits);
   const size_t parts = (size_t)B * splits;
   return 2 * up256(sizeof(float) * (size_t)B * H) + up256(parts * 16) + up256(parts * 8 * list_len(top_k));
 }
@@ -713,7 +789,7 @@ cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, c
   const bool split = a.h_dtype == KVA_F32 || a.norm_w;    // rows that need two bf16 halves
   TcPlan p{};
   if (tc) p = tc_plan(a.B, a.V, split ? 2 : 1);
-  a.splits = tc ? p.splits : stream_splits(a.B, a.V);
+  a.splits = tc ? 2 * p.splits : stream_splits(a.B, a.V);   // two column halves a CTA
   a.hn = reinterpret_cast<float*>(ws);
   ws += up256(sizeof(float) * (size_t)a.B * a.H);
   a.hb = tc && split ? reinterpret_cast<uint16_t*>(ws) : nullptr;
@@ -728,6 +804,7 @@ cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, c
   }
   switch (list_len(a.top_k)) {
     case 8: return launch_k<8>(a, w_dtype, tc ? &p : nullptr, s);
+    case 12: return launch_k<12>(a, w_dtype, tc ? &p : nullptr, s);
     case 16: return launch_k<16>(a, w_dtype, tc ? &p : nullptr, s);
     default: return launch_k<32>(a, w_dtype, tc ? &p : nullptr, s);
   }
