@@ -281,25 +281,6 @@ struct TopList {
   __device__ __forceinline__ u64 key(int i) const { return id[i] < 0 ? 0ull : argmax_key(v[i], (uint32_t)id[i]); }
 };
 
-// Two float32 operations an instruction.
-__device__ __forceinline__ u64 pack_f32x2(float lo, float hi) {
-  return ((u64)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
-__device__ __forceinline__ u64 add_f32x2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ u64 mul_f32x2(u64 a, u64 b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ u64 fma_f32x2(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -436,17 +417,17 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
           st.s *= e;
           st.m = top;
         }
-        const u64 minus_m = pack_f32x2(-st.m, -st.m), log2e = pack_f32x2(LOG2E, LOG2E);
-        u64 s2 = 0ull, u2 = 0ull;                         // pairs of zeros
+        const uint64_t minus_m = pack_f32x2(-st.m, -st.m), log2e = pack_f32x2(LOG2E, LOG2E);
+        uint64_t s2 = 0ull, u2 = 0ull;                         // pairs of zeros
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const u64 d = add_f32x2(((u64)z[j + 1] << 32) | z[j], minus_m), t = mul_f32x2(d, log2e);
-          const u64 e = pack_f32x2(ex2(__uint_as_float((uint32_t)t)), ex2(__uint_as_float((uint32_t)(t >> 32))));
+          const uint64_t d = add_f32x2(((uint64_t)z[j + 1] << 32) | z[j], minus_m), t = mul_f32x2(d, log2e);
+          const uint64_t e = pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t)));
           s2 = add_f32x2(s2, e);
           u2 = fma_f32x2(e, d, u2);
         }
-        st.s += __uint_as_float((uint32_t)s2) + __uint_as_float((uint32_t)(s2 >> 32));
-        st.u += __uint_as_float((uint32_t)u2) + __uint_as_float((uint32_t)(u2 >> 32));
+        st.s += f32x2_lo(s2) + f32x2_hi(s2);
+        st.u += f32x2_lo(u2) + f32x2_hi(u2);
         if (top > list.v[TK - 1] && b < a.B) {
 #pragma unroll
           for (int j0 = 0; j0 < 32; j0 += 16) {
