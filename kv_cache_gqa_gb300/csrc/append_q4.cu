@@ -2,15 +2,15 @@
 // (kv_cache_append_q4), and the expansion of listed slots into a bf16 or float32 cache
 // (kv_cache_expand_q4).  Layout and quantiser: kva_cache_q4 in kv_attn.h.
 //
-// Append: a CTA takes one token (few tokens: a part of its rows) or four, two warps each (long appends),
-// whose angles its threads evaluate once.  A q or K row of D values belongs to SW lanes of a warp (SW = 8,
-// 16 or 32 for rows up to 64, 128 or 256 wide), 8 consecutive values a lane, so the 64 values of a
+// Append: a CTA takes one token (few tokens: a part of its rows) or eight, a warp each (long appends), whose
+// angles its threads evaluate once.  A q or K row of D values belongs to SW lanes of a warp (SW = 8, 16
+// or 32 for rows up to 64, 128 or 256 wide), 8 consecutive values a lane, so the 64 values of a
 // quantisation group sit in 8 consecutive lanes: the group's minimum and maximum are three shuffles
 // each, a lane's 8 codes are one 32-bit word of the cache, and a group's first lane writes its scale and
-// midpoint.  V is only quantised, so a warp takes 4 of its groups whatever the row's width.  A warp loads
-// its next rows before it transforms the current ones; the cosines and sines of its dims stay in
-// registers.  A lane's 8 values rotate as one piece where the rotated range and its halves are multiples
-// of 8 dims.
+// midpoint.  V is only quantised, so a warp takes 4 of its groups whatever the row's width.  A warp walks
+// its q, K and V sets in order with two of them on their way; the cosines, sines and norm weights of its
+// dims stay in registers.  A lane's 8 values rotate as one piece where the rotated range and its
+// halves are multiples of 8 dims.
 //
 // A code is decided by a rounding, so a value that is off by an ulp of float32 becomes another code
 // once in about 10^6.  The float32 steps before it are therefore kept at one rounding each: squares
@@ -34,7 +34,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int TOKENS = 4;        // of a CTA in a long append
+constexpr int TOKENS = WARPS;    // of a CTA in a long append
 constexpr int MAX_D = 256;
 
 // Sum of squares of a row of D values in shared memory, by its SW lanes: strided sums l, l + 32, ... (the
@@ -156,16 +156,29 @@ __device__ __forceinline__ uint32_t quantise8(const uint64_t (&x)[4], uint32_t* 
   return w;
 }
 
-__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&x)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = pack_f32x2(a.x, a.y); x[1] = pack_f32x2(a.z, a.w);
-  x[2] = pack_f32x2(b.x, b.y); x[3] = pack_f32x2(b.z, b.w);
-}
-__device__ __forceinline__ void load_pairs(const bf16_t* p, uint64_t (&x)[4]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  x[0] = pack_f32x2(bf16_lo(a.x), bf16_hi(a.x)); x[1] = pack_f32x2(bf16_lo(a.y), bf16_hi(a.y));
-  x[2] = pack_f32x2(bf16_lo(a.z), bf16_hi(a.z)); x[3] = pack_f32x2(bf16_lo(a.w), bf16_hi(a.w));
-}
+// 8 elements as they lie in memory, and as four pairs of floats.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
+    x[0] = pack_f32x2(a.x, a.y); x[1] = pack_f32x2(a.z, a.w);
+    x[2] = pack_f32x2(b.x, b.y); x[3] = pack_f32x2(b.z, b.w);
+  }
+};
+template <> struct Raw<bf16_t> {
+  uint4 a;
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const bf16_t* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
+    x[0] = pack_f32x2(bf16_lo(a.x), bf16_hi(a.x)); x[1] = pack_f32x2(bf16_lo(a.y), bf16_hi(a.y));
+    x[2] = pack_f32x2(bf16_lo(a.z), bf16_hi(a.z)); x[3] = pack_f32x2(bf16_lo(a.w), bf16_hi(a.w));
+  }
+};
 // a b + c d of both elements, products and sum rounded apart
 __device__ __forceinline__ uint64_t sum_of_products(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
   return pack_f32x2(__fadd_rn(__fmul_rn(f32x2_lo(a), f32x2_lo(b)), __fmul_rn(f32x2_lo(c), f32x2_lo(d))),
@@ -198,40 +211,53 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
   const int Dk = a.c.Dk, Dv = a.c.Dv, Hkv = a.c.Hkv, Hq = a.q ? a.Hq : 0, Gk = Dk / Q4_GROUP, Gv = Dv / Q4_GROUP;
   const int ro = a.rot_offset, rw = a.rot_dim, half = rw / 2, kind_r = a.rope.kind;
   const bool rotate = kind_r != KVA_ROPE_NONE, norm = a.q_w != nullptr;
-  const int sets_q = (Hq + RPW - 1) / RPW, sets_k = (Hkv + RPW - 1) / RPW;
-  const int sets = sets_q + sets_k + (Hkv * Gv + 3) / 4;
   const int64_t tok = (int64_t)n * a.T + t;
   griddep_wait();                               // inputs of this launch are complete from here on
 
-  // set s: kind 0 q, 1 K (head, this lane's dims e0..), 2 V (head, group)
-  struct Where { int kind, head, group; bool on; };
-  auto where = [&](int s) {
-    Where w;
-    w.kind = s < sets_q ? 0 : (s < sets_q + sets_k ? 1 : 2);
+  // Sets of the token's rows: kind 0 q, 1 K (RPW heads, lanes by dims), 2 V (4 quantisation groups, lanes
+  // by groups).  This lane's unit in set i of a kind is unit0 + i * per, of `units`.
+  const int step = WPT * gridDim.z, start = blockIdx.z * WPT + warp % WPT;
+  const int sets_q = (Hq + RPW - 1) / RPW, sets_k = (Hkv + RPW - 1) / RPW, sets_v = (Hkv * Gv + 3) / 4;
+  auto units = [&](int kind) { return kind == 0 ? Hq : (kind == 1 ? Hkv : Hkv * Gv); };
+  auto sets = [&](int kind) { return kind == 0 ? sets_q : (kind == 1 ? sets_k : sets_v); };
+  const bool in_row = e0 < Dk;
+  // the walk that loads: kind, set, and this lane's unit and address in it
+  struct Walk { int kind, set, unit; const InT* p; };
+  auto enter = [&](Walk& w, int set) {          // the first set >= start of the walk's kind, or of a later one
+    w.set = set;
+    while (w.kind < 3 && w.set >= sets(w.kind)) { w.set -= sets(w.kind); ++w.kind; }
     if (w.kind == 2) {
-      const int item = (s - sets_q - sets_k) * 4 + (lane >> 3);
-      w.head = Gv == 1 ? item : (Gv == 2 ? item >> 1 : (Gv == 4 ? item >> 2 : item / 3));
-      w.group = item - w.head * Gv;
-      w.on = w.head < Hkv;
+      w.unit = w.set * 4 + (lane >> 3);
+      w.p = reinterpret_cast<const InT*>(a.v) + tok * Hkv * Dv + (int64_t)w.unit * Q4_GROUP + 8 * (lane & 7);
     } else {
-      w.head = (s - (w.kind ? sets_q : 0)) * RPW + sub;
-      w.group = sl >> 3;
-      w.on = w.head < (w.kind ? Hkv : Hq) && e0 < Dk;
+      w.unit = w.set * RPW + sub;
+      w.p = reinterpret_cast<const InT*>(w.kind ? a.k : a.q) + (tok * (w.kind ? Hkv : Hq) + w.unit) * Dk + e0;
     }
-    return w;
   };
-  auto load = [&](int s, uint64_t (&x)[4]) {
-    const Where w = where(s);
-    x[0] = x[1] = x[2] = x[3] = 0ull;                   // lanes past the heads or the row
-    if (!w.on) return;
-    if (w.kind == 2) load_pairs(reinterpret_cast<const InT*>(a.v) + (tok * Hkv + w.head) * Dv + Q4_GROUP * w.group + 8 * (lane & 7), x);
-    else if (w.kind == 1) load_pairs(reinterpret_cast<const InT*>(a.k) + (tok * Hkv + w.head) * Dk + e0, x);
-    else load_pairs(reinterpret_cast<const InT*>(a.q) + (tok * Hq + w.head) * Dk + e0, x);
+  auto fetch = [&](Walk& w, Raw<InT>& x) {      // the walk's set, then on to the next
+    x.zero();
+    if (w.kind > 2) return;
+    if (w.kind == 2) {
+      if (w.unit < units(2)) x.load(w.p);
+    } else if (in_row && w.unit < units(w.kind)) {
+      x.load(w.p);
+    }
+    w.set += step;
+    if (w.set < sets(w.kind)) {
+      const int by = step * (w.kind == 2 ? 4 : RPW);
+      w.unit += by;
+      w.p += by * (w.kind == 2 ? Q4_GROUP : Dk);
+    } else {
+      enter(w, w.set);
+    }
   };
-  const int step = WPT * gridDim.z;
-  int s = blockIdx.z * WPT + warp % WPT;
-  uint64_t x[4], next[4];
-  if (t < a.T && s < sets) load(s, x);
+  Walk walk{0, 0, 0, nullptr};
+  Raw<InT> ahead[2];
+  if (t < a.T) {
+    enter(walk, start);
+    fetch(walk, ahead[0]);
+    fetch(walk, ahead[1]);
+  }
   if (rotate)                                           // the angles, behind the first loads
     for (int j = tid; j < half * min(TOK, a.T - t0); j += THREADS) {
       const int tt = TOK == 1 ? 0 : j / half, f = j - tt * half;
@@ -239,11 +265,10 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
       rotation(p, a.rope.inv_hi[f], a.rope.inv_lo[f], a.rope.inv[f], &s_cos[tt][f], &s_sin[tt][f]);
     }
   __syncthreads();
-  if (t >= a.T || s >= sets) return;
+  if (t >= a.T) return;
 
   const int slot = a.slot[(int64_t)n * a.slot_stride + t];
   const bool in_cache = slot >= 0 && slot < a.c.capacity;
-  const int64_t row_n = (int64_t)n * a.c.inst_rows + slot;
   // this lane's angles and its partner piece (ALIGNED): outputs d0.. of the rotated range
   const int d0 = e0 - ro;
   const bool turns = rotate && d0 >= 0 && d0 < rw;
@@ -264,106 +289,107 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
     }
   }
   float* row = s_row[warp][sub];
-  auto apply_norm = [&](const Where& w) {               // the row is in shared memory
-    const float r = rsqrtf(__fadd_rn(__fmul_rn(sum_squares<SW>(row, Dk, sl), 1.0f / (float)Dk), a.eps));
-    if (!w.on) return;
-    uint64_t wv[4];
-    load_pairs((w.kind ? a.k_w : a.q_w) + (int64_t)n * a.w_stride + e0, wv);
-    const uint64_t r2 = pack_f32x2(r, r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(mul_f32x2(x[i], r2), wv[i]);
-  };
+  const float inv_d = 1.0f / (float)Dk;
+  uint64_t x[4] = {}, wv[4] = {};
   auto mirror = [&]() {
     reinterpret_cast<ulonglong2*>(row + e0)[0] = make_ulonglong2(x[0], x[1]);
     reinterpret_cast<ulonglong2*>(row + e0)[1] = make_ulonglong2(x[2], x[3]);
     __syncwarp();
   };
-
-  for (;;) {
-    const int ahead = s + step;
-    if (ahead < sets) load(ahead, next);
-    const Where w = where(s);
-    if (w.kind <= 1) {                                  // warp-uniform, as every branch around a shuffle
-      if (norm && !a.after_rope) {
-        mirror();
-        apply_norm(w);
-        __syncwarp();
-      }
-      if (rotate) {
-        mirror();
-        if (w.on) {
-          if constexpr (ALIGNED) {
-            if (turns) {
-              if (kind_r == KVA_ROPE_INTERLEAVED) {     // inputs 2 j0 .. 2 j0 + 15 are 8 pairs
-                float p[16];
+  auto apply_norm = [&]() {                             // the row is in shared memory
+    const float r = rsqrtf(__fadd_rn(__fmul_rn(sum_squares<SW>(row, Dk, sl), inv_d), a.eps));
+    const uint64_t r2 = pack_f32x2(r, r);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint64_t q[4];
-                  shared_pairs(row + partner + 8 * h, q);
+    for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(mul_f32x2(x[i], r2), wv[i]);
+    __syncwarp();                                       // buffer reads done before it is written again
+  };
+  auto turn = [&]() {
+    mirror();
+    if constexpr (ALIGNED) {
+      if (turns) {
+        if (kind_r == KVA_ROPE_INTERLEAVED) {           // inputs 2 j0 .. 2 j0 + 15 are 8 pairs
+          uint64_t q[8];
+          ulonglong2 two;
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) { p[8 * h + 2 * i] = f32x2_lo(q[i]); p[8 * h + 2 * i + 1] = f32x2_hi(q[i]); }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint64_t ev = pack_f32x2(p[4 * i], p[4 * i + 2]), od = pack_f32x2(p[4 * i + 1], p[4 * i + 3]);
-                  x[i] = sum_of_products(low ? ev : od, cs[i], low ? od : ev, sn[i]);
-                }
-              } else {
-                uint64_t p[4];
-                shared_pairs(row + partner, p);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = sum_of_products(x[i], cs[i], p[i], sn[i]);
-              }
-            }
-          } else {
-            float y[8];
-            unpack_pairs(x, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int dd = d0 + i;
-              if (dd < 0 || dd >= rw) continue;
-              const int bi = dd / block, d = dd - bi * block;
-              const bool lo = d < hb;
-              const int j = bi * hb + (lo ? d : d - hb);
-              const float c = s_cos[tl][j], v = lo ? -s_sin[tl][j] : s_sin[tl][j];
-              const bool inter = kind_r == KVA_ROPE_INTERLEAVED;
-              const float own = inter ? row[ro + 2 * j + (lo ? 0 : 1)] : y[i];
-              const float other = inter ? row[ro + 2 * j + (lo ? 1 : 0)] : row[ro + (lo ? dd + hb : dd - hb)];
-              y[i] = __fadd_rn(__fmul_rn(own, c), __fmul_rn(other, v));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = pack_f32x2(y[2 * i], y[2 * i + 1]);
+          for (int i = 0; i < 4; ++i) {
+            two = reinterpret_cast<const ulonglong2*>(row + partner)[i];
+            q[2 * i] = two.x; q[2 * i + 1] = two.y;
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t ev = pack_f32x2(f32x2_lo(q[2 * i]), f32x2_lo(q[2 * i + 1]));
+            const uint64_t od = pack_f32x2(f32x2_hi(q[2 * i]), f32x2_hi(q[2 * i + 1]));
+            x[i] = sum_of_products(low ? ev : od, cs[i], low ? od : ev, sn[i]);
+          }
+        } else {
+          uint64_t p[4];
+          shared_pairs(row + partner, p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = sum_of_products(x[i], cs[i], p[i], sn[i]);
         }
-        __syncwarp();                                   // buffer reads done before it is written again
-      }
-      if (norm && a.after_rope) {
-        mirror();
-        apply_norm(w);
-        __syncwarp();
-      }
-    }
-    if (w.kind == 0) {
-      if (w.on) {
-        float y[8];
-        unpack_pairs(x, y);
-        store8(reinterpret_cast<QOutT*>(a.q_out) + (tok * Hq + w.head) * Dk + e0, y);
       }
     } else {
-      uint32_t par;
-      const uint32_t word = quantise8(x, &par);         // every lane: shuffles
-      if (w.on && in_cache) {
-        const int G = w.kind == 1 ? Gk : Gv;
-        const int64_t gr = (row_n + (int64_t)w.head * a.c.capacity) * G + w.group;
-        const int64_t at = (row_n + (int64_t)w.head * a.c.capacity) * (8 * G) + (lane & 7) * G + w.group;
-        (w.kind == 1 ? a.c.k : a.c.v)[at] = word;
-        if ((lane & 7) == 0) (w.kind == 1 ? a.c.ks : a.c.vs)[gr] = par;
+      float y[8];
+      unpack_pairs(x, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int dd = d0 + i;
+        if (dd < 0 || dd >= rw) continue;
+        const int bi = dd / block, d = dd - bi * block;
+        const bool lo = d < hb;
+        const int j = bi * hb + (lo ? d : d - hb);
+        const float c = s_cos[tl][j], v = lo ? -s_sin[tl][j] : s_sin[tl][j];
+        const bool inter = kind_r == KVA_ROPE_INTERLEAVED;
+        const float own = inter ? row[ro + 2 * j + (lo ? 0 : 1)] : y[i];
+        const float other = inter ? row[ro + 2 * j + (lo ? 1 : 0)] : row[ro + (lo ? dd + hb : dd - hb)];
+        y[i] = __fadd_rn(__fmul_rn(own, c), __fmul_rn(other, v));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = pack_f32x2(y[2 * i], y[2 * i + 1]);
+    }
+    __syncwarp();
+  };
+
+  int set = start;                                      // runs on from kind to kind, as the walk does
+#pragma unroll
+  for (int kind = 0; kind < 3; ++kind) {
+    const bool qk = kind < 2;
+    const int G = kind == 1 ? Gk : Gv, per = qk ? RPW : 4;
+    if (norm && qk && in_row && set < sets(kind)) {
+      Raw<float> w;
+      w.load((kind ? a.k_w : a.q_w) + (int64_t)n * a.w_stride + e0);
+      w.pairs(wv);
+    }
+    int unit = set * per + (qk ? sub : lane >> 3);
+    for (; set < sets(kind); set += step, unit += step * per) {
+      ahead[0].pairs(x);
+      ahead[0] = ahead[1];
+      fetch(walk, ahead[1]);
+      const bool on = unit < units(kind) && (!qk || in_row);
+      if (qk) {
+        if (norm && !a.after_rope) { mirror(); apply_norm(); }
+        if (rotate) turn();
+        if (norm && a.after_rope) { mirror(); apply_norm(); }
+      }
+      if (kind == 0) {
+        if (on) {
+          float y[8];
+          unpack_pairs(x, y);
+          store8(reinterpret_cast<QOutT*>(a.q_out) + (tok * Hq + unit) * Dk + e0, y);
+        }
+      } else {
+        uint32_t par;
+        const uint32_t word = quantise8(x, &par);       // every lane: shuffles
+        const int head = qk ? unit : (G == 1 ? unit : (G == 2 ? unit >> 1 : (G == 4 ? unit >> 2 : unit / 3)));
+        const int group = qk ? sl >> 3 : unit - head * G;
+        if (on && in_cache) {
+          const int64_t at = ((int64_t)n * a.c.inst_rows + (int64_t)head * a.c.capacity + slot) * G + group;
+          (qk ? a.c.k : a.c.v)[8 * (at - group) + (lane & 7) * G + group] = word;
+          if ((lane & 7) == 0) (qk ? a.c.ks : a.c.vs)[at] = par;
+        }
       }
     }
-    if (ahead >= sets) break;
-    s = ahead;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = next[i];
+    set -= sets(kind);
   }
   // a long append must not have its SMs taken by a waiting persistent kernel
   griddep_launch_dependents();
@@ -449,7 +475,7 @@ cudaError_t launch_t(const AppendQ4Args& a, cudaStream_t s) {
   return launch_pdl(append_q4_kernel<InT, QOutT, 32, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
 }
 
-// Four tokens a CTA once that leaves four CTAs per SM.
+// A token per warp once that leaves four CTAs per SM.
 template <typename InT, typename QOutT, bool ALIGNED>
 cudaError_t launch_w(const AppendQ4Args& a, cudaStream_t s) {
   return (int64_t)a.T * a.N >= (int64_t)4 * TOKENS * num_sms_q4() ? launch_t<InT, QOutT, ALIGNED, TOKENS>(a, s)
