@@ -33,10 +33,14 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
 
+#ifndef DQ_C
+#define DQ_C 2048
+#endif
 namespace kva {
 
 namespace {
@@ -72,6 +76,26 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// N consecutive 32-bit words of shared memory at an address that is a multiple of 4 N bytes (of 16 at most; odd N: 4)
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p + 4 * i);
+      w[i] = q.x; w[i + 1] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+  }
+}
 // (lo, hi) - its float16 rounding h, as float16
 __device__ __forceinline__ uint32_t residual_f16x2(float lo, float hi, uint32_t h) {
   const float2 f = unpack_f16x2(h);
@@ -80,7 +104,7 @@ __device__ __forceinline__ uint32_t residual_f16x2(float lo, float hi, uint32_t 
 __device__ __forceinline__ float pow2(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 __device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u); }
 
-template <int DK, int DV, int MODE>
+template <int DK, int DV, int MODE, bool SPLITQ>
 struct Shape {
   static constexpr int GK = DK / Q4_GROUP, GV = DV / Q4_GROUP;
   static constexpr int NB = MODE == 2 ? 2 : 1;              // 8-column blocks of query rows
@@ -89,18 +113,20 @@ struct Shape {
   static constexpr int STAGE = KC + VC + KP + VP;
   static constexpr int RING = NS * STAGE;
   static constexpr int MERGE = WARPS * ROWS * (DV + 2) * 4;
-  static constexpr int SMEM = (WARPS * RING > MERGE ? WARPS * RING : MERGE) + WARPS * NS * 8;
-  static constexpr int CTAS = MODE == 2 ? 3 : 4;            // resident per SM
+  static constexpr int QP = MODE != 0 && SPLITQ ? 2 : 1;    // products per K fragment and block
+  static constexpr int QF = MODE == 2 ? NB * QP * GK * 4 * 256 : 0;   // query fragments held in shared memory
+  static constexpr int BAR = (WARPS * RING > MERGE ? WARPS * RING : MERGE) + QF;
+  static constexpr int SMEM = BAR + WARPS * NS * 8;
+  static constexpr int CTAS = MODE == 0 && DK <= 128 ? 4 : 3;   // resident per SM, for the register limit
 };
 
 // MODE 0: up to 4 rows, halves side by side in the 8 columns; 1: 8 rows; 2: 16 rows.
 // SPLITQ: float32 queries (two halves); else bf16 (exact in one).
 template <int DK, int DV, int MODE, bool SPLITQ>
-__global__ void __launch_bounds__(THREADS, (Shape<DK, DV, MODE>::CTAS))
+__global__ void __launch_bounds__(THREADS, (Shape<DK, DV, MODE, SPLITQ>::CTAS))
 decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
-  using S = Shape<DK, DV, MODE>;
-  constexpr int GK = S::GK, GV = S::GV, NB = S::NB, ROWS = S::ROWS;
-  constexpr int QP = MODE != 0 && SPLITQ ? 2 : 1;           // products per K fragment and block
+  using S = Shape<DK, DV, MODE, SPLITQ>;
+  constexpr int GK = S::GK, GV = S::GV, NB = S::NB, ROWS = S::ROWS, QP = S::QP;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_M[ROWS], s_L[ROWS];
   __shared__ int s_last;
@@ -108,7 +134,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
   const int G = a.Hq / a.c.Hkv, n_rows = G * a.T;
   unsigned char* ring = smem + warp * S::RING;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::SMEM - WARPS * NS * 8) + warp * NS;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::BAR) + warp * NS;
   if (lane == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&bar[s], 1);
     fence_mbar_init();
@@ -154,7 +180,9 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 
   // ---- query fragments: column r of block nb, dims 64 gk + 16 t + 0..15 ----
   // word j (8 dims) of group gk gives two MMAs h = 0, 1 with b0 = dims (2h, 2h + 4), b1 = (2h + 1, 2h + 5)
-  uint32_t qf[NB][QP][GK][2][2][2];
+  // (16 rows: in shared memory, written by warp 0)
+  uint32_t qf[MODE == 2 ? 1 : NB][QP][GK][2][2][2];
+  uint2* s_qf = reinterpret_cast<uint2*>(smem + S::BAR - S::QF) + lane;
   float qs[NB][GK][2], qf_scale[NB][2];         // of the S^T columns 2t, 2t + 1
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -190,20 +218,27 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t f[QP][2];
 #pragma unroll
           for (int o = 0; o < 2; ++o) {         // the odd nibble counts 16 times the even one
             const int d = 8 * j + 2 * h + o;
-            const float f = o ? up * 0.0625f : up;
-            const float y0 = x[gk][d] * f, y1 = x[gk][d + 4] * f;
+            const float by = o ? up * 0.0625f : up;
+            const float y0 = x[gk][d] * by, y1 = x[gk][d + 4] * by;
             const uint32_t hi = pack_f16x2(y0, y1);
-            if constexpr (MODE == 0) {
-              qf[nb][0][gk][j][h][o] = SPLITQ && r >= 4 ? residual_f16x2(y0, y1, hi) : hi;
+            f[0][o] = MODE == 0 && SPLITQ && r >= 4 ? residual_f16x2(y0, y1, hi) : hi;
+            if constexpr (QP == 2) f[1][o] = residual_f16x2(y0, y1, hi);
+          }
+#pragma unroll
+          for (int p = 0; p < QP; ++p) {
+            if constexpr (MODE == 2) {
+              if (warp == 0) s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)] = make_uint2(f[p][0], f[p][1]);
             } else {
-              qf[nb][0][gk][j][h][o] = hi;
-              if constexpr (SPLITQ) qf[nb][1][gk][j][h][o] = residual_f16x2(y0, y1, hi);
+              qf[nb][p][gk][j][h][0] = f[p][0];
+              qf[nb][p][gk][j][h][1] = f[p][1];
             }
           }
+        }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int src = 4 * (2 * t + i);          // any lane of column 2t + i
@@ -213,6 +248,8 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
         qs[nb][gk][i] = __shfl_sync(FULL_MASK, sum[gk] * (up * 5.9604644775390625e-8f), src);
     }
   }
+
+  if constexpr (MODE == 2) __syncthreads();
 
   int lim[NB][2];                               // slots that the columns' tokens see
 #pragma unroll
@@ -225,7 +262,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   const int lim_all = min(L - a.T + (rt * ROWS) / G + 1, k1);   // slots that every column sees
 
   float o[NB][GV][4][4];                        // value dims 64 gv + 8 r + i (and + 4), columns 2t, 2t + 1
-  float om[NB][GV][2], m[NB][2], l[NB][2], vtop[GV], vmul[GV];
+  float om[NB][GV][2], m[NB][2], thr[NB][2], l[NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -234,11 +271,11 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       for (int i = 0; i < 4; ++i) o[nb][gv][i][0] = o[nb][gv][i][1] = o[nb][gv][i][2] = o[nb][gv][i][3] = 0.f;
       om[nb][gv][0] = om[nb][gv][1] = 0.f;
     }
-    m[nb][0] = m[nb][1] = M_NONE;
+    m[nb][0] = m[nb][1] = M_NONE;               // reference maximum, log2 units
+    thr[nb][0] = thr[nb][1] = -INFINITY;        // (m + RESCALE_LOG2) in units of the raw score
     l[nb][0] = l[nb][1] = 0.f;
   }
-#pragma unroll
-  for (int gv = 0; gv < GV; ++gv) { vtop[gv] = 0.f; vmul[gv] = 0.f; }
+  float vtop = 0.f, vmul = 0.f;                 // power of two above every V scale so far; weights carry vmul = 2^6 / vtop
   bool ok = true;
   int done = 0;                                 // stages consumed
 
@@ -247,228 +284,223 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   // shared-memory banks
   const int kr = r ^ ((r >> 1) & 1);            // sigma(r); rows r + 8: + 8
   const int kv0 = (2 * t) ^ (t & 1), kv1 = (2 * t + 1) ^ (t & 1);
+  const int k_at = kr * (DK / 2) + t * (DK / 8), kp_at = S::KC + S::VC + kr * (GK * 4);
+  const int v0_at = S::KC + kv0 * (DV / 2) + r * (GV * 4), v1_at = S::KC + kv1 * (DV / 2) + r * (GV * 4);
+  const int vp_at = S::KC + S::VC + S::KP + kr * (GV * 4);
+  [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on the second halves of the weights
 
-  for (int u = 0; u < n_mine; done = ++u) {
-    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[u % NS], (uint32_t)((u / NS) & 1)))) { ok = false; break; }
-    const unsigned char* stg = ring + (u % NS) * S::STAGE;
-    const int ks = (st0 + warp + u * WARPS) * SK;
-#pragma unroll 1
-    for (int tt = 0; tt < SK / 16; ++tt) {
-      const int kb = ks + 16 * tt;
-      if (kb >= k1) break;                      // warp-uniform
-      // ---- S^T ----
-      float d[NB][GK][4];
+  // One 16-key tile of a stage; kb: its first key.  TAIL: some key is hidden from some column.
+  auto tile = [&](auto tail, const unsigned char* stg, int tt, int kb) {
+    constexpr bool TAIL = decltype(tail)::value;
+    // ---- S^T ----
+    float d[NB][GK][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int gk = 0; gk < GK; ++gk) d[nb][gk][0] = d[nb][gk][1] = d[nb][gk][2] = d[nb][gk][3] = 0.f;
-      const unsigned char* pk = stg + (16 * tt + kr) * (DK / 2) + t * (DK / 8);
-      uint32_t wk[2][2 * GK];
+      for (int gk = 0; gk < GK; ++gk) d[nb][gk][0] = d[nb][gk][1] = d[nb][gk][2] = d[nb][gk][3] = 0.f;
+    uint32_t wk[2][2 * GK], kp[2][GK];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        if constexpr (GK == 2) {
-          const uint4 q4 = *reinterpret_cast<const uint4*>(pk + hh * 8 * (DK / 2));
-          wk[hh][0] = q4.x; wk[hh][1] = q4.y; wk[hh][2] = q4.z; wk[hh][3] = q4.w;
-        } else {
+    for (int hh = 0; hh < 2; ++hh) {
+      load_words(stg + k_at + (16 * tt + 8 * hh) * (DK / 2), wk[hh]);
+      load_words(stg + kp_at + (16 * tt + 8 * hh) * (GK * 4), kp[hh]);
+    }
 #pragma unroll
-          for (int i = 0; i < GK; ++i) {
-            const uint2 q2 = *reinterpret_cast<const uint2*>(pk + hh * 8 * (DK / 2) + 8 * i);
-            wk[hh][2 * i] = q2.x; wk[hh][2 * i + 1] = q2.y;
-          }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int gk = 0; gk < GK; ++gk) {
+        uint32_t x = wk[0][j * GK + gk], y = wk[1][j * GK + gk];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = x & 0x000f000fu, a1 = y & 0x000f000fu, a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int p = 0; p < QP; ++p) {
+              uint2 q;
+              if constexpr (MODE == 2) q = s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)];
+              else q = make_uint2(qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
+              mma16816(d[nb][gk], a0, a1, a2, a3, q.x, q.y);
+            }
+          x >>= 8; y >>= 8;
         }
       }
+    // ---- scale and midpoint of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1 ----
+    float s[NB][4];
+    {
+      float sp[NB][4], sc[NB][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int gk = 0; gk < GK; ++gk) {
-          uint32_t x = wk[0][j * GK + gk], y = wk[1][j * GK + gk];
+          const float scale = bf16_lo(kp[hh][gk]), off = fmaf(-8.f, scale, bf16_hi(kp[hh][gk]));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = x & 0x000f000fu, a1 = y & 0x000f000fu, a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int p = 0; p < QP; ++p) mma16816(d[nb][gk], a0, a1, a2, a3, qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
-            x >>= 8; y >>= 8;
-          }
-        }
-      // ---- scale and midpoint of keys kr (i = 0, 1) and kr + 8 (i = 2, 3); columns 2t, 2t + 1 ----
-      float s[NB][4];
-      {
-        float sp[NB][4], sc[NB][4];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t* pp = reinterpret_cast<const uint32_t*>(stg + S::KC + S::VC) + (16 * tt + kr + 8 * hh) * GK;
-#pragma unroll
-          for (int gk = 0; gk < GK; ++gk) {
-            const uint32_t w = pp[gk];
-            const float scale = bf16_lo(w), off = fmaf(-8.f, scale, bf16_hi(w));
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int e = 2 * hh + i;
-                sp[nb][e] = gk == 0 ? scale * d[nb][gk][e] : fmaf(scale, d[nb][gk][e], sp[nb][e]);
-                sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
-              }
-          }
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
-            s[nb][e] = (sp[nb][e] + sc[nb][e]) * qf_scale[nb][e & 1];
-          }
-      }
-      const bool tail = kb + 16 > lim_all;
-      if (tail) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (kb + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[nb][e] = -INFINITY;
-      }
-      // ---- online softmax ----
-      bool grow = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) grow |= fmaxf(s[nb][i], s[nb][2 + i]) > m[nb][i] + RESCALE_LOG2;
-      if (__any_sync(FULL_MASK, grow)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float mt = fmaxf(s[nb][i], s[nb][2 + i]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
-            if (mt > m[nb][i] + RESCALE_LOG2) {           // uniform over the column's lanes
-              const float alpha = ex2(m[nb][i] - mt);
-              m[nb][i] = mt;
-              l[nb][i] *= alpha;
-#pragma unroll
-              for (int gv = 0; gv < GV; ++gv) {
-                om[nb][gv][i] *= alpha;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) { o[nb][gv][k][i] *= alpha; o[nb][gv][k][2 + i] *= alpha; }
-              }
+            for (int i = 0; i < 2; ++i) {
+              const int e = 2 * hh + i;
+              sp[nb][e] = gk == 0 ? scale * d[nb][gk][e] : fmaf(scale, d[nb][gk][e], sp[nb][e]);
+              sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
             }
-          }
-      }
-      float p[NB][4];
+        }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[nb][e] = ex2(s[nb][e] - m[nb][e & 1]);
-          l[nb][e & 1] += p[nb][e];
+          if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
+          s[nb][e] = sp[nb][e] + sc[nb][e];             // times qf_scale: log2 units
         }
-      // ---- weights p * scale of V, per group ----
-      float vs[GV][2], vm[GV][2];
-      bool wide = false;
+    }
+    if constexpr (TAIL) {
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t* pp = reinterpret_cast<const uint32_t*>(stg + S::KC + S::VC + S::KP) + (16 * tt + kr + 8 * hh) * GV;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int gv = 0; gv < GV; ++gv) {
-          uint32_t w = pp[gv];
-          if (tail && kb + kr + 8 * hh >= k1) w = 0u;     // slots past the chunk may hold anything
-          vs[gv][hh] = bf16_lo(w); vm[gv][hh] = bf16_hi(w);
-          wide |= vs[gv][hh] > vtop[gv];
-        }
-      }
-      if (__any_sync(FULL_MASK, wide)) {                  // a larger scale than any before: follow it
+        for (int e = 0; e < 4; ++e)
+          if (kb + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[nb][e] = -INFINITY;
+    }
+    // ---- scales of V ----
+    uint32_t vp[2][GV];
+    float top = 0.f;
 #pragma unroll
-        for (int gv = 0; gv < GV; ++gv) {
-          float top = fmaxf(vs[gv][0], vs[gv][1]);
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
-          if (top > vtop[gv]) {
-            const int e = max(exponent(top) + 1, 40);     // top < 2^(e-127) (or tiny)
-            vtop[gv] = pow2(min(e, 254));
-            const float now = pow2(127 - (e - 127) + 6);  // weights reach 2^8 * 2^6
-            const float ratio = vmul[gv] == 0.f ? 0.f : now / vmul[gv];
-            vmul[gv] = now;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) o[nb][gv][k][x] *= ratio;
-          }
-        }
-      }
-      uint32_t bh[NB][GV][2], bl[NB][GV][2];              // operand fragments: keys 2t, 2t + 1 (and + 8), column r
-#pragma unroll
-      for (int gv = 0; gv < GV; ++gv)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float mul = vs[gv][hh] * vmul[gv];
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float w0 = p[nb][2 * hh] * mul, w1 = p[nb][2 * hh + 1] * mul;
-            float z0 = p[nb][2 * hh] * vm[gv][hh], z1 = p[nb][2 * hh + 1] * vm[gv][hh];
-            if (tail) {                                   // a hidden key's values may be NaN: no 0 * NaN
-              if (s[nb][2 * hh] == -INFINITY) w0 = z0 = 0.f;
-              if (s[nb][2 * hh + 1] == -INFINITY) w1 = z1 = 0.f;
-            }
-            om[nb][gv][0] += z0;
-            om[nb][gv][1] += z1;
-            const uint32_t hi = pack_f16x2(w0, w1), lo = residual_f16x2(w0, w1, hi);
-            if constexpr (MODE == 0) {
-              bh[nb][gv][hh] = transpose8x8(t >= 2 ? lo : hi);
-            } else {
-              bh[nb][gv][hh] = transpose8x8(hi);
-              bl[nb][gv][hh] = transpose8x8(lo);
-            }
-          }
-        }
-      // ---- O^T += V^T P ----
-      const unsigned char* pv = stg + S::KC + 16 * tt * (DV / 2) + r * (GV * 4);
-      uint32_t wv[4][GV];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const unsigned char* q = pv + ((k & 1 ? kv1 : kv0) + (k & 2 ? 8 : 0)) * (DV / 2);
-        if constexpr (GV == 2) {
-          const uint2 q2 = *reinterpret_cast<const uint2*>(q);
-          wv[k][0] = q2.x; wv[k][1] = q2.y;
-        } else {
-          wv[k][0] = *reinterpret_cast<const uint32_t*>(q);
-        }
-      }
+    for (int hh = 0; hh < 2; ++hh) {
+      load_words(stg + vp_at + (16 * tt + 8 * hh) * (GV * 4), vp[hh]);
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv) {
-        const uint32_t x0 = __byte_perm(wv[0][gv], wv[1][gv], 0x5410), y0 = __byte_perm(wv[0][gv], wv[1][gv], 0x7632);
-        const uint32_t x1 = __byte_perm(wv[2][gv], wv[3][gv], 0x5410), y1 = __byte_perm(wv[2][gv], wv[3][gv], 0x7632);
+        if (TAIL && kb + kr + 8 * hh >= k1) vp[hh][gv] = 0u;    // slots past the chunk may hold anything
+        top = fmaxf(top, bf16_lo(vp[hh][gv]));
+      }
+    }
+    // ---- online softmax: move the references when a score or a scale outgrows them (rare) ----
+    bool grow = top > vtop;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
-          // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
-          auto code = [&](uint32_t v) { return (i == 0 ? v << 4 : v >> (4 * (i > 0 ? i - 1 : 0))) & 0x00f000f0u; };
-          constexpr uint32_t eight = 0x80808080u;                     // -8 2^-20, twice
-          uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
-          if constexpr (MODE == 0) {
-            mma16816(o[0][gv][i], a0, a1, a2, a3, bh[0][gv][0], bh[0][gv][1]);
-            mma16816(o[0][gv][i], eight, eight, eight, eight, bh[0][gv][0], bh[0][gv][1]);
-          } else {
-            const __half2 e2 = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));
-            auto centre = [&](uint32_t v) {
-              const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), e2);
-              return *reinterpret_cast<const uint32_t*>(&z);
-            };
-            a0 = centre(a0); a1 = centre(a1); a2 = centre(a2); a3 = centre(a3);
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
-              mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
+      for (int i = 0; i < 2; ++i) grow |= fmaxf(s[nb][i], s[nb][2 + i]) > thr[nb][i];
+    if (__any_sync(FULL_MASK, grow)) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
+      float ratio = 1.f;
+      if (top > vtop) {
+        const int e = max(exponent(top) + 1, 40);       // top < 2^(e-127) (or tiny)
+        const float now = pow2(260 - e);                // weights reach 2^8 * 2^6
+        vtop = pow2(min(e, 254));
+        ratio = vmul == 0.f ? 0.f : now / vmul;
+        vmul = now;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mt = fmaxf(s[nb][i], s[nb][2 + i]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
+          float alpha = 1.f;
+          if (mt > thr[nb][i]) {                        // uniform over the column's lanes
+            mt *= qf_scale[nb][i];
+            alpha = ex2(m[nb][i] - mt);
+            m[nb][i] = mt;
+            thr[nb][i] = (mt + RESCALE_LOG2) / qf_scale[nb][i];
+            l[nb][i] *= alpha;
+          }
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv) {
+            om[nb][gv][i] *= alpha;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { o[nb][gv][k][i] *= alpha * ratio; o[nb][gv][k][2 + i] *= alpha * ratio; }
+          }
+        }
+    }
+    float p[NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[nb][e] = ex2(fmaf(s[nb][e], qf_scale[nb][e & 1], -m[nb][e & 1]));
+        l[nb][e & 1] += p[nb][e];
+      }
+    // ---- weights p * scale of V, per group: operand fragments of keys 2t, 2t + 1 (and + 8), column r ----
+    uint32_t bh[NB][GV][2];
+    [[maybe_unused]] uint32_t bl[NB][GV][2];
+#pragma unroll
+    for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const float mul = bf16_lo(vp[hh][gv]) * vmul, mid = bf16_hi(vp[hh][gv]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float pi = p[nb][2 * hh + i];
+            w[i] = pi * mul;
+            if constexpr (TAIL) {                       // a hidden key's values may be NaN: no 0 * NaN
+              const bool hidden = s[nb][2 * hh + i] == -INFINITY;
+              if (hidden) w[i] = 0.f;
+              om[nb][gv][i] += hidden ? 0.f : pi * mid;
+            } else {
+              om[nb][gv][i] = fmaf(pi, mid, om[nb][gv][i]);
             }
+          }
+          const uint32_t hi = pack_f16x2(w[0], w[1]);
+          const float2 f = unpack_f16x2(hi);
+          if constexpr (MODE == 0) {                    // lanes t < 2: the first halves; t >= 2: what they leave
+            bh[nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
+          } else {
+            bh[nb][gv][hh] = transpose8x8(hi);
+            bl[nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
+          }
+        }
+      }
+    // ---- O^T += V^T P ----
+    uint32_t wv[4][GV];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_words(stg + (k & 1 ? v1_at : v0_at) + (16 * tt + (k & 2 ? 8 : 0)) * (DV / 2), wv[k]);
+#pragma unroll
+    for (int gv = 0; gv < GV; ++gv) {
+      const uint32_t x0 = __byte_perm(wv[0][gv], wv[1][gv], 0x5410), y0 = __byte_perm(wv[0][gv], wv[1][gv], 0x7632);
+      const uint32_t x1 = __byte_perm(wv[2][gv], wv[3][gv], 0x5410), y1 = __byte_perm(wv[2][gv], wv[3][gv], 0x7632);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
+        // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
+        auto code = [&](uint32_t v) { return (i == 0 ? v * 16u : v >> (4 * (i > 0 ? i - 1 : 0))) & 0x00f000f0u; };
+        constexpr uint32_t eight = 0x80808080u;                     // -8 2^-20, twice
+        uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
+        if constexpr (MODE == 0) {
+          mma16816(o[0][gv][i], a0, a1, a2, a3, bh[0][gv][0], bh[0][gv][1]);
+          mma16816(o[0][gv][i], eight, eight, eight, eight, bh[0][gv][0], bh[0][gv][1]);
+        } else {
+          const __half2 e2 = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));
+          auto centre = [&](uint32_t v) {
+            const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), e2);
+            return *reinterpret_cast<const uint32_t*>(&z);
+          };
+          a0 = centre(a0); a1 = centre(a1); a2 = centre(a2); a3 = centre(a3);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
+            mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
           }
         }
       }
     }
+  };
+
+  int slot = 0;                                 // ring position of stage u
+  uint32_t phase = 0;
+  for (int u = 0; u < n_mine; done = ++u) {
+    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) { ok = false; break; }
+    const unsigned char* stg = ring + slot * S::STAGE;
+    const int ks = (st0 + warp + u * WARPS) * SK;
+    if (ks + SK <= lim_all) {
+#pragma unroll
+      for (int tt = 0; tt < SK / 16; ++tt) tile(std::false_type{}, stg, tt, ks + 16 * tt);
+    } else {
+#pragma unroll 1
+      for (int tt = 0; tt < SK / 16 && ks + 16 * tt < k1; ++tt) tile(std::true_type{}, stg, tt, ks + 16 * tt);
+    }
     __syncwarp();                               // all lanes are done with this stage
     if (lane == 0 && u + NS < n_mine) issue(u + NS);
+    if (++slot == NS) { slot = 0; phase ^= 1; }
   }
   if (!ok)                                      // gave up: the copies still in flight land first (bounded)
     for (int u = done; u < n_mine && u < done + NS; ++u) (void)mbar_wait_bounded(&bar[u % NS], (uint32_t)((u / NS) & 1));
@@ -499,7 +531,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       }
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv) {
-        const float inv = vmul[gv] == 0.f ? 0.f : 1.0f / vmul[gv];
+        const float inv = vmul == 0.f ? 0.f : 1.0f / vmul;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           constexpr float unit = 1048576.f;                     // 1 / the code's subnormal step
@@ -567,7 +599,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 
 template <int DK, int DV, int MODE, bool SPLITQ>
 cudaError_t launch_m(const DecodeQ4Args& a, cudaStream_t s) {
-  constexpr int smem = Shape<DK, DV, MODE>::SMEM;
+  constexpr int smem = Shape<DK, DV, MODE, SPLITQ>::SMEM;
   static DeviceOnce configured;
   if (!configured.done()) {
     cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<DK, DV, MODE, SPLITQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -605,8 +637,8 @@ int decode_q4_plan_chunk(const int32_t* lengths, int B, int units, int max_len, 
   for (int b = 0; b < B; ++b) keys += lengths[b];
   const int floor_chunk = (max_len + max_chunks - 1) / max_chunks;
   int64_t chunk = std::max<int64_t>(floor_chunk, keys * units / slots);
-  chunk = std::min<int64_t>(std::max<int64_t>((chunk + STEP - 1) / STEP, 1) * STEP, std::max(1024, (floor_chunk + STEP - 1) / STEP * STEP));
-  while (chunk < 1024) {
+  chunk = std::min<int64_t>(std::max<int64_t>((chunk + STEP - 1) / STEP, 1) * STEP, std::max(DQ_C, (floor_chunk + STEP - 1) / STEP * STEP));
+  while (chunk < DQ_C) {
     int64_t ctas = 0;
     for (int b = 0; b < B; ++b) ctas += (lengths[b] + chunk - 1) / chunk;
     if (ctas * units <= slots) break;
