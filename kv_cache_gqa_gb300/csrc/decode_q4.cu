@@ -1,10 +1,15 @@
 // Attention of new tokens over a 4-bit cache (kv_attn_decode_q4): split-KV, the codes fed to the
 // tensor cores as they are.
 //
-// Work unit = (chunk c, KV head g and tile of query rows, instance b).  The query rows of a group
-// are (token i, head j) -> i * G + j, 4, 8 or 16 a CTA.  A CTA's 4 warps are independent: warp w takes
-// the 32-key stages w, w+4, ... of the chunk through a private ring, filled by 1-D bulk copies (a
-// head's codes and scales are contiguous in the cache).  Per 16 keys:
+// Work unit = (KV head g and tile of query rows, instance b): a walk over the instance's keys in stages
+// of 32.  The query rows of a group are (token i, head j) -> i * G + j, 4, 8 or 16 a unit.  The stages of
+// all units, in order, are cut into one equal run per CTA, as many CTAs as the GPU holds at once: a
+// CTA ends one unit, takes whole ones and begins the next, so that ragged contexts leave no tail and a
+// single long one still fills the GPU.  (Equal chunks of up to 2048 keys, one CTA each, took 64 ragged
+// sequences 282 us.)  A unit that several CTAs share is joined by the last of them to finish.  The runs
+// follow from the lengths on the device: every CTA sums them itself.
+//   A CTA's 4 warps are independent: warp w takes the stages w, w+4, ... of a run through a private ring,
+// filled by 1-D bulk copies (a head's codes and scales are contiguous in the cache).  Per 16 keys:
 //   S^T = K q^T   keys are the 16 rows of the MMA, query rows its 8 columns.  A 4-bit code u taken
 //                 out of a word by one AND is the float16 subnormal u 2^-24 (or u 2^-20 for the odd
 //                 nibble; V shifts every code there), so K needs 5 instructions per 8 codes; q is scaled by a power of two per
@@ -15,17 +20,19 @@
 //                 more than 2^8, float32
 //   O^T += V^T P  value dims are the MMA's rows, keys its K axis.  The weights p * scale_g, two
 //                 float16 halves (22 bits) against a power of two that follows the largest scale,
-//                 turn from S^T's layout to the operand layout with movmatrix.  The codes' centre
-//                 (u - 8) is taken off by a second product with a constant -8, or in the operand:
-//                 without it O would be the small difference of sums of positive codes.
+//                 turn from S^T's layout to the operand layout with movmatrix.  The codes are
+//                 centred (u - 8) in the operand: else O would be the small difference of sums of
+//                 positive codes.  (Centred by a second product with a constant -8 instead: 3-5%
+//                 slower.)
 //                 mid enters as sum p mid_g in float32.
 // With at most 4 query rows the two halves of the weights (and of q) share the 8 columns.  The
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
 // a lane's codes of K, and of V, are adjacent bytes.
 //
-// Bound: HBM, 144 bytes per key and KV head at D = 128; issue slots come second (about 250 warp
-// instructions per 16 keys, 65% of the slots at full bandwidth), then mma.sync (24 per 16 keys; a
-// measured 1.05 ns each per SM, half of the time).
+// Bound: the instruction mix.  HBM would allow a 16-key tile (2304 bytes at D = 128) per SM every 52 ns;
+// its about 350 warp instructions, half of them on the logic pipe at half rate, and its 16 products of
+// mma.sync (a measured 1.05 ns each per SM) take 79 ns in all: 64 sequences of 1k to 32k tokens run at
+// 4.4 TB/s.  More warps per SM or more tiles in flight per warp do not change that.
 //
 // Method: attention over the valid prefix of the cache (Youtu-VL-4B ncnn port, step 8), GQA grouping
 // (Penguin-VL ncnn port, section 3), softmax as max/subtract/exp/sum/divide (Youtu-VL-4B ncnn port,
@@ -33,14 +40,12 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
 
-#ifndef DQ_C
-#define DQ_C 2048
-#endif
 namespace kva {
 
 namespace {
@@ -59,7 +64,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -114,9 +119,11 @@ struct Shape {
   static constexpr int RING = NS * STAGE;
   static constexpr int MERGE = WARPS * ROWS * (DV + 2) * 4;
   static constexpr int QP = MODE != 0 && SPLITQ ? 2 : 1;    // products per K fragment and block
-  static constexpr int QF = MODE == 2 ? NB * QP * GK * 4 * 256 : 0;   // query fragments held in shared memory
+  static constexpr bool QS = MODE == 2;                     // query fragments in shared memory
+  static constexpr int QF = QS ? NB * QP * GK * 4 * 256 : 0;
   static constexpr int BAR = (WARPS * RING > MERGE ? WARPS * RING : MERGE) + QF;
   static constexpr int SMEM = BAR + WARPS * NS * 8;
+  static constexpr int SUB = MODE == 0 ? 2 : 1;            // 16-key tiles worked on together
   static constexpr int CTAS = MODE == 0 && DK <= 128 ? 4 : 3;   // resident per SM, for the register limit
 };
 
@@ -126,13 +133,12 @@ template <int DK, int DV, int MODE, bool SPLITQ>
 __global__ void __launch_bounds__(THREADS, (Shape<DK, DV, MODE, SPLITQ>::CTAS))
 decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   using S = Shape<DK, DV, MODE, SPLITQ>;
-  constexpr int GK = S::GK, GV = S::GV, NB = S::NB, ROWS = S::ROWS, QP = S::QP;
+  constexpr int GK = S::GK, GV = S::GV, NB = S::NB, ROWS = S::ROWS, QP = S::QP, SUB = S::SUB;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float s_M[ROWS], s_L[ROWS];
+  __shared__ float s_M[ROWS], s_L[ROWS], s_alpha[ROWS];
   __shared__ int s_last;
-  const int c = blockIdx.x, g = blockIdx.y / a.RT, rt = blockIdx.y % a.RT, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
-  const int G = a.Hq / a.c.Hkv, n_rows = G * a.T;
+  const int G = a.Hq / a.c.Hkv, n_rows = G * a.T, units = a.c.Hkv * a.RT;
   unsigned char* ring = smem + warp * S::RING;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::BAR) + warp * NS;
   if (lane == 0) {
@@ -143,30 +149,92 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   griddep_wait();                               // inputs of this launch are complete from here on
   griddep_launch_dependents();
 
-  // ---- the chunk: keys [k0, k1) of the slots that the tile's last token sees ----
-  const int L = min(max(a.lengths[b], 0), a.c.capacity);
+  // ---- this CTA's run: stages [x, x_end) of all units in order (instance, KV head, row tile) ----
+  auto length = [&](int i) { return min(max(a.lengths[i], 0), a.c.capacity); };
+  auto stages_of = [&](int i) { return (length(i) + SK - 1) / SK; };
+  const int c = blockIdx.x;
+  for (int i = c; i < a.B; i += gridDim.x)      // instances that see nothing: zeros
+    if (length(i) == 0) {
+      const int64_t n = (int64_t)a.T * a.Hq * DV;
+      for (int64_t k = tid; k < n; k += THREADS) a.out[i * n + k] = 0.f;
+    }
+  int b, n_cta = 1;
+  int64_t total = 1, base = 0, x, x_end;        // base: first stage of instance b
+  auto start_of = [&](int cta) { return total * cta / n_cta; };
+  auto cta_of = [&](int64_t stage) { return (int)(((stage + 1) * n_cta - 1) / total); };
+  if (a.whole) {                                // one unit each
+    b = c / units;
+    const int stages = stages_of(b);
+    if (stages == 0) return;
+    x = (int64_t)(c % units) * stages;
+    x_end = x + stages;
+  } else {
+    __shared__ int64_t s_sum[WARPS], s_base;
+    __shared__ int s_inst;
+    const int per = (a.B + THREADS - 1) / THREADS, i0 = min(a.B, tid * per), i1 = min(a.B, i0 + per);
+    int64_t mine = 0;                           // stages of the instances i0 .. i1 - 1, per unit
+    for (int i = i0; i < i1; ++i) mine += stages_of(i);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(FULL_MASK, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) upto += s_sum[w];
+      total += s_sum[w];
+    }
+    total *= units;
+    n_cta = (int)min((int64_t)gridDim.x, total);   // every run has a stage
+    if (c >= n_cta) return;
+    x = start_of(c);
+    x_end = start_of(c + 1);
+    int64_t at = (upto - mine) * units;         // stages before instance i0
+    if (at <= x && x < upto * units) {          // one thread's
+      int i = i0;
+      for (; x >= at + (int64_t)stages_of(i) * units; ++i) at += (int64_t)stages_of(i) * units;
+      s_inst = i;
+      s_base = at;
+    }
+    __syncthreads();
+    b = s_inst;
+    base = s_base;
+  }
+  const int64_t x0 = x;
+
+  int slot = 0;                                 // ring position of the next stage to use
+  uint32_t phase = 0;
+  bool ok = true;                               // false: a wait gave up, everything after it is void
+  while (x < x_end) {
+  const int L = length(b), stages = (L + SK - 1) / SK;
+  if (x >= base + (int64_t)stages * units) {    // on to the next instance
+    base += (int64_t)stages * units;
+    ++b;
+    continue;
+  }
+  const int unit = (int)((x - base) / stages), g = unit / a.RT, rt = unit % a.RT;
+  const int64_t unit_at = base + (int64_t)unit * stages;
+  const int st0 = (int)(x - unit_at), st1 = (int)min((int64_t)stages, x_end - unit_at);
+  x = unit_at + st1;
   const int row_end = min(n_rows, (rt + 1) * ROWS);
-  const int end = max(0, L - a.T + (row_end - 1) / G + 1);
-  const int stages = (end + SK - 1) / SK;
-  const int n_chunks = min(a.max_chunks, (end + a.chunk - 1) / a.chunk);
   auto out_row = [&](int row) {                 // row of the tile -> its output
     const int rr = rt * ROWS + row;
     return a.out + (((int64_t)b * a.T + rr / G) * a.Hq + g * G + rr % G) * DV;
   };
-  if (c >= max(n_chunks, 1)) return;
-  if (n_chunks == 0) {                          // nothing visible: zeros
-    for (int i = tid; i < (row_end - rt * ROWS) * DV; i += THREADS) out_row(i / DV)[i % DV] = 0.f;
-    return;
-  }
-  const int st0 = (int)((int64_t)stages * c / n_chunks), st1 = (int)((int64_t)stages * (c + 1) / n_chunks);
-  const int k1 = min(end, st1 * SK);
-  const int n_mine = st1 - st0 > warp ? (st1 - st0 - 1 - warp) / WARPS + 1 : 0;
+  const int k1 = min(L, st1 * SK);
+  const int n_mine = ok && st1 - st0 > warp ? (st1 - st0 - 1 - warp) / WARPS + 1 : 0;
   const int64_t row0 = (int64_t)b * a.c.inst_rows + (int64_t)g * a.c.capacity;
+  const int slot0 = slot;                       // of this run's stage 0
   auto issue = [&](int u) {                     // lane 0: stage u of this warp
     const int ks = (st0 + warp + u * WARPS) * SK;
     const int n = min(SK, (k1 - ks + 3) & ~3);  // whole 16-byte pieces of the scales; capacity is a multiple of 4
-    unsigned char* dst = ring + (u % NS) * S::STAGE;
-    uint64_t* bb = &bar[u % NS];
+    const int at = (slot0 + u) % NS;
+    unsigned char* dst = ring + at * S::STAGE;
+    uint64_t* bb = &bar[at];
     const int64_t row = row0 + ks;
     mbar_arrive_expect_tx(bb, (uint32_t)n * (DK / 2 + DV / 2 + GK * 4 + GV * 4));
     bulk_g2s(dst, a.c.k + row * (DK / 8), (uint32_t)n * (DK / 2), bb);
@@ -181,7 +249,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   // ---- query fragments: column r of block nb, dims 64 gk + 16 t + 0..15 ----
   // word j (8 dims) of group gk gives two MMAs h = 0, 1 with b0 = dims (2h, 2h + 4), b1 = (2h + 1, 2h + 5)
   // (16 rows: in shared memory, written by warp 0)
-  uint32_t qf[MODE == 2 ? 1 : NB][QP][GK][2][2][2];
+  uint32_t qf[S::QS ? 1 : NB][QP][GK][2][2][2];
   uint2* s_qf = reinterpret_cast<uint2*>(smem + S::BAR - S::QF) + lane;
   float qs[NB][GK][2], qf_scale[NB][2];         // of the S^T columns 2t, 2t + 1
 #pragma unroll
@@ -231,7 +299,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           }
 #pragma unroll
           for (int p = 0; p < QP; ++p) {
-            if constexpr (MODE == 2) {
+            if constexpr (S::QS) {
               if (warp == 0) s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)] = make_uint2(f[p][0], f[p][1]);
             } else {
               qf[nb][p][gk][j][h][0] = f[p][0];
@@ -249,7 +317,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
     }
   }
 
-  if constexpr (MODE == 2) __syncthreads();
+  if constexpr (S::QS) __syncthreads();
 
   int lim[NB][2];                               // slots that the columns' tokens see
 #pragma unroll
@@ -276,8 +344,6 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
     l[nb][0] = l[nb][1] = 0.f;
   }
   float vtop = 0.f, vmul = 0.f;                 // power of two above every V scale so far; weights carry vmul = 2^6 / vtop
-  bool ok = true;
-  int done = 0;                                 // stages consumed
 
   // key order inside a 16-key tile: MMA row (and K index) j holds key sigma(j); adjacent rows and
   // every second row alternate between even and odd keys, which spreads the 64-byte rows over the
@@ -287,58 +353,72 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   const int k_at = kr * (DK / 2) + t * (DK / 8), kp_at = S::KC + S::VC + kr * (GK * 4);
   const int v0_at = S::KC + kv0 * (DV / 2) + r * (GV * 4), v1_at = S::KC + kv1 * (DV / 2) + r * (GV * 4);
   const int vp_at = S::KC + S::VC + S::KP + kr * (GV * 4);
+  // factors that the compiler does not know: shifts to the left as products, on the multiply-add pipe (the
+  // logic pipe carries the unpacking)
+  uint32_t sixteen, two16;
+  asm volatile("mov.u32 %0, 16;\n mov.u32 %1, 65536;" : "=r"(sixteen), "=r"(two16));
+  auto scale_of = [&](uint32_t w) { return __uint_as_float(w * two16); };   // bf16_lo
   [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on the second halves of the weights
 
-  // One 16-key tile of a stage; kb: its first key.  TAIL: some key is hidden from some column.
-  auto tile = [&](auto tail, const unsigned char* stg, int tt, int kb) {
+  // SUB 16-key tiles of a stage from tile t0 on; kb: their first key.  TAIL: some key is hidden from some
+  // column.
+  auto tiles = [&](auto tail, const unsigned char* stg, int t0, int kb) {
     constexpr bool TAIL = decltype(tail)::value;
-    // ---- S^T ----
-    float d[NB][GK][4];
+    float s[SUB][NB][4];                        // scores of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1
+    uint32_t vp[SUB][2][GV];                    // scales and midpoints of V
+    float top = 0.f;
+    // ---- S^T: chains of products into the same accumulator interleave ----
+    float d[SUB][NB][GK][4];
+    uint32_t wk[SUB][2][2 * GK], kp[SUB][2][GK];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int q = 0; q < SUB; ++q) {
+      const int tt = t0 + q;
 #pragma unroll
-      for (int gk = 0; gk < GK; ++gk) d[nb][gk][0] = d[nb][gk][1] = d[nb][gk][2] = d[nb][gk][3] = 0.f;
-    uint32_t wk[2][2 * GK], kp[2][GK];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      load_words(stg + k_at + (16 * tt + 8 * hh) * (DK / 2), wk[hh]);
-      load_words(stg + kp_at + (16 * tt + 8 * hh) * (GK * 4), kp[hh]);
+        for (int gk = 0; gk < GK; ++gk) d[q][nb][gk][0] = d[q][nb][gk][1] = d[q][nb][gk][2] = d[q][nb][gk][3] = 0.f;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        load_words(stg + k_at + (16 * tt + 8 * hh) * (DK / 2), wk[q][hh]);
+        load_words(stg + kp_at + (16 * tt + 8 * hh) * (GK * 4), kp[q][hh]);
+        load_words(stg + vp_at + (16 * tt + 8 * hh) * (GV * 4), vp[q][hh]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int gk = 0; gk < GK; ++gk) {
-        uint32_t x = wk[0][j * GK + gk], y = wk[1][j * GK + gk];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = x & 0x000f000fu, a1 = y & 0x000f000fu, a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
+        for (int gk = 0; gk < GK; ++gk)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int p = 0; p < QP; ++p) {
-              uint2 q;
-              if constexpr (MODE == 2) q = s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)];
-              else q = make_uint2(qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
-              mma16816(d[nb][gk], a0, a1, a2, a3, q.x, q.y);
+              uint2 f;
+              if constexpr (S::QS) f = s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)];
+              else f = make_uint2(qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
+#pragma unroll
+              for (int q = 0; q < SUB; ++q) {
+                const uint32_t x = wk[q][0][j * GK + gk] >> (8 * h), y = wk[q][1][j * GK + gk] >> (8 * h);
+                mma16816(d[q][nb][gk], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+              }
             }
-          x >>= 8; y >>= 8;
-        }
-      }
-    // ---- scale and midpoint of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1 ----
-    float s[NB][4];
-    {
+#pragma unroll
+    for (int q = 0; q < SUB; ++q) {
+      const int k0 = kb + 16 * q;
+      // ---- scale and midpoint ----
       float sp[NB][4], sc[NB][4];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int gk = 0; gk < GK; ++gk) {
-          const float scale = bf16_lo(kp[hh][gk]), off = fmaf(-8.f, scale, bf16_hi(kp[hh][gk]));
+          const float scale = scale_of(kp[q][hh][gk]), off = fmaf(-8.f, scale, bf16_hi(kp[q][hh][gk]));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int e = 2 * hh + i;
-              sp[nb][e] = gk == 0 ? scale * d[nb][gk][e] : fmaf(scale, d[nb][gk][e], sp[nb][e]);
+              sp[nb][e] = gk == 0 ? scale * d[q][nb][gk][e] : fmaf(scale, d[q][nb][gk][e], sp[nb][e]);
               sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
             }
         }
@@ -347,34 +427,29 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
-          s[nb][e] = sp[nb][e] + sc[nb][e];             // times qf_scale: log2 units
+          s[q][nb][e] = sp[nb][e] + sc[nb][e];          // times qf_scale: log2 units
+          if (TAIL && k0 + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[q][nb][e] = -INFINITY;
+        }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int gv = 0; gv < GV; ++gv) {
+          if (TAIL && k0 + kr + 8 * hh >= k1) vp[q][hh][gv] = 0u;   // slots past the run may hold anything
+          top = fmaxf(top, scale_of(vp[q][hh][gv]));
         }
     }
-    if constexpr (TAIL) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (kb + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[nb][e] = -INFINITY;
-    }
-    // ---- scales of V ----
-    uint32_t vp[2][GV];
-    float top = 0.f;
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      load_words(stg + vp_at + (16 * tt + 8 * hh) * (GV * 4), vp[hh]);
-#pragma unroll
-      for (int gv = 0; gv < GV; ++gv) {
-        if (TAIL && kb + kr + 8 * hh >= k1) vp[hh][gv] = 0u;    // slots past the chunk may hold anything
-        top = fmaxf(top, bf16_lo(vp[hh][gv]));
-      }
-    }
     // ---- online softmax: move the references when a score or a scale outgrows them (rare) ----
+    float high[NB][2];
     bool grow = top > vtop;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) grow |= fmaxf(s[nb][i], s[nb][2 + i]) > thr[nb][i];
+      for (int i = 0; i < 2; ++i) {
+        high[nb][i] = fmaxf(s[0][nb][i], s[0][nb][2 + i]);
+#pragma unroll
+        for (int q = 1; q < SUB; ++q) high[nb][i] = fmaxf(fmaxf(high[nb][i], s[q][nb][i]), s[q][nb][2 + i]);
+        grow |= high[nb][i] > thr[nb][i];
+      }
     if (__any_sync(FULL_MASK, grow)) {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
@@ -390,7 +465,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mt = fmaxf(s[nb][i], s[nb][2 + i]);
+          float mt = high[nb][i];
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
           float alpha = 1.f;
@@ -409,101 +484,106 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           }
         }
     }
-    float p[NB][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int q = 0; q < SUB; ++q) {
+      const int tt = t0 + q;
+      float p[NB][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[nb][e] = ex2(fmaf(s[nb][e], qf_scale[nb][e & 1], -m[nb][e & 1]));
-        l[nb][e & 1] += p[nb][e];
-      }
-    // ---- weights p * scale of V, per group: operand fragments of keys 2t, 2t + 1 (and + 8), column r ----
-    uint32_t bh[NB][GV][2];
-    [[maybe_unused]] uint32_t bl[NB][GV][2];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int gv = 0; gv < GV; ++gv)
+        for (int e = 0; e < 4; ++e) {
+          p[nb][e] = ex2(fmaf(s[q][nb][e], qf_scale[nb][e & 1], -m[nb][e & 1]));
+          l[nb][e & 1] += p[nb][e];
+        }
+      // ---- weights p * scale of V, per group: operand fragments of keys 2t, 2t + 1 (and + 8), column r ----
+      uint32_t bh[NB][GV][2];
+      [[maybe_unused]] uint32_t bl[NB][GV][2];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const float mul = bf16_lo(vp[hh][gv]) * vmul, mid = bf16_hi(vp[hh][gv]);
+      for (int gv = 0; gv < GV; ++gv)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float w[2];
+        for (int hh = 0; hh < 2; ++hh) {
+          const float mul = scale_of(vp[q][hh][gv]) * vmul, mid = bf16_hi(vp[q][hh][gv]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float pi = p[nb][2 * hh + i];
-            w[i] = pi * mul;
-            if constexpr (TAIL) {                       // a hidden key's values may be NaN: no 0 * NaN
-              const bool hidden = s[nb][2 * hh + i] == -INFINITY;
-              if (hidden) w[i] = 0.f;
-              om[nb][gv][i] += hidden ? 0.f : pi * mid;
+          for (int nb = 0; nb < NB; ++nb) {
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float pi = p[nb][2 * hh + i];
+              w[i] = pi * mul;
+              if constexpr (TAIL) {                     // a hidden key's values may be NaN: no 0 * NaN
+                const bool hidden = s[q][nb][2 * hh + i] == -INFINITY;
+                if (hidden) w[i] = 0.f;
+                om[nb][gv][i] += hidden ? 0.f : pi * mid;
+              } else {
+                om[nb][gv][i] = fmaf(pi, mid, om[nb][gv][i]);
+              }
+            }
+            const uint32_t hi = pack_f16x2(w[0], w[1]);
+            const float2 f = unpack_f16x2(hi);
+            if constexpr (MODE == 0) {                  // lanes t < 2: the first halves; t >= 2: what they leave
+              bh[nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
             } else {
-              om[nb][gv][i] = fmaf(pi, mid, om[nb][gv][i]);
+              bh[nb][gv][hh] = transpose8x8(hi);
+              bl[nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
             }
           }
-          const uint32_t hi = pack_f16x2(w[0], w[1]);
-          const float2 f = unpack_f16x2(hi);
-          if constexpr (MODE == 0) {                    // lanes t < 2: the first halves; t >= 2: what they leave
-            bh[nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
-          } else {
-            bh[nb][gv][hh] = transpose8x8(hi);
-            bl[nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
-          }
         }
-      }
-    // ---- O^T += V^T P ----
-    uint32_t wv[4][GV];
+      // ---- O^T += V^T P ----
+      uint32_t wv[4][GV];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load_words(stg + (k & 1 ? v1_at : v0_at) + (16 * tt + (k & 2 ? 8 : 0)) * (DV / 2), wv[k]);
+      for (int k = 0; k < 4; ++k) load_words(stg + (k & 1 ? v1_at : v0_at) + (16 * tt + (k & 2 ? 8 : 0)) * (DV / 2), wv[k]);
 #pragma unroll
-    for (int gv = 0; gv < GV; ++gv) {
-      const uint32_t x0 = __byte_perm(wv[0][gv], wv[1][gv], 0x5410), y0 = __byte_perm(wv[0][gv], wv[1][gv], 0x7632);
-      const uint32_t x1 = __byte_perm(wv[2][gv], wv[3][gv], 0x5410), y1 = __byte_perm(wv[2][gv], wv[3][gv], 0x7632);
+      for (int gv = 0; gv < GV; ++gv) {
+        // halves of two keys' words side by side, nibbles 0..3 (x) and 4..7 (y), and with their bytes exchanged
+        const uint32_t x0[2] = {__byte_perm(wv[0][gv], wv[1][gv], 0x5410), __byte_perm(wv[0][gv], wv[1][gv], 0x4501)};
+        const uint32_t y0[2] = {__byte_perm(wv[0][gv], wv[1][gv], 0x7632), __byte_perm(wv[0][gv], wv[1][gv], 0x6723)};
+        const uint32_t x1[2] = {__byte_perm(wv[2][gv], wv[3][gv], 0x5410), __byte_perm(wv[2][gv], wv[3][gv], 0x4501)};
+        const uint32_t y1[2] = {__byte_perm(wv[2][gv], wv[3][gv], 0x7632), __byte_perm(wv[2][gv], wv[3][gv], 0x6723)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
-        // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
-        auto code = [&](uint32_t v) { return (i == 0 ? v * 16u : v >> (4 * (i > 0 ? i - 1 : 0))) & 0x00f000f0u; };
-        constexpr uint32_t eight = 0x80808080u;                     // -8 2^-20, twice
-        uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
-        if constexpr (MODE == 0) {
-          mma16816(o[0][gv][i], a0, a1, a2, a3, bh[0][gv][0], bh[0][gv][1]);
-          mma16816(o[0][gv][i], eight, eight, eight, eight, bh[0][gv][0], bh[0][gv][1]);
-        } else {
-          const __half2 e2 = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));
+        for (int i = 0; i < 4; ++i) {
+          // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
+          // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
+          auto code = [&](const uint32_t (&v)[2]) { return (i & 1 ? v[i >> 1] : v[i >> 1] * sixteen) & 0x00f000f0u; };
+          uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
+          const __half2 eight = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));   // -8 2^-20, twice
           auto centre = [&](uint32_t v) {
-            const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), e2);
+            const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), eight);
             return *reinterpret_cast<const uint32_t*>(&z);
           };
           a0 = centre(a0); a1 = centre(a1); a2 = centre(a2); a3 = centre(a3);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
-            mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
+          for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
+          if constexpr (MODE != 0) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
           }
         }
       }
     }
   };
 
-  int slot = 0;                                 // ring position of stage u
-  uint32_t phase = 0;
-  for (int u = 0; u < n_mine; done = ++u) {
-    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) { ok = false; break; }
+  for (int u = 0; u < n_mine; ++u) {
+    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) {
+      ok = false;                               // gave up: the copies still in flight land first (bounded)
+      for (int v = u + 1; v < n_mine && v < u + NS; ++v) {
+        if (++slot == NS) { slot = 0; phase ^= 1; }
+        (void)mbar_wait_bounded(&bar[slot], phase);
+      }
+      break;
+    }
     const unsigned char* stg = ring + slot * S::STAGE;
     const int ks = (st0 + warp + u * WARPS) * SK;
     if (ks + SK <= lim_all) {
 #pragma unroll
-      for (int tt = 0; tt < SK / 16; ++tt) tile(std::false_type{}, stg, tt, ks + 16 * tt);
+      for (int tt = 0; tt < SK / 16; tt += SUB) tiles(std::false_type{}, stg, tt, ks + 16 * tt);
     } else {
 #pragma unroll 1
-      for (int tt = 0; tt < SK / 16 && ks + 16 * tt < k1; ++tt) tile(std::true_type{}, stg, tt, ks + 16 * tt);
+      for (int tt = 0; tt < SK / 16 && ks + 16 * tt < k1; tt += SUB) tiles(std::true_type{}, stg, tt, ks + 16 * tt);
     }
     __syncwarp();                               // all lanes are done with this stage
     if (lane == 0 && u + NS < n_mine) issue(u + NS);
     if (++slot == NS) { slot = 0; phase ^= 1; }
   }
-  if (!ok)                                      // gave up: the copies still in flight land first (bounded)
-    for (int u = done; u < n_mine && u < done + NS; ++u) (void)mbar_wait_bounded(&bar[u % NS], (uint32_t)((u / NS) & 1));
 
   // ---- merge the warps ----
 #pragma unroll
@@ -556,45 +636,96 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
     s_M[tid] = M; s_L[tid] = Ls;
   }
   __syncthreads();
-  const bool single = n_chunks == 1;
+  const bool whole = st0 == 0 && st1 == stages;
   const int rows_here = row_end - rt * ROWS;
-  const int64_t unit0 = ((int64_t)b * gridDim.y + blockIdx.y) * ROWS;
+  // parts of shared units: a CTA keeps two, [0] of the unit that its run begins in, [1] of its last one
+  const int64_t my_part = ((int64_t)c * 2 + (x0 >= unit_at ? 0 : 1)) * ROWS;
   for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
     const int row = idx / DV, dd = idx % DV;
     float tot = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) tot += ex2(sm_m[w * ROWS + row] - s_M[row]) * sm_o[(w * ROWS + row) * DV + dd];
-    if (single) {
+    if (whole) {
       out_row(row)[dd] = s_L[row] == 0.f ? 0.f : tot / s_L[row];
     } else {
-      const int64_t pi = (unit0 + row) * a.max_chunks + c;
+      const int64_t pi = my_part + row;
       a.part_acc[pi * DV + dd] = tot;
       if (dd == 0) { a.part_ml[2 * pi] = s_M[row]; a.part_ml[2 * pi + 1] = s_L[row]; }
     }
   }
-  if (single) return;
-
-  __threadfence();
-  __syncthreads();
-  unsigned* counter = a.counters + (int64_t)b * gridDim.y + blockIdx.y;
-  if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(n_chunks - 1);
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
-    const int row = idx / DV, dd = idx % DV;
-    const int64_t p0 = (unit0 + row) * a.max_chunks;
-    float M = M_NONE;
-    for (int cc = 0; cc < n_chunks; ++cc) M = fmaxf(M, __ldcg(&a.part_ml[2 * (p0 + cc)]));
-    float num = 0.f, den = 0.f;
-    for (int cc = 0; cc < n_chunks; ++cc) {
-      const float w = ex2(__ldcg(&a.part_ml[2 * (p0 + cc)]) - M);
-      num = fmaf(w, __ldcg(&a.part_acc[(p0 + cc) * DV + dd]), num);
-      den = fmaf(w, __ldcg(&a.part_ml[2 * (p0 + cc) + 1]), den);
+  if (!whole) {
+    const int c0 = cta_of(unit_at), c1 = cta_of(unit_at + stages - 1);
+    __threadfence();
+    __syncthreads();
+    unsigned* counter = a.counters + (int64_t)b * units + unit;
+    if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+    __syncthreads();
+    if (s_last) {                               // the unit's last part: join them in order
+      __threadfence();
+      constexpr int EPT = ROWS * DV / THREADS;              // outputs per thread
+      constexpr int BLOCK = (S::BAR - S::QF) / (ROWS * 8) < 256 ? (S::BAR - S::QF) / (ROWS * 8) : 256;   // parts at a time
+      float2* s_ml = reinterpret_cast<float2*>(smem);       // [ROWS][BLOCK] (max, sum); then (weight, -)
+      const int first = c0 * 2 + (start_of(c0) >= unit_at ? 0 : 1);   // the others' parts are their [0]
+      auto part = [&](int cc) { return (int64_t)(cc == c0 ? first : 2 * cc) * ROWS; };
+      float acc[EPT];
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) acc[e] = 0.f;
+      if (tid < ROWS) { s_M[tid] = M_NONE; s_L[tid] = 0.f; }
+      for (int cb = c0; cb <= c1; cb += BLOCK) {            // one pass, unless the unit has very many parts
+        const int n = min(BLOCK, c1 + 1 - cb);
+        __syncthreads();
+        for (int i = tid; i < ROWS * n; i += THREADS) {
+          const int cc = i / ROWS, row = i - cc * ROWS;
+          s_ml[row * BLOCK + cc] = row < rows_here ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + part(cb + cc) + row)
+                                                   : make_float2(M_NONE, 0.f);
+        }
+        __syncthreads();
+        for (int row = warp; row < ROWS; row += WARPS) {    // weights against the maximum so far
+          float M = s_M[row], den = 0.f;
+          const float before = M;
+          for (int cc = lane; cc < n; cc += 32) M = fmaxf(M, s_ml[row * BLOCK + cc].x);
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
+          for (int cc = lane; cc < n; cc += 32) {
+            const float2 ml = s_ml[row * BLOCK + cc];
+            const float w = ex2(ml.x - M);
+            den = fmaf(w, ml.y, den);
+            s_ml[row * BLOCK + cc].x = w;
+          }
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(FULL_MASK, den, x);
+          __syncwarp();
+          if (lane == 0) {
+            const float alpha = ex2(before - M);
+            s_L[row] = fmaf(s_L[row], alpha, den);
+            s_M[row] = M;
+            s_alpha[row] = alpha;
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) acc[e] *= s_alpha[(tid + e * THREADS) / DV];
+        for (int cc = 0; cc < n; ++cc) {
+          const float* src = a.part_acc + part(cb + cc) * DV;
+          float v[EPT];
+#pragma unroll
+          for (int e = 0; e < EPT; ++e)
+            v[e] = (tid + e * THREADS) / DV < rows_here ? __ldcg(src + tid + e * THREADS) : 0.f;
+#pragma unroll
+          for (int e = 0; e < EPT; ++e) acc[e] = fmaf(s_ml[(tid + e * THREADS) / DV * BLOCK + cc].x, v[e], acc[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        const int row = (tid + e * THREADS) / DV, dd = (tid + e * THREADS) % DV;
+        if (row < rows_here) out_row(row)[dd] = s_L[row] == 0.f ? 0.f : acc[e] / s_L[row];
+      }
+      if (tid == 0) *counter = 0u;
     }
-    out_row(row)[dd] = den == 0.f ? 0.f : num / den;
   }
-  if (tid == 0) *counter = 0u;
+  fence_proxy_async_smem();                     // the merge's writes before the next run's copies
+  __syncthreads();
+  }
 }
 
 template <int DK, int DV, int MODE, bool SPLITQ>
@@ -606,7 +737,7 @@ cudaError_t launch_m(const DecodeQ4Args& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured.mark();
   }
-  return launch_pdl(decode_q4_kernel<DK, DV, MODE, SPLITQ>, dim3(a.max_chunks, a.c.Hkv * a.RT, a.B), dim3(THREADS), smem, s, a);
+  return launch_pdl(decode_q4_kernel<DK, DV, MODE, SPLITQ>, dim3(a.ctas), dim3(THREADS), smem, s, a);
 }
 
 template <int DK, int DV>
@@ -627,24 +758,18 @@ bool decode_q4_supports(int Dk, int Dv) {
 
 int decode_q4_row_tile(int rows) { return rows <= 4 ? 4 : (rows <= 8 ? 8 : 16); }
 
-// Chunks of at most 1024 keys (many waves: the last wave's tail is one such chunk), or, when all the
-// work fits the GPU at once, the smallest chunk that keeps it to one wave; at least 128 keys (one
-// stage per warp).
-int decode_q4_plan_chunk(const int32_t* lengths, int B, int units, int max_len, int max_chunks) {
-  constexpr int STEP = WARPS * SK;
-  const int64_t slots = 152 * 4;
-  int64_t keys = 0;
-  for (int b = 0; b < B; ++b) keys += lengths[b];
-  const int floor_chunk = (max_len + max_chunks - 1) / max_chunks;
-  int64_t chunk = std::max<int64_t>(floor_chunk, keys * units / slots);
-  chunk = std::min<int64_t>(std::max<int64_t>((chunk + STEP - 1) / STEP, 1) * STEP, std::max(DQ_C, (floor_chunk + STEP - 1) / STEP * STEP));
-  while (chunk < DQ_C) {
-    int64_t ctas = 0;
-    for (int b = 0; b < B; ++b) ctas += (lengths[b] + chunk - 1) / chunk;
-    if (ctas * units <= slots) break;
-    chunk += STEP;
-  }
-  return (int)chunk;
+// CTAs for `stages` stages of 32 keys in `units` units of at most `longest` stages.  Many units, none of them
+// long against what a CTA would get: one CTA each, in the order that the GPU takes them, and nothing to
+// join (61 sequences x 16 units of about 62 stages: 124 us against 141 in equal runs).  Else equal runs: as many as
+// the GPU holds at once, each with a stage per warp, and not so many that joining a unit's parts
+// (about 40 ns each, one CTA) costs more than its stages take (about 150 ns each, spread over the parts).
+int decode_q4_ctas(int Dk, int rows, int64_t stages, int64_t units, int64_t longest, int64_t all_units, int* whole) {
+  const int per_sm = rows <= 4 && Dk <= 128 ? 4 : (rows <= 8 || Dk <= 128 ? 3 : 2);
+  const int64_t slots = DECODE_Q4_SMS * per_sm;
+  *whole = stages >= 2 * slots * longest && stages > 0 && all_units <= (1 << 24);
+  if (*whole) return (int)all_units;
+  const int64_t most = std::min<int64_t>(slots, (int64_t)(2.0 * std::sqrt((double)stages * (double)units)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, stages / WARPS));
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s) {

@@ -926,12 +926,6 @@ static int64_t decode_q4_units(int Hkv, int Hq, int T, int* tile, int64_t* row_t
   *row_tiles = (rows + *tile - 1) / *tile;
   return (int64_t)Hkv * *row_tiles;
 }
-// Most chunks an instance is cut into: enough CTAs to fill the GPU some times over, and at least
-// 8, so that one long sequence among many short ones is still spread.
-static int decode_q4_max_chunks(int64_t instances_units, int max_len) {
-  const int64_t cap = std::min<int64_t>(DECODE_MAX_CHUNKS, std::max<int64_t>(8, 8192 / std::max<int64_t>(1, instances_units)));
-  return (int)std::min<int64_t>(cap, decode_max_chunks_bound(max_len));
-}
 static size_t decode_q4_zero_bytes(int64_t counters) { return round_up(sizeof(unsigned) * (size_t)counters, 256); }
 
 size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T) {
@@ -949,7 +943,7 @@ size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_h
   int tile;
   int64_t rt;
   const int64_t units = (int64_t)B * decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt);
-  const size_t rows = (size_t)units * tile * decode_q4_max_chunks(units, max_len);
+  const size_t rows = (size_t)DECODE_Q4_MAX_RUNS * 2 * tile;      // two shared units a run
   return decode_q4_zero_bytes(units) + round_up(sizeof(float) * rows * 2, 256) + sizeof(float) * rows * head_dim_v;
 }
 
@@ -976,18 +970,20 @@ kva_status kv_attn_decode_q4(
   if (B > 65535 || units > 65535) return fail(KVA_EUNSUPPORTED, "4-bit decode: B or Hkv * row tiles > 65535");
   if (!workspace) return fail(KVA_EWORKSPACE, "4-bit decode: workspace is NULL");
   if (!aligned16(workspace)) return fail(KVA_EALIGN, "workspace must be 16-byte aligned");
-  int max_len = 0;
+  int64_t stages = 0, used = 0, longest = 0;
   for (int b = 0; b < B; ++b) {
     const int L = lengths_host[b];
     if (L < 0 || L > cache.capacity)
       return fail(KVA_ECAPACITY, "length %d of instance %d outside [0, %d]", L, b, cache.capacity);
-    max_len = std::max(max_len, L);
+    const int64_t n = (L + DECODE_Q4_STAGE - 1) / DECODE_Q4_STAGE;
+    stages += n;
+    longest = std::max(longest, n);
+    used += L > 0;
   }
-  max_len = std::max(max_len, 1);
-  const int max_chunks = decode_q4_max_chunks((int64_t)B * units, max_len);
-  const int chunk = decode_q4_plan_chunk(lengths_host, B, (int)units, max_len, max_chunks);
-  const int chunks = (max_len + chunk - 1) / chunk;
-  const size_t rows = (size_t)B * units * tile * chunks;
+  int whole = 0;
+  const int ctas = decode_q4_ctas(Dk, (int)std::min<int64_t>((int64_t)(n_q_heads / Hkv) * T, 1 << 20), stages * units,
+                                  used * units, longest, (int64_t)B * units, &whole);
+  const size_t rows = whole ? 0 : (size_t)ctas * 2 * tile;
   const size_t zero = decode_q4_zero_bytes(B * units), ml = round_up(sizeof(float) * rows * 2, 256);
   const size_t need = zero + ml + sizeof(float) * rows * Dv;
   if (workspace_bytes < need)
@@ -998,7 +994,7 @@ kva_status kv_attn_decode_q4(
   a.part_ml = reinterpret_cast<float*>(ws + zero);
   a.part_acc = reinterpret_cast<float*>(ws + zero + ml);
   a.q = q; a.c = q4_args(cache); a.lengths = lengths; a.out = out;
-  a.B = B; a.T = T; a.Hq = n_q_heads; a.RT = (int)rt; a.chunk = chunk; a.max_chunks = chunks;
+  a.B = B; a.T = T; a.Hq = n_q_heads; a.RT = (int)rt; a.ctas = ctas; a.whole = whole;
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)Dk);
   a.scale_log2 = sc * 1.4426950408889634f;
   const cudaError_t e = launch_decode_q4(a, q_dtype, (cudaStream_t)stream);

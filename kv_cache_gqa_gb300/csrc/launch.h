@@ -263,15 +263,18 @@ struct DecodeQ4Args {
   const int32_t* lengths;             // [B]
   float* out;                         // [B, T, Hq, Dv]
   unsigned int* counters;             // [B, Hkv, RT] zero on entry, zero on exit
-  float* part_acc;                    // [B, Hkv, RT, rows, max_chunks, Dv]
-  float* part_ml;                     // [B, Hkv, RT, rows, max_chunks, 2]
-  int B, T, Hq, RT, chunk, max_chunks;
+  float* part_acc;                    // [ctas, 2, rows, Dv] (equal runs)
+  float* part_ml;                     // [ctas, 2, rows, 2]
+  int B, T, Hq, RT, ctas;
+  int whole;                          // a CTA per unit; else equal runs of all units' stages
   float scale_log2;
 };
+constexpr int DECODE_Q4_SMS = 152;    // grids are sized for the whole GPU
+constexpr int DECODE_Q4_MAX_RUNS = DECODE_Q4_SMS * 4;
+constexpr int DECODE_Q4_STAGE = 32;   // keys per stage
 bool decode_q4_supports(int Dk, int Dv);
 int decode_q4_row_tile(int rows);     // query rows (G * T) per CTA
-// Keys per CTA: the longest instance is cut into at most max_chunks chunks.
-int decode_q4_plan_chunk(const int32_t* lengths_host, int B, int units, int max_len, int max_chunks);
+int decode_q4_ctas(int Dk, int rows, int64_t stages, int64_t units, int64_t longest, int64_t all_units, int* whole);
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s);
 
 // ---------------------------------------------------------------------------------
