@@ -156,29 +156,6 @@ __device__ __forceinline__ uint32_t quantise8(const uint64_t (&x)[4], uint32_t* 
   return w;
 }
 
-// 8 elements as they lie in memory, and as four pairs of floats.
-template <typename T> struct Raw;
-template <> struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
-    x[0] = pack_f32x2(a.x, a.y); x[1] = pack_f32x2(a.z, a.w);
-    x[2] = pack_f32x2(b.x, b.y); x[3] = pack_f32x2(b.z, b.w);
-  }
-};
-template <> struct Raw<bf16_t> {
-  uint4 a;
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void load(const bf16_t* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
-    x[0] = pack_f32x2(bf16_lo(a.x), bf16_hi(a.x)); x[1] = pack_f32x2(bf16_lo(a.y), bf16_hi(a.y));
-    x[2] = pack_f32x2(bf16_lo(a.z), bf16_hi(a.z)); x[3] = pack_f32x2(bf16_lo(a.w), bf16_hi(a.w));
-  }
-};
 // a b + c d of both elements, products and sum rounded apart
 __device__ __forceinline__ uint64_t sum_of_products(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
   return pack_f32x2(__fadd_rn(__fmul_rn(f32x2_lo(a), f32x2_lo(b)), __fmul_rn(f32x2_lo(c), f32x2_lo(d))),
@@ -234,7 +211,7 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
       w.p = reinterpret_cast<const InT*>(w.kind ? a.k : a.q) + (tok * (w.kind ? Hkv : Hq) + w.unit) * Dk + e0;
     }
   };
-  auto fetch = [&](Walk& w, Raw<InT>& x) {      // the walk's set, then on to the next
+  auto fetch = [&](Walk& w, Raw8<InT>& x) {      // the walk's set, then on to the next
     x.zero();
     if (w.kind > 2) return;
     if (w.kind == 2) {
@@ -252,7 +229,7 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
     }
   };
   Walk walk{0, 0, 0, nullptr};
-  Raw<InT> ahead[2];
+  Raw8<InT> ahead[2];
   if (t < a.T) {
     enter(walk, start);
     fetch(walk, ahead[0]);
@@ -356,7 +333,7 @@ append_q4_kernel(const __grid_constant__ AppendQ4Args a) {
     const bool qk = kind < 2;
     const int G = kind == 1 ? Gk : Gv, per = qk ? RPW : 4;
     if (norm && qk && in_row && set < sets(kind)) {
-      Raw<float> w;
+      Raw8<float> w;
       w.load((kind ? a.k_w : a.q_w) + (int64_t)n * a.w_stride + e0);
       w.pairs(wv);
     }

@@ -83,6 +83,30 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   return r;
 }
 
+// 8 elements as they lie in memory, and as four pairs of floats.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
+    x[0] = pack_f32x2(a.x, a.y); x[1] = pack_f32x2(a.z, a.w);
+    x[2] = pack_f32x2(b.x, b.y); x[3] = pack_f32x2(b.z, b.w);
+  }
+};
+template <> struct Raw8<bf16_t> {
+  uint4 a;
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const bf16_t* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void pairs(uint64_t (&x)[4]) const {
+    x[0] = pack_f32x2(bf16_lo(a.x), bf16_hi(a.x)); x[1] = pack_f32x2(bf16_lo(a.y), bf16_hi(a.y));
+    x[2] = pack_f32x2(bf16_lo(a.z), bf16_hi(a.z)); x[3] = pack_f32x2(bf16_lo(a.w), bf16_hi(a.w));
+  }
+};
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const bf16_t* p) { return __uint_as_float(((uint32_t)p->bits) << 16); }
 

@@ -7,16 +7,15 @@
 // significant bits): two products into the same accumulator; a bf16 row is one.  Persistent CTAs
 // walk vocabulary tiles for one block of 128 rows: warp 0 loads (TMA, 128-byte swizzle, a ring of
 // 64-wide K chunks), warp 1 issues the MMAs into one of two accumulators, warps 2-9 read the other one
-// (a thread: one row, half of the columns) and keep, per row, the maximum, the two sums and a list of candidates.  With fewer than 128 rows only
-// those are loaded: the MMA reads whatever follows them in shared memory into lanes that nobody
-// reads.  Up to 8 row blocks run side by side, so that a table tile is read from HBM once per 8.
+// (a thread: one row, half of the columns) and keep, per row, the maximum, the two sums and a list of
+// candidates.  With fewer than 128 rows only those are loaded: the MMA reads whatever follows them in
+// shared memory into lanes that nobody reads.  Up to 8 row blocks run side by side, so that a table tile is read from HBM once per 8.
 //
-// Streaming form: grid (vocabulary split p, block of 8 batch rows).  The 8 warps of a CTA dot 4
-// table rows each with the 8 hidden rows (staged in shared memory) and leave 32 x 8 logits in
-// shared memory; then warp b owns batch row b and lane r the r-th logit.  A lane keeps, over the
-// rows that pass it, the running maximum m, s = sum exp(z - m), u = sum exp(z - m) (z - m) and a
-// sorted list of its TK best (logit, id) keys; the warp joins its lanes at the end and writes one
-// partial per (split, batch row).
+// Streaming form: grid (vocabulary split, block of NB = 1, 2, 4 or 8 batch rows).  A warp takes 4 table rows at
+// a time and loads the next 256 columns of them before it multiplies the current ones with the NB hidden
+// rows, which lie in shared memory in the lanes' order (two products an instruction).  The lanes' 4 NB sums
+// are reduced by halving, which leaves one logit (table row, batch row) in a lane or a few: it keeps the
+// maximum, the two sums and a list of the logits that it meets, and the CTA joins its lanes at the end.
 //
 // Merge (one CTA per batch row): joins the splits' (m, s, u) in a fixed order and their lists, then
 // scores the given token and the TK candidates again: the lists hold TK > top_k candidates by
@@ -42,8 +41,6 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int BG = 8;                         // batch rows per CTA (one per warp)
-constexpr int ROWS = 32;                      // vocabulary rows per step (one per lane)
 // Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per token scored again.
 __host__ __device__ constexpr int merge_max(int TK) { return TK <= 16 ? 544 : 320; }
 
@@ -174,88 +171,6 @@ __device__ __forceinline__ float hidden_at(const LogprobArgs& a, int64_t i) {
   return a.h_dtype == KVA_BF16 ? load1(reinterpret_cast<const bf16_t*>(a.h) + i) : reinterpret_cast<const float*>(a.h)[i];
 }
 
-template <typename WT, int TK>
-__global__ void __launch_bounds__(THREADS)
-logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
-  extern __shared__ __align__(16) float sh[];   // [nb][H]
-  __shared__ float s_z[BG][ROWS + 1];
-  __shared__ u64 s_list[WARPS][TK];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b0 = blockIdx.y * BG, nb = min(BG, a.B - b0), H = a.H;
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int i = tid; i < nb * H; i += THREADS) sh[i] = hidden_at(a, (int64_t)b0 * H + i);
-  __syncthreads();
-
-  Stat st{-INFINITY, 0.f, 0.f};
-  u64 L[TK];
-#pragma unroll
-  for (int i = 0; i < TK; ++i) L[i] = 0ull;
-  const int n_steps = (a.V + ROWS - 1) / ROWS;
-  for (int step = blockIdx.x; step < n_steps; step += a.splits) {
-    for (int r = 0; r < ROWS / WARPS; ++r) {
-      const int rr = warp * (ROWS / WARPS) + r, v = step * ROWS + rr;
-      float part[BG];
-#pragma unroll
-      for (int b = 0; b < BG; ++b) part[b] = 0.f;
-      if (v < a.V) {                            // warp-uniform
-        const WT* wrow = reinterpret_cast<const WT*>(a.W) + (int64_t)v * H;
-        for (int c = lane * 8; c < H; c += 256) {
-          float x[8];
-          load8(wrow + c, x);
-#pragma unroll
-          for (int b = 0; b < BG; ++b)
-            if (b < nb) {
-              const float4 p = *reinterpret_cast<const float4*>(sh + b * H + c);
-              const float4 q = *reinterpret_cast<const float4*>(sh + b * H + c + 4);
-              part[b] = fmaf(x[0], p.x, part[b]); part[b] = fmaf(x[1], p.y, part[b]);
-              part[b] = fmaf(x[2], p.z, part[b]); part[b] = fmaf(x[3], p.w, part[b]);
-              part[b] = fmaf(x[4], q.x, part[b]); part[b] = fmaf(x[5], q.y, part[b]);
-              part[b] = fmaf(x[6], q.z, part[b]); part[b] = fmaf(x[7], q.w, part[b]);
-            }
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < BG; ++b) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part[b] += __shfl_xor_sync(FULL_MASK, part[b], o);
-        if (lane == 0) s_z[b][rr] = part[b];
-      }
-    }
-    __syncthreads();
-    const int v = step * ROWS + lane;
-    if (v < a.V && warp < nb) {
-      const float z = s_z[warp][lane];
-      stat_add(st, z);
-      list_insert<TK>(L, argmax_key(z, (uint32_t)v));
-    }
-    __syncthreads();
-  }
-  if (warp >= nb) return;
-  st = stat_warp(st);
-  const int64_t slot = (int64_t)(b0 + warp) * a.splits + blockIdx.x;
-  if (lane == 0) {
-    float* p = a.part_stat + slot * 4;
-    p[0] = st.m; p[1] = st.s; p[2] = st.u;
-  }
-  warp_merge<TK>(L, s_list[warp]);
-  __syncwarp();
-  for (int i = lane; i < TK; i += 32) a.part_key[slot * TK + i] = s_list[warp][i];
-}
-
-// ---------------------------------------------------------------------------------
-// tcgen05 form
-// ---------------------------------------------------------------------------------
-constexpr int EPI_WARPS = 8;                  // two per TMEM lane quarter, each with half of a tile's columns
-constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
-constexpr int KCH = 64;                       // K elements per chunk (one 128-byte swizzle row)
-constexpr int MROWS = 128;                    // batch rows per block (TMEM lanes)
-constexpr int MAX_N = 256;                    // vocabulary rows per tile
-constexpr int MAX_STAGES = 8;
-constexpr int Z_LD = 17;                      // padded row of the candidate buffer: 16 logits a thread
-constexpr int Z_BYTES = 32 * EPI_WARPS * Z_LD * 4;
-constexpr int TC_FIXED = 1024 + Z_BYTES;      // alignment slack, candidate buffer
-
 // Sorted list of a row's TK best logits; larger first, equal ones in the order of insertion.
 template <int TK>
 struct TopList {
@@ -280,6 +195,146 @@ struct TopList {
   }
   __device__ __forceinline__ u64 key(int i) const { return id[i] < 0 ? 0ull : argmax_key(v[i], (uint32_t)id[i]); }
 };
+
+// Sum over the warp of N values a lane (N a power of two up to 32): by halving, so that lane l ends with the
+// sum of value l / (32 / N).
+template <int N>
+__device__ __forceinline__ float reduce_spread(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = upper ? v[i + n / 2] : v[i], send = upper ? v[i] : v[i + n / 2];
+      v[i] = keep + __shfl_xor_sync(FULL_MASK, send, o);
+    }
+  }
+  for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(FULL_MASK, v[0], o);
+  return v[0];
+}
+
+constexpr int R = 4;                          // table rows at a time of a warp
+// CTAs per SM: two where 128 registers hold the sums (4 x 1024 columns of a 32000-row float32 table: 48 us with
+// the flush of L2, 52 with one CTA of 8 table rows a warp).
+__host__ __device__ constexpr int stream_ctas(int nb, int tk) { return nb <= 4 && tk <= 16 ? 2 : 1; }
+
+template <typename WT, int NB, int TK>
+__global__ void __launch_bounds__(THREADS, stream_ctas(NB, TK))
+logprob_stream_kernel(const __grid_constant__ LogprobArgs a) {
+  constexpr int N = R * NB, SHARE = 32 / N;             // lanes that hold one logit
+  constexpr int LISTS = R * WARPS;                      // of a batch row, one per lane of the warp that joins them
+  static_assert(LISTS == 32, "a list per lane");
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* s_h = reinterpret_cast<float*>(smem);          // [NB][columns / 256][2][32 lanes][4]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b0 = blockIdx.y * NB, nb = min(NB, a.B - b0), H = a.H, chunks = (H + 255) / 256;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int groups = (a.V + R - 1) / R, step = gridDim.x * WARPS;
+  const WT* table = reinterpret_cast<const WT*>(a.W) + 8 * lane;
+  Raw8<WT> raw[R];
+  auto load = [&](int g, int c) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (256 * c + 8 * lane < H) raw[r].load(table + (int64_t)min(g * R + r, a.V - 1) * H + 256 * c);
+      else raw[r].zero();
+    }
+  };
+  int g = blockIdx.x * WARPS + warp;
+  if (g < groups) load(g, 0);
+  // column k = 256 c + 8 l + 4 h + e of a batch row at [c][h][l][e]; columns past H are zeros
+  for (int i = tid; i < NB * chunks * 256; i += THREADS) {
+    const int b = i / (chunks * 256), k = i - b * chunks * 256;
+    const float x = b < nb && k < H ? hidden_at(a, (int64_t)(b0 + b) * H + k) : 0.f;
+    s_h[b * chunks * 256 + (k & ~255) + ((k >> 2) & 1) * 128 + ((k >> 3) & 31) * 4 + (k & 3)] = x;
+  }
+  __syncthreads();
+
+  const int value = lane / SHARE, my_r = value / NB, my_b = value % NB;
+  const bool counts = lane % SHARE == 0 && my_b < nb;
+  Stat st{-INFINITY, 0.f, 0.f};
+  TopList<TK> list;
+  list.clear();
+  for (; g < groups; g += step) {
+    uint64_t acc[R][NB];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[r][b] = 0ull;
+    for (int c = 0; c < chunks; ++c) {
+      uint64_t x[R][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r) raw[r].pairs(x[r]);
+      if (c + 1 < chunks) load(g, c + 1);
+      else if (g + step < groups) load(g + step, 0);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (b >= nb) break;                             // warp-uniform
+        const ulonglong2* h = reinterpret_cast<const ulonglong2*>(s_h + (b * chunks + c) * 256) + lane;
+        const ulonglong2 lo = h[0], hi = h[32];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][b] = fma_f32x2(x[r][0], lo.x, acc[r][b]);
+          acc[r][b] = fma_f32x2(x[r][1], lo.y, acc[r][b]);
+          acc[r][b] = fma_f32x2(x[r][2], hi.x, acc[r][b]);
+          acc[r][b] = fma_f32x2(x[r][3], hi.y, acc[r][b]);
+        }
+      }
+    }
+    float v[N];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) v[r * NB + b] = f32x2_lo(acc[r][b]) + f32x2_hi(acc[r][b]);
+    const float z = reduce_spread<N>(v);
+    const int id = g * R + my_r;
+    if (counts && id < a.V) {
+      stat_add(st, z);
+      if (z > list.v[TK - 1]) list.insert(z, id);
+    }
+  }
+  // join the CTA's lanes: the lists of batch row b, R a warp, through shared memory
+  __syncthreads();
+  u64* s_key = reinterpret_cast<u64*>(smem);            // [NB][LISTS][TK]
+  float4* s_stat = reinterpret_cast<float4*>(s_key + NB * LISTS * TK);   // [NB][LISTS]
+  if (lane % SHARE == 0) {
+    const int at = my_b * LISTS + warp * R + my_r;
+#pragma unroll
+    for (int i = 0; i < TK; ++i) s_key[at * TK + i] = list.key(i);
+    s_stat[at] = make_float4(st.m, st.s, st.u, 0.f);
+  }
+  __syncthreads();
+  for (int b = warp; b < nb; b += WARPS) {
+    u64 L[TK];
+#pragma unroll
+    for (int i = 0; i < TK; ++i) L[i] = s_key[(b * LISTS + lane) * TK + i];
+    const float4 q = s_stat[b * LISTS + lane];
+    const Stat all = stat_warp(Stat{q.x, q.y, q.z});
+    const int64_t slot = (int64_t)(b0 + b) * a.splits + blockIdx.x;
+    __shared__ u64 s_out[WARPS][TK];
+    warp_merge<TK>(L, s_out[warp]);
+    __syncwarp();
+    if (lane == 0) *reinterpret_cast<float4*>(a.part_stat + slot * 4) = make_float4(all.m, all.s, all.u, 0.f);
+    for (int i = lane; i < TK; i += 32) a.part_key[slot * TK + i] = s_out[warp][i];
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// tcgen05 form
+// ---------------------------------------------------------------------------------
+constexpr int EPI_WARPS = 8;                  // two per TMEM lane quarter, each with half of a tile's columns
+constexpr int TC_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int KCH = 64;                       // K elements per chunk (one 128-byte swizzle row)
+constexpr int MROWS = 128;                    // batch rows per block (TMEM lanes)
+constexpr int MAX_N = 256;                    // vocabulary rows per tile
+constexpr int MAX_STAGES = 8;
+constexpr int Z_LD = 17;                      // padded row of the candidate buffer: 16 logits a thread
+constexpr int Z_BYTES = 32 * EPI_WARPS * Z_LD * 4;
+constexpr int TC_FIXED = 1024 + Z_BYTES;      // alignment slack, candidate buffer
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -680,9 +735,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int list_len(int top_k) { return top_k <= 5 ? 8 : (top_k <= 8 ? 12 : (top_k <= 12 ? 16 : 32)); }
 
 constexpr int SMS = 152;                      // grids are sized for the whole GPU; fewer SMs only take longer
-int stream_splits(int B, int V) {
-  const int groups = (B + BG - 1) / BG, ctas = 2 * SMS;
-  return std::max(1, std::min((V + ROWS - 1) / ROWS, ctas / std::min(groups, ctas)));
+// Streaming form: batch rows of a CTA (1, 2, 4 or 8) and the vocabulary splits.
+int stream_rows(int B) { return B >= 5 ? 8 : (B >= 3 ? 4 : B); }
+int stream_splits(int B, int V, int tk) {
+  const int nb = stream_rows(B), blocks = (B + nb - 1) / nb;
+  const int ctas = SMS * stream_ctas(nb, tk);
+  return std::max(1, std::min((V + R * WARPS - 1) / (R * WARPS), ctas / std::min(blocks, ctas)));
 }
 
 bool tc_supports(int H) { return H % KCH == 0; }
@@ -733,19 +791,29 @@ cudaError_t launch_tc(const LogprobArgs& a, const TcPlan& p, cudaStream_t s) {
   return launch_merge<bf16_t, TK>(a, s);
 }
 
-template <typename WT, int TK>
-cudaError_t launch_stream(const LogprobArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(float) * (size_t)std::min(BG, a.B) * a.H;
+template <typename WT, int NB, int TK>
+cudaError_t launch_stream_n(const LogprobArgs& a, cudaStream_t s) {
+  constexpr int join = NB * R * WARPS * (TK * 8 + 16);
+  const int smem = std::max(join, (int)(sizeof(float) * NB * ((a.H + 255) / 256 * 256)));
   static DeviceOnce configured;
   if (!configured.done()) {
-    cudaError_t e = cudaFuncSetAttribute(logprob_stream_kernel<WT, TK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(float) * BG * lmhead_max_hidden()));
+    cudaError_t e = cudaFuncSetAttribute(logprob_stream_kernel<WT, NB, TK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         std::max(join, (int)sizeof(float) * NB * lmhead_max_hidden()));
     if (e != cudaSuccess) return e;
     configured.mark();
   }
-  cudaError_t e = launch_pdl(logprob_stream_kernel<WT, TK>, dim3(a.splits, (a.B + BG - 1) / BG), dim3(THREADS), smem, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_merge<WT, TK>(a, s);
+  const cudaError_t e = launch_pdl(logprob_stream_kernel<WT, NB, TK>, dim3(a.splits, (a.B + NB - 1) / NB), dim3(THREADS),
+                                   (size_t)smem, s, a);
+  return e != cudaSuccess ? e : launch_merge<WT, TK>(a, s);
+}
+template <typename WT, int TK>
+cudaError_t launch_stream(const LogprobArgs& a, cudaStream_t s) {
+  switch (stream_rows(a.B)) {
+    case 1: return launch_stream_n<WT, 1, TK>(a, s);
+    case 2: return launch_stream_n<WT, 2, TK>(a, s);
+    case 4: return launch_stream_n<WT, 4, TK>(a, s);
+    default: return launch_stream_n<WT, 8, TK>(a, s);
+  }
 }
 
 template <int TK>
@@ -758,7 +826,7 @@ cudaError_t launch_k(const LogprobArgs& a, kva_dtype w_dtype, const TcPlan* p, c
 
 // Workspace: [normalised rows, float32][bf16 halves][partial statistics][partial lists]
 size_t logprob_workspace_bytes(int B, int H, int V, int top_k) {
-  int splits = stream_splits(B, V);
+  int splits = stream_splits(B, V, list_len(top_k));
   if (tc_supports(H)) splits = std::max(splits, 2 * tc_plan(B, V, 2).splits);
   const size_t parts = (size_t)B * splits;
   return 2 * up256(sizeof(float) * (size_t)B * H) + up256(parts * 16) + up256(parts * 8 * list_len(top_k));
@@ -770,7 +838,7 @@ cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, c
   const bool split = a.h_dtype == KVA_F32 || a.norm_w;    // rows that need two bf16 halves
   TcPlan p{};
   if (tc) p = tc_plan(a.B, a.V, split ? 2 : 1);
-  a.splits = tc ? 2 * p.splits : stream_splits(a.B, a.V);   // two column halves a CTA
+  a.splits = tc ? 2 * p.splits : stream_splits(a.B, a.V, list_len(a.top_k));   // two column halves a CTA
   a.hn = reinterpret_cast<float*>(ws);
   ws += up256(sizeof(float) * (size_t)a.B * a.H);
   a.hb = tc && split ? reinterpret_cast<uint16_t*>(ws) : nullptr;
