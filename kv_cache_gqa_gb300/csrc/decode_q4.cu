@@ -12,9 +12,11 @@
 // filled by 1-D bulk copies (a head's codes and scales are contiguous in the cache).  Per 16 keys:
 //   S^T = K q^T   keys are the 16 rows of the MMA, query rows its 8 columns.  A 4-bit code u taken
 //                 out of a word by one AND is the float16 subnormal u 2^-24 (or u 2^-20 for the odd
-//                 nibble; V shifts every code there), so K needs 5 instructions per 8 codes; q is scaled by a power of two per
-//                 row so that its float16 (two halves for float32 q) loses nothing.  Scale and
-//                 midpoint of a group enter in float32 after the product:
+//                 nibble; V shifts every code there), so K needs 5 instructions per 8 codes; q is
+//                 scaled by a power of two per row so that its float16 loses nothing: bf16 as it is,
+//                 float32 as multiples of 2^-11 of the largest element, whose sums stay exact, and
+//                 what is left, summed apart.  Scale and midpoint of a group enter in float32 after
+//                 the product:
 //                   s = sum_g scale_g (u . q)_g + (mid_g - 8 scale_g) sum(q)_g.
 //   softmax       online, against a reference maximum that moves only when a score exceeds it by
 //                 more than 2^8, float32
@@ -23,16 +25,18 @@
 //                 turn from S^T's layout to the operand layout with movmatrix.  The codes are
 //                 centred (u - 8) in the operand: else O would be the small difference of sums of
 //                 positive codes.  (Centred by a second product with a constant -8 instead: 3-5%
-//                 slower.)
+//                 slower.)  The tensor core cuts a sum off towards zero: kept in its accumulators,
+//                 the sums of 64 long sequences came out 7e-6 too small.  So it sums 16 or 32 keys,
+//                 which float32 additions join (4e-7; 1.5-4% slower, 15% with 16 rows).
 //                 mid enters as sum p mid_g in float32.
 // With at most 4 query rows the two halves of the weights (and of q) share the 8 columns.  The
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
 // a lane's codes of K, and of V, are adjacent bytes.
 //
 // Bound: the instruction mix.  HBM would allow a 16-key tile (2304 bytes at D = 128) per SM every 52 ns;
-// its about 350 warp instructions, half of them on the logic pipe at half rate, and its 16 products of
+// its about 360 warp instructions, half of them on the logic pipe at half rate, and its 16 products of
 // mma.sync (a measured 1.05 ns each per SM) take 79 ns in all: 64 sequences of 1k to 32k tokens run at
-// 4.4 TB/s.  More warps per SM or more tiles in flight per warp do not change that.
+// 4.3 TB/s.  More warps per SM or more tiles in flight per warp do not change that.
 //
 // Method: attention over the valid prefix of the cache (Youtu-VL-4B ncnn port, step 8), GQA grouping
 // (Penguin-VL ncnn port, section 3), softmax as max/subtract/exp/sum/divide (Youtu-VL-4B ncnn port,
@@ -55,6 +59,7 @@ constexpr int THREADS = WARPS * 32;
 constexpr int SK = 32;                          // keys per stage
 constexpr int NS = 3;                           // ring stages per warp
 constexpr float RESCALE_LOG2 = 8.0f;            // a row's reference max lags its true max by <= 2^8
+constexpr float GRID = 100663296.f;              // 1.5 2^26: adding it rounds to a multiple of 8
 constexpr float M_NONE = -3.0e38f;              // reference max of a row that has seen no key
 
 __device__ __forceinline__ float ex2(float x) {
@@ -100,11 +105,6 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   }
-}
-// (lo, hi) - its float16 rounding h, as float16
-__device__ __forceinline__ uint32_t residual_f16x2(float lo, float hi, uint32_t h) {
-  const float2 f = unpack_f16x2(h);
-  return pack_f16x2(lo - f.x, hi - f.y);
 }
 __device__ __forceinline__ float pow2(int biased) { return __uint_as_float((uint32_t)biased << 23); }
 __device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u); }
@@ -210,521 +210,554 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
   uint32_t phase = 0;
   bool ok = true;                               // false: a wait gave up, everything after it is void
   while (x < x_end) {
-  const int L = length(b), stages = (L + SK - 1) / SK;
-  if (x >= base + (int64_t)stages * units) {    // on to the next instance
-    base += (int64_t)stages * units;
-    ++b;
-    continue;
-  }
-  const int unit = (int)((x - base) / stages), g = unit / a.RT, rt = unit % a.RT;
-  const int64_t unit_at = base + (int64_t)unit * stages;
-  const int st0 = (int)(x - unit_at), st1 = (int)min((int64_t)stages, x_end - unit_at);
-  x = unit_at + st1;
-  const int row_end = min(n_rows, (rt + 1) * ROWS);
-  auto out_row = [&](int row) {                 // row of the tile -> its output
-    const int rr = rt * ROWS + row;
-    return a.out + (((int64_t)b * a.T + rr / G) * a.Hq + g * G + rr % G) * DV;
-  };
-  const int k1 = min(L, st1 * SK);
-  const int n_mine = ok && st1 - st0 > warp ? (st1 - st0 - 1 - warp) / WARPS + 1 : 0;
-  const int64_t row0 = (int64_t)b * a.c.inst_rows + (int64_t)g * a.c.capacity;
-  const int slot0 = slot;                       // of this run's stage 0
-  auto issue = [&](int u) {                     // lane 0: stage u of this warp
-    const int ks = (st0 + warp + u * WARPS) * SK;
-    const int n = min(SK, (k1 - ks + 3) & ~3);  // whole 16-byte pieces of the scales; capacity is a multiple of 4
-    const int at = (slot0 + u) % NS;
-    unsigned char* dst = ring + at * S::STAGE;
-    uint64_t* bb = &bar[at];
-    const int64_t row = row0 + ks;
-    mbar_arrive_expect_tx(bb, (uint32_t)n * (DK / 2 + DV / 2 + GK * 4 + GV * 4));
-    bulk_g2s(dst, a.c.k + row * (DK / 8), (uint32_t)n * (DK / 2), bb);
-    bulk_g2s(dst + S::KC + S::VC, a.c.ks + row * GK, (uint32_t)n * (GK * 4), bb);
-    bulk_g2s(dst + S::KC, a.c.v + row * (DV / 8), (uint32_t)n * (DV / 2), bb);
-    bulk_g2s(dst + S::KC + S::VC + S::KP, a.c.vs + row * GV, (uint32_t)n * (GV * 4), bb);
-  };
-  if (lane == 0)
-    for (int u = 0; u < NS && u < n_mine; ++u) issue(u);
-  __syncwarp();
-
-  // ---- query fragments: column r of block nb, dims 64 gk + 16 t + 0..15 ----
-  // word j (8 dims) of group gk gives two MMAs h = 0, 1 with b0 = dims (2h, 2h + 4), b1 = (2h + 1, 2h + 5)
-  // (16 rows: in shared memory, written by warp 0)
-  uint32_t qf[S::QS ? 1 : NB][QP][GK][2][2][2];
-  uint2* s_qf = reinterpret_cast<uint2*>(smem + S::BAR - S::QF) + lane;
-  float qs[NB][GK][2], qf_scale[NB][2];         // of the S^T columns 2t, 2t + 1
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int col = MODE == 0 ? (r & 3) : 8 * nb + r;
-    const int rr = rt * ROWS + col;
-    const bool on = rr < n_rows;
-    const int64_t qrow = (((int64_t)b * a.T + (on ? rr / G : 0)) * a.Hq + g * G + (on ? rr % G : 0)) * DK;
-    float x[GK][16], big = 0.f, sum[GK];
-#pragma unroll
-    for (int gk = 0; gk < GK; ++gk) {
-      const int64_t o = qrow + 64 * gk + 16 * t;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float y[8];
-        if constexpr (SPLITQ) load8(reinterpret_cast<const float*>(a.q) + o + 8 * j, y);
-        else load8(reinterpret_cast<const bf16_t*>(a.q) + o + 8 * j, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[gk][8 * j + i] = on ? y[i] : 0.f;
-      }
-      sum[gk] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) { big = fmaxf(big, fabsf(x[gk][i])); sum[gk] += x[gk][i]; }
-      sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 1);
-      sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 2);
+    const int L = length(b), stages = (L + SK - 1) / SK;
+    if (x >= base + (int64_t)stages * units) {    // on to the next instance
+      base += (int64_t)stages * units;
+      ++b;
+      continue;
     }
-    big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 2));
-    // the row's largest element becomes 2^13 .. 2^14
-    const int e = min(max(exponent(big), 20), 240);
-    const float up = pow2(267 - e), down = pow2(e + 11) * a.scale_log2;   // 2^(13-(e-127)); 2^24 / up
+    const int unit = (int)((x - base) / stages), g = unit / a.RT, rt = unit % a.RT;
+    const int64_t unit_at = base + (int64_t)unit * stages;
+    const int st0 = (int)(x - unit_at), st1 = (int)min((int64_t)stages, x_end - unit_at);
+    x = unit_at + st1;
+    const int row_end = min(n_rows, (rt + 1) * ROWS);
+    auto out_row = [&](int row) {                 // row of the tile -> its output
+      const int rr = rt * ROWS + row;
+      return a.out + (((int64_t)b * a.T + rr / G) * a.Hq + g * G + rr % G) * DV;
+    };
+    const int k1 = min(L, st1 * SK);
+    const int n_mine = ok && st1 - st0 > warp ? (st1 - st0 - 1 - warp) / WARPS + 1 : 0;
+    const int64_t row0 = (int64_t)b * a.c.inst_rows + (int64_t)g * a.c.capacity;
+    const int slot0 = slot;                       // of this run's stage 0
+    auto issue = [&](int u) {                     // lane 0: stage u of this warp
+      const int ks = (st0 + warp + u * WARPS) * SK;
+      const int n = min(SK, (k1 - ks + 3) & ~3);  // whole 16-byte pieces of the scales; capacity is a multiple of 4
+      const int at = (slot0 + u) % NS;
+      unsigned char* dst = ring + at * S::STAGE;
+      uint64_t* bb = &bar[at];
+      const int64_t row = row0 + ks;
+      mbar_arrive_expect_tx(bb, (uint32_t)n * (DK / 2 + DV / 2 + GK * 4 + GV * 4));
+      bulk_g2s(dst, a.c.k + row * (DK / 8), (uint32_t)n * (DK / 2), bb);
+      bulk_g2s(dst + S::KC + S::VC, a.c.ks + row * GK, (uint32_t)n * (GK * 4), bb);
+      bulk_g2s(dst + S::KC, a.c.v + row * (DV / 8), (uint32_t)n * (DV / 2), bb);
+      bulk_g2s(dst + S::KC + S::VC + S::KP, a.c.vs + row * GV, (uint32_t)n * (GV * 4), bb);
+    };
+    if (lane == 0)
+      for (int u = 0; u < NS && u < n_mine; ++u) issue(u);
+    __syncwarp();
+
+    // ---- query fragments: column r of block nb, dims 64 gk + 16 t + 0..15 ----
+    // word j (8 dims) of group gk gives two MMAs h = 0, 1 with b0 = dims (2h, 2h + 4), b1 = (2h + 1, 2h + 5)
+    // (16 rows: in shared memory, written by warp 0)
+    uint32_t qf[S::QS ? 1 : NB][QP][GK][2][2][2];
+    uint2* s_qf = reinterpret_cast<uint2*>(smem + S::BAR - S::QF) + lane;
+    float qs[NB][GK][2], qf_scale[NB][2];         // of the S^T columns 2t, 2t + 1
 #pragma unroll
-    for (int gk = 0; gk < GK; ++gk)
+    for (int nb = 0; nb < NB; ++nb) {
+      const int col = MODE == 0 ? (r & 3) : 8 * nb + r;
+      const int rr = rt * ROWS + col;
+      const bool on = rr < n_rows;
+      const int64_t qrow = (((int64_t)b * a.T + (on ? rr / G : 0)) * a.Hq + g * G + (on ? rr % G : 0)) * DK;
+      float x[GK][16], big = 0.f, sum[GK];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int gk = 0; gk < GK; ++gk) {
+        const int64_t o = qrow + 64 * gk + 16 * t;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t f[QP][2];
+        for (int j = 0; j < 2; ++j) {
+          float y[8];
+          if constexpr (SPLITQ) load8(reinterpret_cast<const float*>(a.q) + o + 8 * j, y);
+          else load8(reinterpret_cast<const bf16_t*>(a.q) + o + 8 * j, y);
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {         // the odd nibble counts 16 times the even one
-            const int d = 8 * j + 2 * h + o;
-            const float by = o ? up * 0.0625f : up;
-            const float y0 = x[gk][d] * by, y1 = x[gk][d + 4] * by;
-            const uint32_t hi = pack_f16x2(y0, y1);
-            f[0][o] = MODE == 0 && SPLITQ && r >= 4 ? residual_f16x2(y0, y1, hi) : hi;
-            if constexpr (QP == 2) f[1][o] = residual_f16x2(y0, y1, hi);
-          }
-#pragma unroll
-          for (int p = 0; p < QP; ++p) {
-            if constexpr (S::QS) {
-              if (warp == 0) s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)] = make_uint2(f[p][0], f[p][1]);
-            } else {
-              qf[nb][p][gk][j][h][0] = f[p][0];
-              qf[nb][p][gk][j][h][1] = f[p][1];
-            }
-          }
+          for (int i = 0; i < 8; ++i) x[gk][8 * j + i] = on ? y[i] : 0.f;
         }
+        sum[gk] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int src = 4 * (2 * t + i);          // any lane of column 2t + i
-      qf_scale[nb][i] = __shfl_sync(FULL_MASK, down, src);
-#pragma unroll
-      for (int gk = 0; gk < GK; ++gk)           // in units of the product (2^-24 up)
-        qs[nb][gk][i] = __shfl_sync(FULL_MASK, sum[gk] * (up * 5.9604644775390625e-8f), src);
-    }
-  }
-
-  if constexpr (S::QS) __syncthreads();
-
-  int lim[NB][2];                               // slots that the columns' tokens see
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = MODE == 0 ? ((2 * t + i) & 3) : 8 * nb + 2 * t + i;
-      lim[nb][i] = min(L - a.T + min(rt * ROWS + col, n_rows - 1) / G + 1, k1);
-    }
-  const int lim_all = min(L - a.T + (rt * ROWS) / G + 1, k1);   // slots that every column sees
-
-  float o[NB][GV][4][4];                        // value dims 64 gv + 8 r + i (and + 4), columns 2t, 2t + 1
-  float om[NB][GV][2], m[NB][2], thr[NB][2], l[NB][2];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-    for (int gv = 0; gv < GV; ++gv) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[nb][gv][i][0] = o[nb][gv][i][1] = o[nb][gv][i][2] = o[nb][gv][i][3] = 0.f;
-      om[nb][gv][0] = om[nb][gv][1] = 0.f;
-    }
-    m[nb][0] = m[nb][1] = M_NONE;               // reference maximum, log2 units
-    thr[nb][0] = thr[nb][1] = -INFINITY;        // (m + RESCALE_LOG2) in units of the raw score
-    l[nb][0] = l[nb][1] = 0.f;
-  }
-  float vtop = 0.f, vmul = 0.f;                 // power of two above every V scale so far; weights carry vmul = 2^6 / vtop
-
-  // key order inside a 16-key tile: MMA row (and K index) j holds key sigma(j); adjacent rows and
-  // every second row alternate between even and odd keys, which spreads the 64-byte rows over the
-  // shared-memory banks
-  const int kr = r ^ ((r >> 1) & 1);            // sigma(r); rows r + 8: + 8
-  const int kv0 = (2 * t) ^ (t & 1), kv1 = (2 * t + 1) ^ (t & 1);
-  const int k_at = kr * (DK / 2) + t * (DK / 8), kp_at = S::KC + S::VC + kr * (GK * 4);
-  const int v0_at = S::KC + kv0 * (DV / 2) + r * (GV * 4), v1_at = S::KC + kv1 * (DV / 2) + r * (GV * 4);
-  const int vp_at = S::KC + S::VC + S::KP + kr * (GV * 4);
-  // factors that the compiler does not know: shifts to the left as products, on the multiply-add pipe (the
-  // logic pipe carries the unpacking)
-  uint32_t sixteen, two16;
-  asm volatile("mov.u32 %0, 16;\n mov.u32 %1, 65536;" : "=r"(sixteen), "=r"(two16));
-  auto scale_of = [&](uint32_t w) { return __uint_as_float(w * two16); };   // bf16_lo
-  [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on the second halves of the weights
-
-  // SUB 16-key tiles of a stage from tile t0 on; kb: their first key.  TAIL: some key is hidden from some
-  // column.
-  auto tiles = [&](auto tail, const unsigned char* stg, int t0, int kb) {
-    constexpr bool TAIL = decltype(tail)::value;
-    float s[SUB][NB][4];                        // scores of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1
-    uint32_t vp[SUB][2][GV];                    // scales and midpoints of V
-    float top = 0.f;
-    // ---- S^T: chains of products into the same accumulator interleave ----
-    float d[SUB][NB][GK][4];
-    uint32_t wk[SUB][2][2 * GK], kp[SUB][2][GK];
-#pragma unroll
-    for (int q = 0; q < SUB; ++q) {
-      const int tt = t0 + q;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int gk = 0; gk < GK; ++gk) d[q][nb][gk][0] = d[q][nb][gk][1] = d[q][nb][gk][2] = d[q][nb][gk][3] = 0.f;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        load_words(stg + k_at + (16 * tt + 8 * hh) * (DK / 2), wk[q][hh]);
-        load_words(stg + kp_at + (16 * tt + 8 * hh) * (GK * 4), kp[q][hh]);
-        load_words(stg + vp_at + (16 * tt + 8 * hh) * (GV * 4), vp[q][hh]);
+        for (int i = 0; i < 16; ++i) { big = fmaxf(big, fabsf(x[gk][i])); sum[gk] += x[gk][i]; }
+        sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 1);
+        sum[gk] += __shfl_xor_sync(FULL_MASK, sum[gk], 2);
       }
-    }
+      big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, 2));
+      // the row's largest element becomes 2^13 .. 2^14
+      const int e = min(max(exponent(big), 20), 240);
+      const float up = pow2(267 - e), down = pow2(e + 11) * a.scale_log2;   // 2^(13-(e-127)); 2^24 / up
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int gk = 0; gk < GK; ++gk)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int gk = 0; gk < GK; ++gk)
+          for (int h = 0; h < 2; ++h) {
+            uint32_t f[QP][2];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int p = 0; p < QP; ++p) {
-              uint2 f;
-              if constexpr (S::QS) f = s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)];
-              else f = make_uint2(qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
-#pragma unroll
-              for (int q = 0; q < SUB; ++q) {
-                const uint32_t x = wk[q][0][j * GK + gk] >> (8 * h), y = wk[q][1][j * GK + gk] >> (8 * h);
-                mma16816(d[q][nb][gk], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+            for (int o = 0; o < 2; ++o) {         // the odd nibble counts 16 times the even one
+              const int d = 8 * j + 2 * h + o;
+              const float by = o ? 0.0625f : 1.f;
+              float y0 = x[gk][d] * up, y1 = x[gk][d + 4] * up;
+              if constexpr (SPLITQ) {             // first halves: multiples of 8, whose sums the tensor core keeps whole
+                const float h0 = (y0 + GRID) - GRID, h1 = (y1 + GRID) - GRID;
+                const uint32_t hi = pack_f16x2(h0 * by, h1 * by), lo = pack_f16x2((y0 - h0) * by, (y1 - h1) * by);
+                f[0][o] = MODE == 0 && r < 4 ? hi : lo;
+                if constexpr (QP == 2) f[1][o] = hi;
+              } else {
+                f[0][o] = pack_f16x2(y0 * by, y1 * by);
               }
             }
 #pragma unroll
-    for (int q = 0; q < SUB; ++q) {
-      const int k0 = kb + 16 * q;
-      // ---- scale and midpoint ----
-      float sp[NB][4], sc[NB][4];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int gk = 0; gk < GK; ++gk) {
-          const float scale = scale_of(kp[q][hh][gk]), off = fmaf(-8.f, scale, bf16_hi(kp[q][hh][gk]));
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int e = 2 * hh + i;
-              sp[nb][e] = gk == 0 ? scale * d[q][nb][gk][e] : fmaf(scale, d[q][nb][gk][e], sp[nb][e]);
-              sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
+            for (int p = 0; p < QP; ++p) {
+              if constexpr (S::QS) {
+                if (warp == 0) s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)] = make_uint2(f[p][0], f[p][1]);
+              } else {
+                qf[nb][p][gk][j][h][0] = f[p][0];
+                qf[nb][p][gk][j][h][1] = f[p][1];
+              }
             }
-        }
+          }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int i = 0; i < 2; ++i) {
+        const int src = 4 * (2 * t + i);          // any lane of column 2t + i
+        qf_scale[nb][i] = __shfl_sync(FULL_MASK, down, src);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
-          s[q][nb][e] = sp[nb][e] + sc[nb][e];          // times qf_scale: log2 units
-          if (TAIL && k0 + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[q][nb][e] = -INFINITY;
-        }
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int gv = 0; gv < GV; ++gv) {
-          if (TAIL && k0 + kr + 8 * hh >= k1) vp[q][hh][gv] = 0u;   // slots past the run may hold anything
-          top = fmaxf(top, scale_of(vp[q][hh][gv]));
-        }
+        for (int gk = 0; gk < GK; ++gk)           // in units of the product (2^-24 up)
+          qs[nb][gk][i] = __shfl_sync(FULL_MASK, sum[gk] * (up * 5.9604644775390625e-8f), src);
+      }
     }
-    // ---- online softmax: move the references when a score or a scale outgrows them (rare) ----
-    float high[NB][2];
-    bool grow = top > vtop;
+
+    if constexpr (S::QS) __syncthreads();
+
+    int lim[NB][2];                               // slots that the columns' tokens see
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        high[nb][i] = fmaxf(s[0][nb][i], s[0][nb][2 + i]);
-#pragma unroll
-        for (int q = 1; q < SUB; ++q) high[nb][i] = fmaxf(fmaxf(high[nb][i], s[q][nb][i]), s[q][nb][2 + i]);
-        grow |= high[nb][i] > thr[nb][i];
+        const int col = MODE == 0 ? ((2 * t + i) & 3) : 8 * nb + 2 * t + i;
+        lim[nb][i] = min(L - a.T + min(rt * ROWS + col, n_rows - 1) / G + 1, k1);
       }
-    if (__any_sync(FULL_MASK, grow)) {
+    const int lim_all = min(L - a.T + (rt * ROWS) / G + 1, k1);   // slots that every column sees
+
+    uint64_t o[NB][GV][4][2];                     // value dims 64 gv + 8 r + i ([1]: + 4), columns 2t, 2t + 1
+    float om[NB][GV][2], m[NB][2], thr[NB][2], l[NB][2];
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
-      float ratio = 1.f;
-      if (top > vtop) {
-        const int e = max(exponent(top) + 1, 40);       // top < 2^(e-127) (or tiny)
-        const float now = pow2(260 - e);                // weights reach 2^8 * 2^6
-        vtop = pow2(min(e, 254));
-        ratio = vmul == 0.f ? 0.f : now / vmul;
-        vmul = now;
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nb][gv][i][0] = o[nb][gv][i][1] = 0ull;
+        om[nb][gv][0] = om[nb][gv][1] = 0.f;
       }
+      m[nb][0] = m[nb][1] = M_NONE;               // reference maximum, log2 units
+      thr[nb][0] = thr[nb][1] = -INFINITY;        // (m + RESCALE_LOG2) in units of the raw score
+      l[nb][0] = l[nb][1] = 0.f;
+    }
+    float vtop = 0.f, vmul = 0.f;                 // power of two above every V scale so far; weights carry vmul = 2^6 / vtop
+
+    // key order inside a 16-key tile: MMA row (and K index) j holds key sigma(j); adjacent rows and
+    // every second row alternate between even and odd keys, which spreads the 64-byte rows over the
+    // shared-memory banks
+    const int kr = r ^ ((r >> 1) & 1);            // sigma(r); rows r + 8: + 8
+    const int kv0 = (2 * t) ^ (t & 1), kv1 = (2 * t + 1) ^ (t & 1);
+    const int k_at = kr * (DK / 2) + t * (DK / 8), kp_at = S::KC + S::VC + kr * (GK * 4);
+    const int v0_at = S::KC + kv0 * (DV / 2) + r * (GV * 4), v1_at = S::KC + kv1 * (DV / 2) + r * (GV * 4);
+    const int vp_at = S::KC + S::VC + S::KP + kr * (GV * 4);
+    // factors that the compiler does not know: shifts to the left as products, on the multiply-add pipe (the
+    // logic pipe carries the unpacking)
+    uint32_t sixteen, two16;
+    asm volatile("mov.u32 %0, 16;\n mov.u32 %1, 65536;" : "=r"(sixteen), "=r"(two16));
+    auto scale_of = [&](uint32_t w) { return __uint_as_float(w * two16); };   // bf16_lo
+    [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on second halves
+
+    // SUB 16-key tiles of a stage from tile t0 on; kb: their first key.  TAIL: some key is hidden from some
+    // column.
+    auto tiles = [&](auto tail, const unsigned char* stg, int t0, int kb) {
+      constexpr bool TAIL = decltype(tail)::value;
+      float s[SUB][NB][4];                        // scores of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1
+      uint32_t vp[SUB][2][GV];                    // scales and midpoints of V
+      float top = 0.f;
+      // ---- S^T: chains of products into the same accumulator interleave ----
+      float d[SUB][NB][GK][QP][4];             // the halves of q apart: the first ones' sums stay exact
+      uint32_t wk[SUB][2][2 * GK], kp[SUB][2][GK];
+#pragma unroll
+      for (int q = 0; q < SUB; ++q) {
+        const int tt = t0 + q;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int gk = 0; gk < GK; ++gk)
+#pragma unroll
+            for (int p = 0; p < QP; ++p) d[q][nb][gk][p][0] = d[q][nb][gk][p][1] = d[q][nb][gk][p][2] = d[q][nb][gk][p][3] = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          load_words(stg + k_at + (16 * tt + 8 * hh) * (DK / 2), wk[q][hh]);
+          load_words(stg + kp_at + (16 * tt + 8 * hh) * (GK * 4), kp[q][hh]);
+          load_words(stg + vp_at + (16 * tt + 8 * hh) * (GV * 4), vp[q][hh]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int gk = 0; gk < GK; ++gk)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int p = 0; p < QP; ++p) {
+                uint2 f;
+                if constexpr (S::QS) f = s_qf[32 * ((((nb * QP + p) * GK + gk) * 2 + j) * 2 + h)];
+                else f = make_uint2(qf[nb][p][gk][j][h][0], qf[nb][p][gk][j][h][1]);
+#pragma unroll
+                for (int q = 0; q < SUB; ++q) {
+                  const uint32_t x = wk[q][0][j * GK + gk] >> (8 * h), y = wk[q][1][j * GK + gk] >> (8 * h);
+                  mma16816(d[q][nb][gk][p], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+                }
+              }
+#pragma unroll
+      for (int q = 0; q < SUB; ++q) {
+        const int k0 = kb + 16 * q;
+        // ---- scale and midpoint ----
+        float sp[NB][4], sc[NB][4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int gk = 0; gk < GK; ++gk) {
+            const float scale = scale_of(kp[q][hh][gk]), off = fmaf(-8.f, scale, bf16_hi(kp[q][hh][gk]));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int e = 2 * hh + i;
+                const float z = QP == 2 ? d[q][nb][gk][0][e] + d[q][nb][gk][QP - 1][e] : d[q][nb][gk][0][e];
+                sp[nb][e] = gk == 0 ? scale * z : fmaf(scale, z, sp[nb][e]);
+                sc[nb][e] = gk == 0 ? off * qs[nb][gk][i] : fmaf(off, qs[nb][gk][i], sc[nb][e]);
+              }
+          }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (MODE == 0 && SPLITQ) sp[nb][e] += __shfl_xor_sync(FULL_MASK, sp[nb][e], 2);
+            s[q][nb][e] = sp[nb][e] + sc[nb][e];          // times qf_scale: log2 units
+            if (TAIL && k0 + kr + 8 * (e >> 1) >= lim[nb][e & 1]) s[q][nb][e] = -INFINITY;
+          }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv) {
+            if (TAIL && k0 + kr + 8 * hh >= k1) vp[q][hh][gv] = 0u;   // slots past the run may hold anything
+            top = fmaxf(top, scale_of(vp[q][hh][gv]));
+          }
+      }
+      // ---- online softmax: move the references when a score or a scale outgrows them (rare) ----
+      float high[NB][2];
+      bool grow = top > vtop;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mt = high[nb][i];
+          high[nb][i] = fmaxf(s[0][nb][i], s[0][nb][2 + i]);
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
-          float alpha = 1.f;
-          if (mt > thr[nb][i]) {                        // uniform over the column's lanes
-            mt *= qf_scale[nb][i];
-            alpha = ex2(m[nb][i] - mt);
-            m[nb][i] = mt;
-            thr[nb][i] = (mt + RESCALE_LOG2) / qf_scale[nb][i];
-            l[nb][i] *= alpha;
-          }
-#pragma unroll
-          for (int gv = 0; gv < GV; ++gv) {
-            om[nb][gv][i] *= alpha;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) { o[nb][gv][k][i] *= alpha * ratio; o[nb][gv][k][2 + i] *= alpha * ratio; }
-          }
+          for (int q = 1; q < SUB; ++q) high[nb][i] = fmaxf(fmaxf(high[nb][i], s[q][nb][i]), s[q][nb][2 + i]);
+          grow |= high[nb][i] > thr[nb][i];
         }
-    }
+      if (__any_sync(FULL_MASK, grow)) {
 #pragma unroll
-    for (int q = 0; q < SUB; ++q) {
-      const int tt = t0 + q;
-      float p[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[nb][e] = ex2(fmaf(s[q][nb][e], qf_scale[nb][e & 1], -m[nb][e & 1]));
-          l[nb][e & 1] += p[nb][e];
+        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
+        float ratio = 1.f;
+        if (top > vtop) {
+          const int e = max(exponent(top) + 1, 40);       // top < 2^(e-127) (or tiny)
+          const float now = pow2(260 - e);                // weights reach 2^8 * 2^6
+          vtop = pow2(min(e, 254));
+          ratio = vmul == 0.f ? 0.f : now / vmul;
+          vmul = now;
         }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float by[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mt = high[nb][i];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL_MASK, mt, x));
+            float alpha = 1.f;
+            if (mt > thr[nb][i]) {                        // uniform over the column's lanes
+              mt *= qf_scale[nb][i];
+              alpha = ex2(m[nb][i] - mt);
+              m[nb][i] = mt;
+              thr[nb][i] = (mt + RESCALE_LOG2) / qf_scale[nb][i];
+              l[nb][i] *= alpha;
+            }
+#pragma unroll
+            for (int gv = 0; gv < GV; ++gv) om[nb][gv][i] *= alpha;
+            by[i] = alpha * ratio;
+          }
+          const uint64_t by2 = pack_f32x2(by[0], by[1]);
+#pragma unroll
+          for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[nb][gv][k][0] = mul_f32x2(o[nb][gv][k][0], by2);
+              o[nb][gv][k][1] = mul_f32x2(o[nb][gv][k][1], by2);
+            }
+        }
+      }
       // ---- weights p * scale of V, per group: operand fragments of keys 2t, 2t + 1 (and + 8), column r ----
-      uint32_t bh[NB][GV][2];
-      [[maybe_unused]] uint32_t bl[NB][GV][2];
+      uint32_t bh[SUB][NB][GV][2];
+      [[maybe_unused]] uint32_t bl[SUB][NB][GV][2];
 #pragma unroll
-      for (int gv = 0; gv < GV; ++gv)
+      for (int q = 0; q < SUB; ++q) {
+        float p[NB][4];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float mul = scale_of(vp[q][hh][gv]) * vmul, mid = bf16_hi(vp[q][hh][gv]);
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float w[2];
+          for (int e = 0; e < 4; ++e) {
+            p[nb][e] = ex2(fmaf(s[q][nb][e], qf_scale[nb][e & 1], -m[nb][e & 1]));
+            l[nb][e & 1] += p[nb][e];
+          }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float pi = p[nb][2 * hh + i];
-              w[i] = pi * mul;
-              if constexpr (TAIL) {                     // a hidden key's values may be NaN: no 0 * NaN
-                const bool hidden = s[q][nb][2 * hh + i] == -INFINITY;
-                if (hidden) w[i] = 0.f;
-                om[nb][gv][i] += hidden ? 0.f : pi * mid;
+        for (int gv = 0; gv < GV; ++gv)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float mul = scale_of(vp[q][hh][gv]) * vmul, mid = bf16_hi(vp[q][hh][gv]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float pi = p[nb][2 * hh + i];
+                w[i] = pi * mul;
+                if constexpr (TAIL) {                     // a hidden key's values may be NaN: no 0 * NaN
+                  const bool hidden = s[q][nb][2 * hh + i] == -INFINITY;
+                  if (hidden) w[i] = 0.f;
+                  om[nb][gv][i] += hidden ? 0.f : pi * mid;
+                } else {
+                  om[nb][gv][i] = fmaf(pi, mid, om[nb][gv][i]);
+                }
+              }
+              const uint32_t hi = pack_f16x2(w[0], w[1]);
+              const float2 f = unpack_f16x2(hi);
+              if constexpr (MODE == 0) {                  // lanes t < 2: the first halves; t >= 2: what they leave
+                bh[q][nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
               } else {
-                om[nb][gv][i] = fmaf(pi, mid, om[nb][gv][i]);
+                bh[q][nb][gv][hh] = transpose8x8(hi);
+                bl[q][nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
               }
             }
-            const uint32_t hi = pack_f16x2(w[0], w[1]);
-            const float2 f = unpack_f16x2(hi);
-            if constexpr (MODE == 0) {                  // lanes t < 2: the first halves; t >= 2: what they leave
-              bh[nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
-            } else {
-              bh[nb][gv][hh] = transpose8x8(hi);
-              bl[nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
-            }
           }
-        }
-      // ---- O^T += V^T P ----
-      uint32_t wv[4][GV];
+      }
+      // ---- O^T += V^T P: the tensor core cuts a sum off towards zero, so its sums stay short ----
+      uint32_t wv[SUB][4][GV];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) load_words(stg + (k & 1 ? v1_at : v0_at) + (16 * tt + (k & 2 ? 8 : 0)) * (DV / 2), wv[k]);
+      for (int q = 0; q < SUB; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          load_words(stg + (k & 1 ? v1_at : v0_at) + (16 * (t0 + q) + (k & 2 ? 8 : 0)) * (DV / 2), wv[q][k]);
 #pragma unroll
       for (int gv = 0; gv < GV; ++gv) {
         // halves of two keys' words side by side, nibbles 0..3 (x) and 4..7 (y), and with their bytes exchanged
-        const uint32_t x0[2] = {__byte_perm(wv[0][gv], wv[1][gv], 0x5410), __byte_perm(wv[0][gv], wv[1][gv], 0x4501)};
-        const uint32_t y0[2] = {__byte_perm(wv[0][gv], wv[1][gv], 0x7632), __byte_perm(wv[0][gv], wv[1][gv], 0x6723)};
-        const uint32_t x1[2] = {__byte_perm(wv[2][gv], wv[3][gv], 0x5410), __byte_perm(wv[2][gv], wv[3][gv], 0x4501)};
-        const uint32_t y1[2] = {__byte_perm(wv[2][gv], wv[3][gv], 0x7632), __byte_perm(wv[2][gv], wv[3][gv], 0x6723)};
+        uint32_t x[SUB][4][2];
+#pragma unroll
+        for (int q = 0; q < SUB; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = wv[q][k & 2][gv], hi = wv[q][(k & 2) + 1][gv];
+            x[q][k][0] = __byte_perm(lo, hi, k & 1 ? 0x7632 : 0x5410);
+            x[q][k][1] = __byte_perm(lo, hi, k & 1 ? 0x6723 : 0x4501);
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
-          // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
-          auto code = [&](const uint32_t (&v)[2]) { return (i & 1 ? v[i >> 1] : v[i >> 1] * sixteen) & 0x00f000f0u; };
-          uint32_t a0 = code(x0), a1 = code(y0), a2 = code(x1), a3 = code(y1);
-          const __half2 eight = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));   // -8 2^-20, twice
-          auto centre = [&](uint32_t v) {
-            const __half2 z = __hadd2(*reinterpret_cast<const __half2*>(&v), eight);
-            return *reinterpret_cast<const uint32_t*>(&z);
-          };
-          a0 = centre(a0); a1 = centre(a1); a2 = centre(a2); a3 = centre(a3);
+          float z[NB][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][gv][i], a0, a1, a2, a3, bh[nb][gv][0], bh[nb][gv][1]);
-          if constexpr (MODE != 0) {
+          for (int nb = 0; nb < NB; ++nb) z[nb][0] = z[nb][1] = z[nb][2] = z[nb][3] = 0.f;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][gv][i], a0, a1, a2, a3, bl[nb][gv][0], bl[nb][gv][1]);
+          for (int q = 0; q < SUB; ++q) {
+            // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
+            // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
+            const __half2 eight = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));   // -8 2^-20, twice
+            auto code = [&](const uint32_t (&v)[2]) {
+              const uint32_t w = (i & 1 ? v[i >> 1] : v[i >> 1] * sixteen) & 0x00f000f0u;
+              const __half2 c = __hadd2(*reinterpret_cast<const __half2*>(&w), eight);
+              return *reinterpret_cast<const uint32_t*>(&c);
+            };
+            const uint32_t a0 = code(x[q][0]), a1 = code(x[q][1]), a2 = code(x[q][2]), a3 = code(x[q][3]);
+            if constexpr (MODE != 0) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816(z[nb], a0, a1, a2, a3, bl[q][nb][gv][0], bl[q][nb][gv][1]);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(z[nb], a0, a1, a2, a3, bh[q][nb][gv][0], bh[q][nb][gv][1]);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            o[nb][gv][i][0] = add_f32x2(o[nb][gv][i][0], pack_f32x2(z[nb][0], z[nb][1]));
+            o[nb][gv][i][1] = add_f32x2(o[nb][gv][i][1], pack_f32x2(z[nb][2], z[nb][3]));
           }
         }
       }
-    }
-  };
+    };
 
-  for (int u = 0; u < n_mine; ++u) {
-    if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) {
-      ok = false;                               // gave up: the copies still in flight land first (bounded)
-      for (int v = u + 1; v < n_mine && v < u + NS; ++v) {
-        if (++slot == NS) { slot = 0; phase ^= 1; }
-        (void)mbar_wait_bounded(&bar[slot], phase);
+    for (int u = 0; u < n_mine; ++u) {
+      if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) {
+        ok = false;                               // gave up: the copies still in flight land first (bounded)
+        for (int v = u + 1; v < n_mine && v < u + NS; ++v) {
+          if (++slot == NS) { slot = 0; phase ^= 1; }
+          (void)mbar_wait_bounded(&bar[slot], phase);
+        }
+        break;
       }
-      break;
-    }
-    const unsigned char* stg = ring + slot * S::STAGE;
-    const int ks = (st0 + warp + u * WARPS) * SK;
-    if (ks + SK <= lim_all) {
+      const unsigned char* stg = ring + slot * S::STAGE;
+      const int ks = (st0 + warp + u * WARPS) * SK;
+      if (ks + SK <= lim_all) {
 #pragma unroll
-      for (int tt = 0; tt < SK / 16; tt += SUB) tiles(std::false_type{}, stg, tt, ks + 16 * tt);
-    } else {
+        for (int tt = 0; tt < SK / 16; tt += SUB) tiles(std::false_type{}, stg, tt, ks + 16 * tt);
+      } else {
 #pragma unroll 1
-      for (int tt = 0; tt < SK / 16 && ks + 16 * tt < k1; tt += SUB) tiles(std::true_type{}, stg, tt, ks + 16 * tt);
+        for (int tt = 0; tt < SK / 16 && ks + 16 * tt < k1; tt += SUB) tiles(std::true_type{}, stg, tt, ks + 16 * tt);
+      }
+      __syncwarp();                               // all lanes are done with this stage
+      if (lane == 0 && u + NS < n_mine) issue(u + NS);
+      if (++slot == NS) { slot = 0; phase ^= 1; }
     }
-    __syncwarp();                               // all lanes are done with this stage
-    if (lane == 0 && u + NS < n_mine) issue(u + NS);
-    if (++slot == NS) { slot = 0; phase ^= 1; }
-  }
 
-  // ---- merge the warps ----
+    // ---- merge the warps ----
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        l[nb][i] += __shfl_xor_sync(FULL_MASK, l[nb][i], x);
+        for (int x = 4; x < 32; x <<= 1) {
+          l[nb][i] += __shfl_xor_sync(FULL_MASK, l[nb][i], x);
 #pragma unroll
-        for (int gv = 0; gv < GV; ++gv) om[nb][gv][i] += __shfl_xor_sync(FULL_MASK, om[nb][gv][i], x);
-      }
-  __syncthreads();                              // rings drained: reuse them
-  float* sm_m = reinterpret_cast<float*>(smem);                 // [WARPS][ROWS]
-  float* sm_l = sm_m + WARPS * ROWS;
-  float* sm_o = sm_l + WARPS * ROWS;                            // [WARPS][ROWS][DV]
+          for (int gv = 0; gv < GV; ++gv) om[nb][gv][i] += __shfl_xor_sync(FULL_MASK, om[nb][gv][i], x);
+        }
+    __syncthreads();                              // rings drained: reuse them
+    float* sm_m = reinterpret_cast<float*>(smem);                 // [WARPS][ROWS]
+    float* sm_l = sm_m + WARPS * ROWS;
+    float* sm_o = sm_l + WARPS * ROWS;                            // [WARPS][ROWS][DV]
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 8 * nb + 2 * t + i;       // MODE 0: rows 0..3 in lanes t < 2
-      if (r == 0 && row < ROWS) {
-        sm_m[warp * ROWS + row] = ok ? m[nb][i] : NAN;
-        sm_l[warp * ROWS + row] = ok ? l[nb][i] : NAN;
-      }
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * nb + 2 * t + i;       // MODE 0: rows 0..3 in lanes t < 2
+        if (r == 0 && row < ROWS) {
+          sm_m[warp * ROWS + row] = ok ? m[nb][i] : NAN;
+          sm_l[warp * ROWS + row] = ok ? l[nb][i] : NAN;
+        }
 #pragma unroll
-      for (int gv = 0; gv < GV; ++gv) {
-        const float inv = vmul == 0.f ? 0.f : 1.0f / vmul;
+        for (int gv = 0; gv < GV; ++gv) {
+          const float inv = vmul == 0.f ? 0.f : 1.0f / vmul;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          constexpr float unit = 1048576.f;                     // 1 / the code's subnormal step
-          float lo = o[nb][gv][k][i], hi = o[nb][gv][k][2 + i];
-          if constexpr (MODE == 0) {
-            lo += __shfl_xor_sync(FULL_MASK, lo, 2);
-            hi += __shfl_xor_sync(FULL_MASK, hi, 2);
-          }
-          if (row < ROWS) {
-            float* dst = sm_o + (warp * ROWS + row) * DV + 64 * gv + 8 * r + k;
-            dst[0] = fmaf(lo * unit, inv, om[nb][gv][i]);
-            dst[4] = fmaf(hi * unit, inv, om[nb][gv][i]);
+          for (int k = 0; k < 4; ++k) {
+            constexpr float unit = 1048576.f;                     // 1 / the code's subnormal step
+            float lo = i ? f32x2_hi(o[nb][gv][k][0]) : f32x2_lo(o[nb][gv][k][0]);
+            float hi = i ? f32x2_hi(o[nb][gv][k][1]) : f32x2_lo(o[nb][gv][k][1]);
+            if constexpr (MODE == 0) {
+              lo += __shfl_xor_sync(FULL_MASK, lo, 2);
+              hi += __shfl_xor_sync(FULL_MASK, hi, 2);
+            }
+            if (row < ROWS) {
+              float* dst = sm_o + (warp * ROWS + row) * DV + 64 * gv + 8 * r + k;
+              dst[0] = fmaf(lo * unit, inv, om[nb][gv][i]);
+              dst[4] = fmaf(hi * unit, inv, om[nb][gv][i]);
+            }
           }
         }
       }
+    __syncthreads();
+    if (tid < ROWS) {
+      float M = M_NONE, Ls = 0.f;
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
+      for (int w = 0; w < WARPS; ++w) Ls += ex2(sm_m[w * ROWS + tid] - M) * sm_l[w * ROWS + tid];
+      s_M[tid] = M; s_L[tid] = Ls;
     }
-  __syncthreads();
-  if (tid < ROWS) {
-    float M = M_NONE, Ls = 0.f;
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
-    for (int w = 0; w < WARPS; ++w) Ls += ex2(sm_m[w * ROWS + tid] - M) * sm_l[w * ROWS + tid];
-    s_M[tid] = M; s_L[tid] = Ls;
-  }
-  __syncthreads();
-  const bool whole = st0 == 0 && st1 == stages;
-  const int rows_here = row_end - rt * ROWS;
-  // parts of shared units: a CTA keeps two, [0] of the unit that its run begins in, [1] of its last one
-  const int64_t my_part = ((int64_t)c * 2 + (x0 >= unit_at ? 0 : 1)) * ROWS;
-  for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
-    const int row = idx / DV, dd = idx % DV;
-    float tot = 0.f;
+    __syncthreads();
+    const bool whole = st0 == 0 && st1 == stages;
+    const int rows_here = row_end - rt * ROWS;
+    // parts of shared units: a CTA keeps two, [0] of the unit that its run begins in, [1] of its last one
+    const int64_t my_part = ((int64_t)c * 2 + (x0 >= unit_at ? 0 : 1)) * ROWS;
+    for (int idx = tid; idx < rows_here * DV; idx += THREADS) {
+      const int row = idx / DV, dd = idx % DV;
+      float tot = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) tot += ex2(sm_m[w * ROWS + row] - s_M[row]) * sm_o[(w * ROWS + row) * DV + dd];
-    if (whole) {
-      out_row(row)[dd] = s_L[row] == 0.f ? 0.f : tot / s_L[row];
-    } else {
-      const int64_t pi = my_part + row;
-      a.part_acc[pi * DV + dd] = tot;
-      if (dd == 0) { a.part_ml[2 * pi] = s_M[row]; a.part_ml[2 * pi + 1] = s_L[row]; }
+      for (int w = 0; w < WARPS; ++w) tot += ex2(sm_m[w * ROWS + row] - s_M[row]) * sm_o[(w * ROWS + row) * DV + dd];
+      if (whole) {
+        out_row(row)[dd] = s_L[row] == 0.f ? 0.f : tot / s_L[row];
+      } else {
+        const int64_t pi = my_part + row;
+        a.part_acc[pi * DV + dd] = tot;
+        if (dd == 0) { a.part_ml[2 * pi] = s_M[row]; a.part_ml[2 * pi + 1] = s_L[row]; }
+      }
     }
-  }
-  if (!whole) {
-    const int c0 = cta_of(unit_at), c1 = cta_of(unit_at + stages - 1);
-    __threadfence();
-    __syncthreads();
-    unsigned* counter = a.counters + (int64_t)b * units + unit;
-    if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-    __syncthreads();
-    if (s_last) {                               // the unit's last part: join them in order
+    if (!whole) {
+      const int c0 = cta_of(unit_at), c1 = cta_of(unit_at + stages - 1);
       __threadfence();
-      constexpr int EPT = ROWS * DV / THREADS;              // outputs per thread
-      constexpr int BLOCK = (S::BAR - S::QF) / (ROWS * 8) < 256 ? (S::BAR - S::QF) / (ROWS * 8) : 256;   // parts at a time
-      float2* s_ml = reinterpret_cast<float2*>(smem);       // [ROWS][BLOCK] (max, sum); then (weight, -)
-      const int first = c0 * 2 + (start_of(c0) >= unit_at ? 0 : 1);   // the others' parts are their [0]
-      auto part = [&](int cc) { return (int64_t)(cc == c0 ? first : 2 * cc) * ROWS; };
-      float acc[EPT];
+      __syncthreads();
+      unsigned* counter = a.counters + (int64_t)b * units + unit;
+      if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+      __syncthreads();
+      if (s_last) {                               // the unit's last part: join them in order
+        __threadfence();
+        constexpr int EPT = ROWS * DV / THREADS;              // outputs per thread
+        constexpr int BLOCK = (S::BAR - S::QF) / (ROWS * 8) < 256 ? (S::BAR - S::QF) / (ROWS * 8) : 256;   // parts at a time
+        float2* s_ml = reinterpret_cast<float2*>(smem);       // [ROWS][BLOCK] (max, sum); then (weight, -)
+        const int first = c0 * 2 + (start_of(c0) >= unit_at ? 0 : 1);   // the others' parts are their [0]
+        auto part = [&](int cc) { return (int64_t)(cc == c0 ? first : 2 * cc) * ROWS; };
+        float acc[EPT];
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) acc[e] = 0.f;
-      if (tid < ROWS) { s_M[tid] = M_NONE; s_L[tid] = 0.f; }
-      for (int cb = c0; cb <= c1; cb += BLOCK) {            // one pass, unless the unit has very many parts
-        const int n = min(BLOCK, c1 + 1 - cb);
-        __syncthreads();
-        for (int i = tid; i < ROWS * n; i += THREADS) {
-          const int cc = i / ROWS, row = i - cc * ROWS;
-          s_ml[row * BLOCK + cc] = row < rows_here ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + part(cb + cc) + row)
-                                                   : make_float2(M_NONE, 0.f);
-        }
-        __syncthreads();
-        for (int row = warp; row < ROWS; row += WARPS) {    // weights against the maximum so far
-          float M = s_M[row], den = 0.f;
-          const float before = M;
-          for (int cc = lane; cc < n; cc += 32) M = fmaxf(M, s_ml[row * BLOCK + cc].x);
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
-          for (int cc = lane; cc < n; cc += 32) {
-            const float2 ml = s_ml[row * BLOCK + cc];
-            const float w = ex2(ml.x - M);
-            den = fmaf(w, ml.y, den);
-            s_ml[row * BLOCK + cc].x = w;
+        for (int e = 0; e < EPT; ++e) acc[e] = 0.f;
+        if (tid < ROWS) { s_M[tid] = M_NONE; s_L[tid] = 0.f; }
+        for (int cb = c0; cb <= c1; cb += BLOCK) {            // one pass, unless the unit has very many parts
+          const int n = min(BLOCK, c1 + 1 - cb);
+          __syncthreads();
+          for (int i = tid; i < ROWS * n; i += THREADS) {
+            const int cc = i / ROWS, row = i - cc * ROWS;
+            s_ml[row * BLOCK + cc] = row < rows_here ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + part(cb + cc) + row)
+                                                     : make_float2(M_NONE, 0.f);
           }
+          __syncthreads();
+          for (int row = warp; row < ROWS; row += WARPS) {    // weights against the maximum so far
+            float M = s_M[row], den = 0.f;
+            const float before = M;
+            for (int cc = lane; cc < n; cc += 32) M = fmaxf(M, s_ml[row * BLOCK + cc].x);
 #pragma unroll
-          for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(FULL_MASK, den, x);
-          __syncwarp();
-          if (lane == 0) {
-            const float alpha = ex2(before - M);
-            s_L[row] = fmaf(s_L[row], alpha, den);
-            s_M[row] = M;
-            s_alpha[row] = alpha;
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
+            for (int cc = lane; cc < n; cc += 32) {
+              const float2 ml = s_ml[row * BLOCK + cc];
+              const float w = ex2(ml.x - M);
+              den = fmaf(w, ml.y, den);
+              s_ml[row * BLOCK + cc].x = w;
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(FULL_MASK, den, x);
+            __syncwarp();
+            if (lane == 0) {
+              const float alpha = ex2(before - M);
+              s_L[row] = fmaf(s_L[row], alpha, den);
+              s_M[row] = M;
+              s_alpha[row] = alpha;
+            }
+          }
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < EPT; ++e) acc[e] *= s_alpha[(tid + e * THREADS) / DV];
+          for (int cc = 0; cc < n; ++cc) {
+            const float* src = a.part_acc + part(cb + cc) * DV;
+            float v[EPT];
+#pragma unroll
+            for (int e = 0; e < EPT; ++e)
+              v[e] = (tid + e * THREADS) / DV < rows_here ? __ldcg(src + tid + e * THREADS) : 0.f;
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) acc[e] = fmaf(s_ml[(tid + e * THREADS) / DV * BLOCK + cc].x, v[e], acc[e]);
           }
         }
-        __syncthreads();
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) acc[e] *= s_alpha[(tid + e * THREADS) / DV];
-        for (int cc = 0; cc < n; ++cc) {
-          const float* src = a.part_acc + part(cb + cc) * DV;
-          float v[EPT];
-#pragma unroll
-          for (int e = 0; e < EPT; ++e)
-            v[e] = (tid + e * THREADS) / DV < rows_here ? __ldcg(src + tid + e * THREADS) : 0.f;
-#pragma unroll
-          for (int e = 0; e < EPT; ++e) acc[e] = fmaf(s_ml[(tid + e * THREADS) / DV * BLOCK + cc].x, v[e], acc[e]);
+        for (int e = 0; e < EPT; ++e) {
+          const int row = (tid + e * THREADS) / DV, dd = (tid + e * THREADS) % DV;
+          if (row < rows_here) out_row(row)[dd] = s_L[row] == 0.f ? 0.f : acc[e] / s_L[row];
         }
+        if (tid == 0) *counter = 0u;
       }
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const int row = (tid + e * THREADS) / DV, dd = (tid + e * THREADS) % DV;
-        if (row < rows_here) out_row(row)[dd] = s_L[row] == 0.f ? 0.f : acc[e] / s_L[row];
-      }
-      if (tid == 0) *counter = 0u;
     }
-  }
-  fence_proxy_async_smem();                     // the merge's writes before the next run's copies
-  __syncthreads();
+    fence_proxy_async_smem();                     // the merge's writes before the next run's copies
+    __syncthreads();
   }
 }
 
