@@ -12,22 +12,21 @@
 // filled by 1-D bulk copies (a head's codes and scales are contiguous in the cache).  Per 16 keys:
 //   S^T = K q^T   keys are the 16 rows of the MMA, query rows its 8 columns.  A 4-bit code u taken
 //                 out of a word by one AND is the float16 subnormal u 2^-24 (or u 2^-20 for the odd
-//                 nibble; V shifts every code there), so K needs 5 instructions per 8 codes; q is
-//                 scaled by a power of two per row so that its float16 loses nothing: bf16 as it is,
-//                 float32 as multiples of 2^-11 of the largest element, whose sums stay exact, and
-//                 what is left, summed apart.  Scale and midpoint of a group enter in float32 after
-//                 the product:
+//                 nibble), so K needs 5 instructions per 8 codes; q is scaled by a power of two per
+//                 row so that its float16 loses nothing: bf16 as it is, float32 as multiples of 2^-11
+//                 of the largest element, whose sums stay exact, and what is left, summed apart.
+//                 Scale and midpoint of a group enter in float32 after the product:
 //                   s = sum_g scale_g (u . q)_g + (mid_g - 8 scale_g) sum(q)_g.
 //   softmax       online, against a reference maximum that moves only when a score exceeds it by
 //                 more than 2^8, float32
 //   O^T += V^T P  value dims are the MMA's rows, keys its K axis.  The weights p * scale_g, two
 //                 float16 halves (22 bits) against a power of two that follows the largest scale,
 //                 turn from S^T's layout to the operand layout with movmatrix.  The codes are
-//                 centred (u - 8) in the operand: else O would be the small difference of sums of
-//                 positive codes.  (Centred by a second product with a constant -8 instead: 3-5%
-//                 slower.)  The tensor core cuts a sum off towards zero: kept in its accumulators,
-//                 the sums of 64 long sequences came out 7e-6 too small.  So it sums 16 or 32 keys,
-//                 which float32 additions join (4e-7; 1.5-4% slower, 15% with 16 rows).
+//                 centred in the operand, (u - 8) 2^-9 by one multiply-add of halves: else O would be
+//                 the small difference of sums of positive codes.  The tensor core cuts a sum off
+//                 towards zero: kept in its accumulators, the sums of 64 long sequences came out
+//                 7e-6 too small.  So it sums 16 or 32 keys, which float32 additions join (6e-7;
+//                 1-2% slower, 15% with 16 rows).
 //                 mid enters as sum p mid_g in float32.
 // With at most 4 query rows the two halves of the weights (and of q) share the 8 columns.  The
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
@@ -358,13 +357,16 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
     const int k_at = kr * (DK / 2) + t * (DK / 8), kp_at = S::KC + S::VC + kr * (GK * 4);
     const int v0_at = S::KC + kv0 * (DV / 2) + r * (GV * 4), v1_at = S::KC + kv1 * (DV / 2) + r * (GV * 4);
     const int vp_at = S::KC + S::VC + S::KP + kr * (GV * 4);
-    // factors that the compiler does not know: shifts to the left as products, on the multiply-add pipe (the
-    // logic pipe carries the unpacking)
-    uint32_t sixteen, two16;
-    asm volatile("mov.u32 %0, 16;\n mov.u32 %1, 65536;" : "=r"(sixteen), "=r"(two16));
+    // a factor that the compiler does not know: a shift to the left as a product, on the multiply-add pipe
+    // (the logic pipe carries the unpacking)
+    uint32_t two16;
+    asm volatile("mov.u32 %0, 65536;" : "=r"(two16));
     auto scale_of = [&](uint32_t w) { return __uint_as_float(w * two16); };   // bf16_lo
     [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on second halves
 
+    const __half2 times_even = __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800));   // 2^15
+    const __half2 times_odd = __halves2half2(__ushort_as_half(0x6800), __ushort_as_half(0x6800));    // 2^11
+    const __half2 centre = __halves2half2(__ushort_as_half(0xa400), __ushort_as_half(0xa400));       // -8 2^-9
     // SUB 16-key tiles of a stage from tile t0 on; kb: their first key.  TAIL: some key is hidden from some
     // column.
     auto tiles = [&](auto tail, const unsigned char* stg, int t0, int kb) {
@@ -569,12 +571,11 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           for (int nb = 0; nb < NB; ++nb) z[nb][0] = z[nb][1] = z[nb][2] = z[nb][3] = 0.f;
 #pragma unroll
           for (int q = 0; q < SUB; ++q) {
-            // nibble i at bits 4..7 of each half: u 2^-20.  (The tensor core aligns a subnormal as if it
-            // were 2^-14: at bits 0..3 the sums lost 4 more bits, 3e-5 of a row over 9000 flat keys.)
-            const __half2 eight = __halves2half2(__ushort_as_half(0x8080), __ushort_as_half(0x8080));   // -8 2^-20, twice
+            // nibble i of each half as the float16 subnormal u 2^-24 or u 2^-20, made (u - 8) 2^-9: the
+            // tensor core aligns a subnormal as if it were 2^-14, and the sums would lose as many bits
             auto code = [&](const uint32_t (&v)[2]) {
-              const uint32_t w = (i & 1 ? v[i >> 1] : v[i >> 1] * sixteen) & 0x00f000f0u;
-              const __half2 c = __hadd2(*reinterpret_cast<const __half2*>(&w), eight);
+              const uint32_t w = v[i >> 1] & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+              const __half2 c = __hfma2(*reinterpret_cast<const __half2*>(&w), i & 1 ? times_odd : times_even, centre);
               return *reinterpret_cast<const uint32_t*>(&c);
             };
             const uint32_t a0 = code(x[q][0]), a1 = code(x[q][1]), a2 = code(x[q][2]), a3 = code(x[q][3]);
@@ -646,7 +647,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           const float inv = vmul == 0.f ? 0.f : 1.0f / vmul;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            constexpr float unit = 1048576.f;                     // 1 / the code's subnormal step
+            constexpr float unit = 512.f;                         // 1 / the codes' step
             float lo = i ? f32x2_hi(o[nb][gv][k][0]) : f32x2_lo(o[nb][gv][k][0]);
             float hi = i ? f32x2_hi(o[nb][gv][k][1]) : f32x2_lo(o[nb][gv][k][1]);
             if constexpr (MODE == 0) {

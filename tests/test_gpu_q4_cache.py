@@ -4,9 +4,9 @@ the float64 definitions in oracle/q4_oracle.py.
 Tolerances.  Codes and scales of inputs whose quotients are exact are equal bit for bit.  Transformed
 inputs (norm, rotation) carry a float32 error of at most 4e-6 of the row's largest value, so a value
 read back is off by that plus scale / 2 plus half a bf16 step of mid (2^-9 |mid|).  Attention: the
-probabilities enter the product with V as two bf16 halves, each rounded by at most 2^-9, i.e. a
-weight is off by at most 2^-18 of itself; a float32 q likewise (bf16 q is exact), which moves a
-score s by up to 2^-18 sum |q k| and its weight by as much, relatively.  With |sum| terms of the inputs below
+bounds allow for weights of 17 significant bits or more (two bf16 halves; the kernel's float16 halves hold
+22), i.e. a weight is off by at most 2^-18 of itself, and for a float32 q likewise (bf16 q is exact),
+which moves a score s by up to 2^-18 sum |q k| and its weight by as much, relatively.  With |sum| terms of the inputs below
 (sum |q k| scale <= 12) a row is off by at most (2^-18 + 2 * 12 * 2^-18) < 1e-4 of sum p |v| when every
 rounding conspires; independent roundings leave the root of that, below 2e-5 of the row's norm,
 which is the bound used; float32 sums add less than 1e-6 to it.
@@ -273,6 +273,29 @@ def test_decode_flat_long_context_keeps_its_precision(K):
     value's size.  The weights' rounding (2^-18 each, independent) and the float32 sums leave an
     error below 2e-5 of the row's norm."""
     check_decode(K, seeded("flat-long"), 1, 1, 1, 2, 128, 128, [30001], 30004, "bf16", q_width=0.1)
+
+
+@pytest.mark.parametrize("G,D,L", [(8, 128, 100001), (2, 128, 100001), (16, 64, 50003)])
+def test_decode_long_sums_are_not_cut_off(K, G, D, L):
+    """Thousands of values a sum.  A score of at most 8 (base 2) takes up to 6 roundings of 2^-24, 2.9e-6 of
+    its weight, exp and the weight's halves 2^-22 + 2^-23: 3.3e-6 when all conspire.  Values of either
+    sign: errors and output are both root sums of p^2 v^2, so the row is off by less than that."""
+    check_decode(K, seeded("sums", G, D), 1, 1, 1, G, D, D, [L], (L + 3) // 4 * 4, "bf16", tol=3.3e-6)
+
+
+@pytest.mark.parametrize("G,T,D,Hkv,q_dt", [(2, 1, 64, 4, "bf16"), (3, 2, 64, 4, "f32"), (2, 8, 128, 4, "bf16")])
+def test_decode_many_short_instances(K, G, T, D, Hkv, q_dt):
+    """More units than the GPU holds at once, each of one or two stages, empty ones among them."""
+    lengths = [(0, 1, 31, 64, 33, 63, 2, 32, 64, 50)[b % 10] for b in range(800)]
+    check_decode(K, seeded("many", G, T, D), len(lengths), T, Hkv, G, D, D, lengths, 64, q_dt)
+
+
+@pytest.mark.parametrize("G,T", [(2, 1), (2, 4)])
+def test_decode_many_instances_and_a_long_one(K, G, T):
+    """More instances than a CTA has threads, a long one among short and empty ones."""
+    lengths = [(0, 1, 31, 64, 33)[b % 5] for b in range(300)]
+    lengths[137] = 1001
+    check_decode(K, seeded("mixed", G, T), len(lengths), T, 1, G, 64, 64, lengths, 1004, "bf16")
 
 
 def test_decode_lengths_on_the_device_rule(K):
