@@ -26,7 +26,7 @@
 //                 the small difference of sums of positive codes.  The tensor core cuts a sum off
 //                 towards zero: kept in its accumulators, the sums of 64 long sequences came out
 //                 7e-6 too small.  So it sums 16 or 32 keys, which float32 additions join (6e-7;
-//                 1-2% slower, 15% with 16 rows).
+//                 1-2% slower, 6% with 16 rows).
 //                 mid enters as sum p mid_g in float32.
 // With at most 4 query rows the two halves of the weights (and of q) share the 8 columns.  The
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
@@ -607,7 +607,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       const unsigned char* stg = ring + slot * S::STAGE;
       const int ks = (st0 + warp + u * WARPS) * SK;
       if (ks + SK <= lim_all) {
-#pragma unroll
+#pragma unroll 1                                // unrolled, 16 rows spill (64 blocks of 16 tokens: 151 us, so 139)
         for (int tt = 0; tt < SK / 16; tt += SUB) tiles(std::false_type{}, stg, tt, ks + 16 * tt);
       } else {
 #pragma unroll 1
@@ -790,11 +790,12 @@ bool decode_q4_supports(int Dk, int Dv) {
   return (Dk == 64 && Dv == 64) || (Dk == 128 && Dv == 128) || (Dk == 192 && Dv == 128);
 }
 
+// Query rows of a unit.  16 in one rather than 8 in two: 139 against 159 us on blocks of 32 rows a KV head.
 int decode_q4_row_tile(int rows) { return rows <= 4 ? 4 : (rows <= 8 ? 8 : 16); }
 
 // CTAs for `stages` stages of 32 keys in `units` units of at most `longest` stages.  Many units, none of them
 // long against what a CTA would get: one CTA each, in the order that the GPU takes them, and nothing to
-// join (61 sequences x 16 units of about 62 stages: 124 us against 141 in equal runs).  Else equal runs: as many as
+// join (61 sequences x 16 units of about 62 stages: 139 us against 146 in equal runs).  Else equal runs: as many as
 // the GPU holds at once, each with a stage per warp, and not so many that joining a unit's parts
 // (about 40 ns each, one CTA) costs more than its stages take (about 150 ns each, spread over the parts).
 int decode_q4_ctas(int Dk, int rows, int64_t stages, int64_t units, int64_t longest, int64_t all_units, int* whole) {
