@@ -451,8 +451,8 @@ kva_status kv_cache_expand_q4(
  *             bound: validation and planning).  A token that sees no slot (L - T + i < 0: a padding
  *             instance with L = 0, or a block longer than its sequence) gives a row of zeros.
  *  Probabilities meet the codes as two float16 halves (22 significant bits), a float32 q as two
- *  parts that hold 24 bits of its row's largest element; all sums are float32.  Slots at or beyond L are never used, whatever they
- *  hold.  Any Hq/Hkv.  1 <= T <= KVA_DECODE_Q4_MAX_BLOCK.
+ *  parts that hold 24 bits of its row's largest element; all sums are float32.  Slots at or
+ *  beyond L are never used, whatever they hold.  Any Hq/Hkv.  1 <= T <= KVA_DECODE_Q4_MAX_BLOCK.
  *  workspace  as for kv_attn_decode, sized by kva_decode_q4_workspace_size; zero before the first
  *             call (its first kva_decode_q4_workspace_zero_bytes bytes), left so by every call.
  *  Built for (Dk, Dv) = (64, 64), (128, 128) and (192, 128).  Errors as kv_attn_decode. */
