@@ -17,7 +17,9 @@
 // summed in 32 strided sums and then pairwise, products and sums of the rotation rounded apart, cosines
 // and sines within 3.5e-8 (rotation() below), quotients correctly rounded.
 //
-// Bound: HBM for long appends, but close to the issue slots.
+// Bound: issue slots.  512 tokens in 28 caches (16 + 8 + 8 heads of 128, bf16): 160 MB in 93 us, 63% of the
+// slots used with three CTAs an SM (two: 131 us with the read-back instead of 113; four, at 64 registers: 113, and
+// 114 instead of 94 where rows are 192 wide).  Its read-back, 75 MB in 20 us, uses 74%.
 //
 // Method: the append of the decode step (Youtu-VL-4B ncnn port, step 6) with per-head RMSNorm and
 // rotate-half RoPE (Penguin-VL ncnn port, sections 2.1 and 4.2; Youtu-VL-4B ncnn port,

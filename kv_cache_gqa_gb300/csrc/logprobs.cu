@@ -41,8 +41,8 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-// Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per token scored again.
-__host__ __device__ constexpr int merge_max(int TK) { return TK <= 16 ? 544 : 320; }
+// Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per candidate.
+__host__ __device__ constexpr int merge_max(int TK) { return TK <= 16 ? 512 : 320; }
 
 using u64 = unsigned long long;
 
@@ -636,13 +636,21 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ Stat s_stat[merge_max(TK) / 32];
   __shared__ int s_rank[TK];                            // candidate of each rank, -1: none
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  griddep_wait();
-  griddep_launch_dependents();
+  // While the last tiles end: the row and the given token's logit.  The kernel before this one let it start
+  // only after its own wait, so all that they read is complete.
   const int target = a.targets ? a.targets[b] : -1;
+  for (int k = tid; k < a.H; k += blockDim.x) s_h[k] = hidden_at(a, (int64_t)b * a.H + k);
   Stat st{-INFINITY, 0.f, 0.f};
   u64 L[TK];
 #pragma unroll
   for (int i = 0; i < TK; ++i) L[i] = 0ull;
+  __syncthreads();
+  if (warp == warps - 1) {
+    const float2 d = target >= 0 && target < a.V ? dot_again<WT>(a, s_h, target) : make_float2(0.f, 0.f);
+    if (lane == 0) s_val[TK] = d;
+  }
+  griddep_wait();
+  griddep_launch_dependents();
   if (tid < a.splits) {                                 // one split per thread: its list is sorted
     const int64_t slot = (int64_t)b * a.splits + tid;
     const float4 q = *reinterpret_cast<const float4*>(a.part_stat + slot * 4);
@@ -654,7 +662,6 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
       L[2 * i] = two.x; L[2 * i + 1] = two.y;
     }
   }
-  for (int k = tid; k < a.H; k += blockDim.x) s_h[k] = hidden_at(a, (int64_t)b * a.H + k);
   // lists and statistics: within the warps, then (second round) those of the warps in warp 0
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
@@ -678,8 +685,8 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   }
   auto id_of = [&](int c) { return (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)); };
 #pragma unroll 1
-  for (int c = warp; c <= TK; c += warps) {
-    const int v = c == TK ? target : (s_top[c] ? id_of(c) : -1);
+  for (int c = warp; c < TK; c += warps) {
+    const int v = s_top[c] ? id_of(c) : -1;
     float2 d = make_float2(0.f, 0.f);
     if (v >= 0 && v < a.V) d = dot_again<WT>(a, s_h, v);
     if (lane == 0) s_val[c] = d;
@@ -766,10 +773,10 @@ TcPlan tc_plan(int B, int V, int parts) {
   return p;
 }
 
-// One thread per split; a warp for each token scored again while the rows do not fill the GPU, else 4.
+// One thread per split; a warp for each candidate scored again while the rows do not fill the GPU, else 4.
 template <typename WT, int TK>
 cudaError_t launch_merge(const LogprobArgs& a, cudaStream_t s) {
-  const int threads = std::max((a.splits + 31) / 32 * 32, a.B <= SMS ? std::min(32 * (TK + 1), merge_max(TK)) : 128);
+  const int threads = std::max((a.splits + 31) / 32 * 32, a.B <= SMS ? std::min(32 * TK, merge_max(TK)) : 128);
   return launch_pdl(logprob_merge_kernel<WT, TK>, dim3(a.B), dim3(threads), sizeof(float) * a.H, s, a);
 }
 
