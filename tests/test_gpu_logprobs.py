@@ -114,6 +114,40 @@ def test_parity(K, B, H, V, wdt, hdt, norm, k):
     check(got, host(hd), Wh, V, k, nw, targets)
 
 
+# the streaming form's blocks of 1, 2, 4 and 8 rows, full and partly filled, long rows, more blocks than CTAs
+@pytest.mark.parametrize("B,H,V,wdt,hdt,norm,k", [
+    (2, 136, 333, "f32", "f32", True, 3), (3, 264, 1001, "f32", "bf16", True, 24), (4, 1024, 2050, "f32", "f32", True, 8),
+    (8, 520, 70, "bf16", "f32", False, 12), (9, 4096, 515, "f32", "f32", True, 5), (2, 4096, 130, "f32", "bf16", False, 1),
+    (2500, 8, 41, "f32", "f32", False, 2), (1, 4088, 260, "bf16", "bf16", True, 9)])
+def test_streaming_form(K, B, H, V, wdt, hdt, norm, k):
+    test_parity(K, B, H, V, wdt, hdt, norm, k)
+
+
+@pytest.mark.parametrize("wdt,hdt,norm", [("bf16", "f32", True), ("bf16", "bf16", False), ("f32", "f32", True), ("f32", "bf16", False)])
+def test_inputs_written_just_before_the_call(K, wdt, hdt, norm):
+    """Rows and targets change between calls that follow each other without a pause: each call sees its own."""
+    torch = _torch()
+    rng = seeded("fresh", wdt, hdt, norm)
+    B, H, V, calls = 3, 256, 2000, 6
+    hd, Wd, Wh, nw, _ = inputs(rng, B, H, V, wdt, hdt, norm)
+    nd = dev(nw) if norm else None
+    rows = [dev((3 * rng.standard_normal((B, H))).astype(np.float32)).to(hd.dtype) for _ in range(calls)]
+    picks = [rng.integers(0, V, B).astype(np.int32) for _ in range(calls)]
+    pd = [dev(x) for x in picks]
+    td = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ws = torch.empty(K.lmhead_logprobs_workspace_bytes(B, H, V, 1), dtype=torch.uint8, device="cuda")
+    lps = torch.empty((calls, B), device="cuda")
+    torch.cuda.synchronize()
+    for i in range(calls):
+        hd.copy_(rows[i])
+        td.copy_(pd[i])
+        K.lmhead_logprobs(hd, Wd, ws, targets=td, out_logprob=lps[i], norm_w=nd)
+    torch.cuda.synchronize()
+    for i in range(calls):
+        want = Q.logprobs(host(rows[i]), Wh, V, targets=picks[i], norm_w=nw if norm else None)[0]
+        assert np.allclose(host(lps[i]), want, rtol=0, atol=1e-4), f"call {i}"      # |z| < 40
+
+
 def test_vocabulary_shorter_than_the_table_and_the_model_size(K):
     rng = seeded("qwen")
     B, H, rows, V = 3, WL.QWEN3_HIDDEN, WL.QWEN3_VOCAB, WL.QWEN3_VOCAB - 267
