@@ -48,8 +48,9 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-// Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per candidate.
-__host__ __device__ constexpr int merge_max(int TK) { return TK <= 16 ? 512 : 320; }
+// Most threads of a merge CTA: at least one per split, and (lists of up to 16) a warp per candidate; no more
+// than the lists' registers allow.
+__host__ __device__ constexpr int merge_max(int TK) { return TK <= 24 ? 512 : 320; }
 
 using u64 = unsigned long long;
 
@@ -745,8 +746,9 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Candidates kept for top_k alternatives: the rest is room for neighbours that rounding exchanges.
-int list_len(int top_k) { return top_k <= 5 ? 8 : (top_k <= 8 ? 12 : (top_k <= 12 ? 16 : 32)); }
+// Candidates kept for top_k alternatives: the rest is room for neighbours that rounding exchanges.  (20
+// alternatives with lists of 24 instead of 32: 64 rows of 151936 153 to 118 us, 10 rows of 1325 46 to 34 us.)
+int list_len(int top_k) { return top_k <= 5 ? 8 : (top_k <= 8 ? 12 : (top_k <= 12 ? 16 : (top_k <= 20 ? 24 : 32))); }
 
 constexpr int SMS = 152;                      // grids are sized for the whole GPU; fewer SMs only take longer
 // Streaming form: batch rows of a CTA (1, 2, 4 or 8) and the vocabulary splits.
@@ -869,6 +871,7 @@ cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, c
     case 8: return launch_k<8>(a, w_dtype, tc ? &p : nullptr, s);
     case 12: return launch_k<12>(a, w_dtype, tc ? &p : nullptr, s);
     case 16: return launch_k<16>(a, w_dtype, tc ? &p : nullptr, s);
+    case 24: return launch_k<24>(a, w_dtype, tc ? &p : nullptr, s);
     default: return launch_k<32>(a, w_dtype, tc ? &p : nullptr, s);
   }
 }

@@ -100,6 +100,7 @@ CASES = [
     (33, 72, 513, "f32", "bf16", False, 4), (127, 256, 2049, "bf16", "bf16", False, 1), (128, 256, 1025, "bf16", "f32", False, 20),
     (129, 128, 1000, "bf16", "f32", True, 5), (300, 64, 333, "bf16", "bf16", False, 2), (1100, 64, 777, "bf16", "f32", True, 1),
     (1, 2048, 5000, "bf16", "bf16", False, 24), (4, 4096, 640, "bf16", "f32", True, 6), (1, 64, 24, "f32", "f32", False, 24),
+    (5, 64, 100, "bf16", "f32", True, 13), (70, 128, 6001, "bf16", "f32", True, 20), (2, 128, 700, "bf16", "bf16", False, 21),
 ]
 
 
@@ -118,7 +119,7 @@ def test_parity(K, B, H, V, wdt, hdt, norm, k):
 @pytest.mark.parametrize("B,H,V,wdt,hdt,norm,k", [
     (2, 136, 333, "f32", "f32", True, 3), (3, 264, 1001, "f32", "bf16", True, 24), (4, 1024, 2050, "f32", "f32", True, 8),
     (8, 520, 70, "bf16", "f32", False, 12), (9, 4096, 515, "f32", "f32", True, 5), (2, 4096, 130, "f32", "bf16", False, 1),
-    (2500, 8, 41, "f32", "f32", False, 2), (1, 4088, 260, "bf16", "bf16", True, 9)])
+    (2500, 8, 41, "f32", "f32", False, 2), (1, 4088, 260, "bf16", "bf16", True, 9), (3, 72, 90, "f32", "f32", False, 20)])
 def test_streaming_form(K, B, H, V, wdt, hdt, norm, k):
     test_parity(K, B, H, V, wdt, hdt, norm, k)
 
