@@ -454,7 +454,9 @@ kva_status kv_cache_expand_q4(
  *  parts that hold 24 bits of its row's largest element; all sums are float32.  Slots at or
  *  beyond L are never used, whatever they hold.  Any Hq/Hkv.  1 <= T <= KVA_DECODE_Q4_MAX_BLOCK.
  *  workspace  as for kv_attn_decode, sized by kva_decode_q4_workspace_size; zero before the first
- *             call (its first kva_decode_q4_workspace_zero_bytes bytes), left so by every call.
+ *             call (its first kva_decode_q4_workspace_zero_bytes bytes), left so by every call.  These
+ *             bytes are as many for every shape: one workspace of the largest size serves calls of
+ *             any B, T and heads, one after another (single tokens and draft blocks in turn).
  *  Built for (Dk, Dv) = (64, 64), (128, 128) and (192, 128).  Errors as kv_attn_decode. */
 #define KVA_DECODE_Q4_MAX_BLOCK 64
 kva_status kv_attn_decode_q4(

@@ -6,8 +6,9 @@
 // all units, in order, are cut into one equal run per CTA, as many CTAs as the GPU holds at once: a
 // CTA ends one unit, takes whole ones and begins the next, so that ragged contexts leave no tail and a
 // single long one still fills the GPU.  (Equal chunks of up to 2048 keys, one CTA each: 64 ragged sequences
-// 282 us against 278, two contexts of 100k 104 against 80.)  A unit that several CTAs share is joined by the last of them to finish.  The runs
-// follow from the lengths on the device: every CTA sums them itself.
+// 282 us against 278, two contexts of 100k 104 against 80.)  A unit that several CTAs share is joined by the last of them to finish:
+// they count themselves at the index of the first one, so that the counters lie in the same words of the workspace whatever
+// the call's shape.  The runs follow from the lengths on the device: every CTA sums them itself.
 //   A CTA's 4 warps are independent: warp w takes the stages w, w+4, ... of a run through a private ring,
 // filled by 1-D bulk copies (a head's codes and scales are contiguous in the cache).  Per 16 keys:
 //   S^T = K q^T   keys are the 16 rows of the MMA, query rows its 8 columns.  A 4-bit code u taken
@@ -691,7 +692,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       const int c0 = cta_of(unit_at), c1 = cta_of(unit_at + stages - 1);
       __threadfence();
       __syncthreads();
-      unsigned* counter = a.counters + (int64_t)b * units + unit;
+      unsigned* counter = a.counters + c0;        // only the last unit of a run goes on into the next one
       if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
       __syncthreads();
       if (s_last) {                               // the unit's last part: join them in order

@@ -926,13 +926,12 @@ static int64_t decode_q4_units(int Hkv, int Hq, int T, int* tile, int64_t* row_t
   *row_tiles = (rows + *tile - 1) / *tile;
   return (int64_t)Hkv * *row_tiles;
 }
-static size_t decode_q4_zero_bytes(int64_t counters) { return round_up(sizeof(unsigned) * (size_t)counters, 256); }
+// A workspace begins with its counters, as many whatever the call's shape: calls of several shapes share it.
+static size_t decode_q4_zero_bytes() { return round_up(sizeof(unsigned) * DECODE_Q4_MAX_RUNS, 256); }
 
 size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T) {
   if (B <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || T <= 0 || n_q_heads % n_kv_heads != 0) return 0;
-  int tile;
-  int64_t rt;
-  return decode_q4_zero_bytes((int64_t)B * decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt));
+  return decode_q4_zero_bytes();
 }
 
 size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T, int32_t max_len,
@@ -942,9 +941,9 @@ size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_h
     return 0;
   int tile;
   int64_t rt;
-  const int64_t units = (int64_t)B * decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt);
+  (void)decode_q4_units(n_kv_heads, n_q_heads, T, &tile, &rt);
   const size_t rows = (size_t)DECODE_Q4_MAX_RUNS * 2 * tile;      // two shared units a run
-  return decode_q4_zero_bytes(units) + round_up(sizeof(float) * rows * 2, 256) + sizeof(float) * rows * head_dim_v;
+  return decode_q4_zero_bytes() + round_up(sizeof(float) * rows * 2, 256) + sizeof(float) * rows * head_dim_v;
 }
 
 kva_status kv_attn_decode_q4(
@@ -984,7 +983,7 @@ kva_status kv_attn_decode_q4(
   const int ctas = decode_q4_ctas(Dk, (int)std::min<int64_t>((int64_t)(n_q_heads / Hkv) * T, 1 << 20), stages * units,
                                   used * units, longest, (int64_t)B * units, &whole);
   const size_t rows = whole ? 0 : (size_t)ctas * 2 * tile;
-  const size_t zero = decode_q4_zero_bytes(B * units), ml = round_up(sizeof(float) * rows * 2, 256);
+  const size_t zero = decode_q4_zero_bytes(), ml = round_up(sizeof(float) * rows * 2, 256);
   const size_t need = zero + ml + sizeof(float) * rows * Dv;
   if (workspace_bytes < need)
     return fail(KVA_EWORKSPACE, "4-bit decode workspace %zu bytes < %zu needed", workspace_bytes, need);

@@ -262,7 +262,7 @@ struct DecodeQ4Args {
   Q4Cache c;
   const int32_t* lengths;             // [B]
   float* out;                         // [B, T, Hq, Dv]
-  unsigned int* counters;             // [B, Hkv, RT] zero on entry, zero on exit
+  unsigned int* counters;             // [DECODE_Q4_MAX_RUNS], by a shared unit's first CTA; zero on entry, zero on exit
   float* part_acc;                    // [ctas, 2, rows, Dv] (equal runs)
   float* part_ml;                     // [ctas, 2, rows, 2]
   int B, T, Hq, RT, ctas;
