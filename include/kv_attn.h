@@ -375,8 +375,9 @@ size_t kva_lmhead_workspace_zero_bytes(int32_t B);
  *  top_ids      [B,top_k] int32, top_logprobs [B,top_k] float32 or NULL; top_k = 0: neither read
  *  workspace    kva_lmhead_logprobs_workspace_size(B, H, V, top_k) bytes, of any contents.  Calls
  *               sharing one workspace must not overlap on the GPU.
- *  0 <= top_k <= KVA_LOGPROBS_MAX_TOP and top_k <= V, else KVA_EINVAL.  NaN inputs are outside the
- *  contract (a row with one gives NaN or id -1).  Errors as lmhead_topk.  B == 0 is a no-op. */
+ *  0 <= top_k <= KVA_LOGPROBS_MAX_TOP and top_k <= V, else KVA_EINVAL.  A row with a
+ *  logit of NaN or +infinity, or whose kernel gave up a wait, gives NaN in its float outputs (a
+ *  negative target's 0 stays) and -1 in its ids.  Errors as lmhead_topk.  B == 0 is a no-op. */
 #define KVA_LOGPROBS_MAX_TOP 24
 kva_status lmhead_logprobs(
     const void* h, kva_dtype h_dtype, const float* norm_w, float eps, const void* W, kva_dtype w_dtype,

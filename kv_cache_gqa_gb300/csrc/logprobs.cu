@@ -367,7 +367,6 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t s_taddr;
-  __shared__ int s_err;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int w_bytes = p.N * 128, a_bytes = p.a_rows * 128;
   const int stage = w_bytes + p.parts * a_bytes;
@@ -386,7 +385,6 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], EPI_WARPS); }
     mbar_init(&drain, 1);
     fence_mbar_init();
-    s_err = 0;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -416,7 +414,6 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
             if (++s == p.stages) { s = 0; phase ^= 1; }
           }
       if (!ok) {                              // gave up: the copies in flight land first (bounded)
-        s_err = 1;
         for (int j = max(0, it - p.stages); j < it; ++j) (void)mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1);
       }
     }
@@ -443,7 +440,6 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
       if (ok) tc::mma_commit_elect(&acc_full[ab]);
     }
     if (!ok) {                                // gave up: the products in flight end first (bounded)
-      s_err = 1;
       tc::mma_commit_elect(&drain);
       (void)mbar_wait_bounded(&drain, 0);
     }
@@ -542,8 +538,7 @@ logprob_tc_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__
         list.clear();
       }
     }
-    if (!ok) {                                            // gave up: the rows of every pass are void
-      s_err = 1;
+    if (!ok) {                                            // gave up: the rows of every pass are void (the merge sees NaN)
       for (int ps = 0; ps < my_passes; ++ps) {
         const int b = (rb0 + ps * p.group) * MROWS + row;
         if (b >= a.B) continue;
@@ -727,6 +722,9 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
       du += __shfl_xor_sync(FULL_MASK, du, o);
     }
     const float sum = st.s + ds, ls = logf(sum);
+    // a sum of NaN: a wait gave up and part of the vocabulary is missing, or a logit is NaN or +infinity.  No id
+    // is the best then.
+    const bool lost = sum != sum;
     __syncwarp();
     auto logprob = [&](float2 z) { return ((z.x - st.m) + z.y) - ls; };
     if (lane == 0) {
@@ -736,7 +734,7 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
         a.out_logprob[b] = target < 0 ? 0.f : (target < a.V ? logprob(s_val[TK]) : __uint_as_float(0x7fc00000u));
     }
     if (lane < a.top_k) {
-      const int c = s_rank[lane];
+      const int c = lost ? -1 : s_rank[lane];
       const int64_t o = (int64_t)b * a.top_k + lane;
       a.top_ids[o] = c < 0 ? -1 : id_of(c);
       if (a.top_logprobs) a.top_logprobs[o] = c < 0 ? __uint_as_float(0x7fc00000u) : logprob(s_val[c]);
