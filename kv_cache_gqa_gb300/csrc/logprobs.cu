@@ -639,8 +639,8 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ Stat s_stat[merge_max(TK) / 32];
   __shared__ int s_rank[TK];                            // candidate of each rank, -1: none
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  // While the last tiles end: the row and the given token's logit.  The kernel before this one let it start
-  // only after its own wait, so all that they read is complete.
+  griddep_wait();
+  griddep_launch_dependents();
   const int target = a.targets ? a.targets[b] : -1;
   for (int k = tid; k < a.H; k += blockDim.x) s_h[k] = hidden_at(a, (int64_t)b * a.H + k);
   Stat st{-INFINITY, 0.f, 0.f};
@@ -648,12 +648,12 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
 #pragma unroll
   for (int i = 0; i < TK; ++i) L[i] = 0ull;
   __syncthreads();
-  if (warp == warps - 1) {
-    const float2 d = target >= 0 && target < a.V ? dot_again<WT>(a, s_h, target) : make_float2(0.f, 0.f);
-    if (lane == 0) s_val[TK] = d;
-  }
-  griddep_wait();
-  griddep_launch_dependents();
+  auto score = [&](int c, int v) {                      // the logit of token v (< 0: none) for entry c
+    const float2 d = v >= 0 && v < a.V ? dot_again<WT>(a, s_h, v) : make_float2(0.f, 0.f);
+    if (lane == 0) s_val[c] = d;
+  };
+  const bool idle = (warps - 1) * 32 >= a.splits;       // a last warp without splits takes the given token now
+  if (idle && warp == warps - 1) score(TK, target);
   if (tid < a.splits) {                                 // one split per thread: its list is sorted
     const int64_t slot = (int64_t)b * a.splits + tid;
     const float4 q = *reinterpret_cast<const float4*>(a.part_stat + slot * 4);
@@ -688,12 +688,7 @@ logprob_merge_kernel(const __grid_constant__ LogprobArgs a) {
   }
   auto id_of = [&](int c) { return (int)(0xffffffffu - (uint32_t)(s_top[c] & 0xffffffffull)); };
 #pragma unroll 1
-  for (int c = warp; c < TK; c += warps) {
-    const int v = s_top[c] ? id_of(c) : -1;
-    float2 d = make_float2(0.f, 0.f);
-    if (v >= 0 && v < a.V) d = dot_again<WT>(a, s_h, v);
-    if (lane == 0) s_val[c] = d;
-  }
+  for (int c = warp; c < (idle ? TK : TK + 1); c += warps) score(c, c == TK ? target : (s_top[c] ? id_of(c) : -1));
   if (tid < TK) s_rank[tid] = -1;
   __syncthreads();
   if (warp == 0) {

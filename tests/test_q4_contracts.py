@@ -1,6 +1,12 @@
 """What the header promises of the 4-bit cache calls and lmhead_logprobs, where it shows without a GPU:
 sizes, and the order in the kernels' sources."""
+import glob
+import os
+import re
+
 import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kv_cache_gqa_gb300", "csrc")
 
 
 @pytest.fixture(scope="module")
@@ -21,3 +27,48 @@ def test_decode_q4_counters_lie_in_the_same_bytes_whatever_the_shape(K):
     for B, Hkv, Hq, T in shapes:                               # the widest block's workspace serves the narrower ones
         need = L.kva_decode_q4_workspace_size(B, Hkv, Hq, T, 1000, 128)
         assert need <= L.kva_decode_q4_workspace_size(4096, 32, 512, 64, 1000, 128)
+
+
+def _block_end(src, at):
+    """Past the } of the { at src[at]."""
+    depth = 0
+    for end in range(at, len(src)):
+        depth += {"{": 1, "}": -1}.get(src[end], 0)
+        if depth == 0:
+            return end + 1
+    raise AssertionError("unbalanced braces")
+
+
+def _kernels():
+    """(file, kernel, body) of every __global__ function that waits for the kernel before it."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        src = re.sub(r"//[^\n]*", "", open(path).read())
+        for m in re.finditer(r"__global__[^;{]*?(\w+)\(const[^{]*\{", src):
+            body = src[m.end() - 1:_block_end(src, m.end() - 1)]
+            if "griddep_wait()" in body:
+                yield os.path.basename(path), m.group(1), body
+
+
+def _without_lambdas(text):
+    """A lambda runs where it is called, not where it stands."""
+    while True:
+        m = re.search(r"auto \w+ = \[&\]\([^)]*\)(?: -> \w+)? \{", text)
+        if not m:
+            return text
+        text = text[:m.start()] + text[_block_end(text, m.end() - 1):]
+
+
+READS = re.compile(r"\b[ap]\.\w+\s*\[|\b(?:__ldg|__ldcg|load1|load8|hidden_at|dot_again|tma_load_4d|bulk_g2s|load|issue)\s*[<(]")
+
+
+def test_no_kernel_reads_global_memory_before_its_dependency_wait():
+    """A kernel that starts while the one before it runs sees memory only after griddep_wait(): what earlier
+    kernels wrote is visible to the grid that has waited, however long ago they ended.  (Prefetches into L2
+    return no data.)"""
+    names = []
+    for path, kernel, body in _kernels():
+        names.append(kernel)
+        early = READS.search(_without_lambdas(body[:body.index("griddep_wait()")]))
+        assert not early, f"{path}: {kernel} reads before the wait: {early.group(0)}"
+    assert {"append_q4_kernel", "expand_q4_kernel", "decode_q4_kernel", "logprob_prep_kernel", "logprob_stream_kernel",
+            "logprob_tc_kernel", "logprob_merge_kernel", "decode_mma_kernel", "verify_tc_kernel"} <= set(names)
