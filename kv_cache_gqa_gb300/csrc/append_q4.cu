@@ -120,19 +120,19 @@ __device__ __forceinline__ float quotient(float a, float b, float r) {
 // lanes.  Returns the code word; *par = (scale, mid) packed for the group's first lane.
 __device__ __forceinline__ uint32_t quantise8(const uint64_t (&x)[4], uint32_t* par) {
   float lo = f32x2_lo(x[0]), hi = lo;
-  uint64_t sum = 0ull;                                  // NaN if an element is (fminf drops NaN)
+  uint64_t probe = 0ull;                                // sums of 0 x: NaN if an element is NaN (which fminf drops) or infinite
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     lo = fminf(fminf(lo, f32x2_lo(x[i])), f32x2_hi(x[i]));
     hi = fmaxf(fmaxf(hi, f32x2_lo(x[i])), f32x2_hi(x[i]));
-    sum = add_f32x2(sum, x[i]);
+    probe = fma_f32x2(x[i], 0ull, probe);
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(FULL_MASK, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(FULL_MASK, hi, o));
   }
-  const float all = f32x2_lo(sum) + f32x2_hi(sum);
+  const float all = f32x2_lo(probe) + f32x2_hi(probe);
   const unsigned any = __ballot_sync(FULL_MASK, all != all);
   const bool odd = ((any >> (threadIdx.x & 24)) & 0xffu) != 0;
   // the scale is rounded up, so 15 steps cover the spread; one below bf16's normal range is 0

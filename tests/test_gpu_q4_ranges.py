@@ -72,3 +72,40 @@ def test_tokens_and_draft_blocks_share_a_workspace(K):
         for b in range(n):
             ref = attend(q[b].double(), vk[b], vv[b], int(lengths[b]))
             assert row_rel_err(host(out[b]), host(ref)) <= ROW_REL, f"n={n} T={T} b={b}"
+
+
+# ---------------------------------------------------------------------------------------------
+# append and read-back
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("in_dt", ["f32", "bf16"])
+def test_groups_of_huge_values_whose_spread_is_finite(K, in_dt):
+    """Values up to 1.6e38 of either sign: their sums overflow, their spread does not.  The elements are
+    their groups' ends, far from a tie between codes, so a value read back is the definition's rounded to float32."""
+    torch = _torch()
+    T, D = 6, 128
+    x = np.zeros((1, T, 1, D), np.float64)
+    big = float(O.bf16_round(np.float64(1.6e38)))
+    sign = np.where(np.arange(D) % 2 == 0, 1.0, -1.0)
+    x[0, 0, 0] = big * sign                                    # a lane's even elements positive, its odd ones negative
+    x[0, 1, 0] = big * np.where(np.arange(D) % 8 < 4, 1.0, -1.0)
+    x[0, 2, 0] = 1.0e38 * sign
+    x[0, 3, 0, :64] = 0.9e38 * sign[:64]                       # huge beside small
+    x[0, 3, 0, 64:] = sign[64:]
+    x[0, 4, 0] = 2.0e38                                        # equal values whose sum overflows
+    x[0, 5, 0, :] = -1.6e38
+    x[0, 5, 0, ::2] = 0.0
+    x = O.store(x, in_dt)
+    slot = np.arange(T, dtype=np.int32)
+    cache = K.KVCacheQ4.zeros(1, 1, 8, D)
+    xd = dev(x.astype(np.float32), dt(in_dt))
+    K.kv_cache_append_q4(None, xd, xd, None, dev(slot), slot, cache, None, K.Rope("none"))
+    out = K.KVCache(*(torch.zeros((1, 1, T, D), device="cuda") for _ in range(2)))
+    K.kv_cache_expand_q4(cache, dev(slot), slot, out)
+    torch.cuda.synchronize()
+    u, scale, mid = Q.q4_quantise(x[0, :, 0])
+    assert np.all(np.isfinite(scale))
+    want = Q.q4_values(u, scale, mid)
+    for t in (out.k, out.v):
+        got = host(t)[0, 0]
+        assert np.all(np.isfinite(got))
+        assert np.max(np.abs(got - want)) <= 2.0 ** -24 * np.abs(want).max()
