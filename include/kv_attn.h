@@ -451,8 +451,10 @@ kva_status kv_cache_expand_q4(
  *  lengths    [B] valid slots, 0 <= L <= capacity (device) + lengths_host (host mirror or an upper
  *             bound: validation and planning).  A token that sees no slot (L - T + i < 0: a padding
  *             instance with L = 0, or a block longer than its sequence) gives a row of zeros.
- *  Probabilities meet the codes as two float16 halves (22 significant bits), a float32 q as two
- *  parts that hold 24 bits of its row's largest element; all sums are float32.  Slots at or
+ *  A weight (probability, between 1 and 2^5 at the row's largest score, times the scale of V) meets
+ *  the codes as two float16 halves: off by at most 2^-22 of itself and 2^-34 (2^-45 where
+ *  Hq/Hkv * T <= 4) of the largest scale of V in its group of 64 dims among the 16 or 32 keys of its
+ *  tile.  A float32 q is two parts that hold 24 bits of its row's largest element; all sums are float32.  Slots at or
  *  beyond L are never used, whatever they hold.  Any Hq/Hkv.  1 <= T <= KVA_DECODE_Q4_MAX_BLOCK.
  *  workspace  as for kv_attn_decode, sized by kva_decode_q4_workspace_size; zero before the first
  *             call (its first kva_decode_q4_workspace_zero_bytes bytes), left so by every call.  These

@@ -19,10 +19,15 @@
 //                 Scale and midpoint of a group enter in float32 after the product:
 //                   s = sum_g scale_g (u . q)_g + (mid_g - 8 scale_g) sum(q)_g.
 //   softmax       online, against a reference maximum that moves only when a score exceeds it by
-//                 more than 2^8, float32
-//   O^T += V^T P  value dims are the MMA's rows, keys its K axis.  The weights p * scale_g, two
-//                 float16 halves (22 bits) against a power of two that follows the largest scale,
-//                 turn from S^T's layout to the operand layout with movmatrix.  The codes are
+//                 more than 2^5, float32
+//   O^T += V^T P  value dims are the MMA's rows, keys its K axis.  The weights p * scale_g are two
+//                 float16 halves, 22 bits against a power of two that each tile and group takes from its
+//                 largest scale (2^9 to 2^10 where p = 1) and that leaves again with the products: a group or
+//                 key of large scale takes no bits from the others.  A weight below 2^-3 there loses bits to
+//                 float16's 2^-24: with S the tile's largest scale of the group it is off by at most
+//                 2^-22 of itself and 2^-34 S; with at most 4 rows the second halves are held 2^11
+//                 times, and it is 2^-45 S (the same with more rows took a product more: 144 us instead of 136 on
+//                 blocks).  They turn from S^T's layout to the operand layout with movmatrix.  The codes are
 //                 centred in the operand, (u - 8) 2^-9 by one multiply-add of halves: else O would be
 //                 the small difference of sums of positive codes.  The tensor core cuts a sum off
 //                 towards zero: kept in its accumulators, the sums of 64 long sequences came out
@@ -58,7 +63,7 @@ constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int SK = 32;                          // keys per stage
 constexpr int NS = 3;                           // ring stages per warp
-constexpr float RESCALE_LOG2 = 8.0f;            // a row's reference max lags its true max by <= 2^8
+constexpr float RESCALE_LOG2 = 5.0f;            // a row's reference max lags its true max by <= 2^5
 constexpr float GRID = 100663296.f;              // 1.5 2^26: adding it rounds to a multiple of 8
 constexpr float M_NONE = -3.0e38f;              // reference max of a row that has seen no key
 
@@ -348,7 +353,6 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       thr[nb][0] = thr[nb][1] = -INFINITY;        // (m + RESCALE_LOG2) in units of the raw score
       l[nb][0] = l[nb][1] = 0.f;
     }
-    float vtop = 0.f, vmul = 0.f;                 // power of two above every V scale so far; weights carry vmul = 2^6 / vtop
 
     // key order inside a 16-key tile: MMA row (and K index) j holds key sigma(j); adjacent rows and
     // every second row alternate between even and odd keys, which spreads the 64-byte rows over the
@@ -363,7 +367,12 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
     uint32_t two16;
     asm volatile("mov.u32 %0, 65536;" : "=r"(two16));
     auto scale_of = [&](uint32_t w) { return __uint_as_float(w * two16); };   // bf16_lo
-    [[maybe_unused]] const float minus_half = MODE == 0 && t >= 2 ? -1.f : 0.f;   // these lanes pass on second halves
+    // second halves are held 2^11 times: what float16 leaves of a weight is normal as long as the weight is.
+    // MODE 0: lanes t >= 2 pass on second halves and take their sums back
+    const bool second = MODE == 0 && t >= 2;
+    [[maybe_unused]] const uint64_t half_of = second ? pack_f32x2(2048.f, 2048.f) : pack_f32x2(1.f, 1.f);
+    [[maybe_unused]] const uint64_t half_less = second ? pack_f32x2(-2048.f, -2048.f) : 0ull;
+    const int half_exp = second ? 11 : 0;
 
     const __half2 times_even = __halves2half2(__ushort_as_half(0x7800), __ushort_as_half(0x7800));   // 2^15
     const __half2 times_odd = __halves2half2(__ushort_as_half(0x6800), __ushort_as_half(0x6800));    // 2^11
@@ -374,7 +383,9 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
       constexpr bool TAIL = decltype(tail)::value;
       float s[SUB][NB][4];                        // scores of keys kr (e = 0, 1) and kr + 8 (e = 2, 3); columns 2t, 2t + 1
       uint32_t vp[SUB][2][GV];                    // scales and midpoints of V
-      float top = 0.f;
+      float top[GV];                              // the largest scale of V in these tiles, by group
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv) top[gv] = 0.f;
       // ---- S^T: chains of products into the same accumulator interleave ----
       float d[SUB][NB][GK][QP][4];             // the halves of q apart: the first ones' sums stay exact
       uint32_t wk[SUB][2][2 * GK], kp[SUB][2][GK];
@@ -446,12 +457,12 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 #pragma unroll
           for (int gv = 0; gv < GV; ++gv) {
             if (TAIL && k0 + kr + 8 * hh >= k1) vp[q][hh][gv] = 0u;   // slots past the run may hold anything
-            top = fmaxf(top, scale_of(vp[q][hh][gv]));
+            top[gv] = fmaxf(top[gv], scale_of(vp[q][hh][gv]));
           }
       }
-      // ---- online softmax: move the references when a score or a scale outgrows them (rare) ----
+      // ---- online softmax: move the references when a score outgrows them (rare) ----
       float high[NB][2];
-      bool grow = top > vtop;
+      bool grow = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -462,16 +473,6 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           grow |= high[nb][i] > thr[nb][i];
         }
       if (__any_sync(FULL_MASK, grow)) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, x));
-        float ratio = 1.f;
-        if (top > vtop) {
-          const int e = max(exponent(top) + 1, 40);       // top < 2^(e-127) (or tiny)
-          const float now = pow2(260 - e);                // weights reach 2^8 * 2^6
-          vtop = pow2(min(e, 254));
-          ratio = vmul == 0.f ? 0.f : now / vmul;
-          vmul = now;
-        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float by[2];
@@ -490,7 +491,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
             }
 #pragma unroll
             for (int gv = 0; gv < GV; ++gv) om[nb][gv][i] *= alpha;
-            by[i] = alpha * ratio;
+            by[i] = alpha;
           }
           const uint64_t by2 = pack_f32x2(by[0], by[1]);
 #pragma unroll
@@ -501,6 +502,14 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
               o[nb][gv][k][1] = mul_f32x2(o[nb][gv][k][1], by2);
             }
         }
+      }
+      // ---- a power of two for these tiles' weights, by group: p = 1 at the largest scale becomes 2^9 .. 2^10, p = 2^5 2^15 ----
+      float vmul[GV], vinv[GV];
+#pragma unroll
+      for (int gv = 0; gv < GV; ++gv) {
+        const int e = min(max(exponent(__uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(top[gv])))) + 1, 14), 251);
+        vmul[gv] = pow2(264 - e);
+        vinv[gv] = pow2(e - 1 - half_exp);                // 2^9 / vmul: the codes' step is 2^-9
       }
       // ---- weights p * scale of V, per group: operand fragments of keys 2t, 2t + 1 (and + 8), column r ----
       uint32_t bh[SUB][NB][GV][2];
@@ -519,7 +528,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
         for (int gv = 0; gv < GV; ++gv)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const float mul = scale_of(vp[q][hh][gv]) * vmul, mid = bf16_hi(vp[q][hh][gv]);
+            const float mul = scale_of(vp[q][hh][gv]) * vmul[gv], mid = bf16_hi(vp[q][hh][gv]);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               float w[2];
@@ -538,7 +547,8 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
               const uint32_t hi = pack_f16x2(w[0], w[1]);
               const float2 f = unpack_f16x2(hi);
               if constexpr (MODE == 0) {                  // lanes t < 2: the first halves; t >= 2: what they leave
-                bh[q][nb][gv][hh] = transpose8x8(pack_f16x2(fmaf(f.x, minus_half, w[0]), fmaf(f.y, minus_half, w[1])));
+                const uint64_t z = fma_f32x2(pack_f32x2(f.x, f.y), half_less, mul_f32x2(pack_f32x2(w[0], w[1]), half_of));
+                bh[q][nb][gv][hh] = transpose8x8(pack_f16x2(f32x2_lo(z), f32x2_hi(z)));
               } else {
                 bh[q][nb][gv][hh] = transpose8x8(hi);
                 bl[q][nb][gv][hh] = transpose8x8(pack_f16x2(w[0] - f.x, w[1] - f.y));
@@ -589,8 +599,8 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            o[nb][gv][i][0] = add_f32x2(o[nb][gv][i][0], pack_f32x2(z[nb][0], z[nb][1]));
-            o[nb][gv][i][1] = add_f32x2(o[nb][gv][i][1], pack_f32x2(z[nb][2], z[nb][3]));
+            o[nb][gv][i][0] = fma_f32x2(pack_f32x2(z[nb][0], z[nb][1]), pack_f32x2(vinv[gv], vinv[gv]), o[nb][gv][i][0]);
+            o[nb][gv][i][1] = fma_f32x2(pack_f32x2(z[nb][2], z[nb][3]), pack_f32x2(vinv[gv], vinv[gv]), o[nb][gv][i][1]);
           }
         }
       }
@@ -645,10 +655,8 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
         }
 #pragma unroll
         for (int gv = 0; gv < GV; ++gv) {
-          const float inv = vmul == 0.f ? 0.f : 1.0f / vmul;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            constexpr float unit = 512.f;                         // 1 / the codes' step
             float lo = i ? f32x2_hi(o[nb][gv][k][0]) : f32x2_lo(o[nb][gv][k][0]);
             float hi = i ? f32x2_hi(o[nb][gv][k][1]) : f32x2_lo(o[nb][gv][k][1]);
             if constexpr (MODE == 0) {
@@ -657,8 +665,8 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
             }
             if (row < ROWS) {
               float* dst = sm_o + (warp * ROWS + row) * DV + 64 * gv + 8 * r + k;
-              dst[0] = fmaf(lo * unit, inv, om[nb][gv][i]);
-              dst[4] = fmaf(hi * unit, inv, om[nb][gv][i]);
+              dst[0] = lo + om[nb][gv][i];
+              dst[4] = hi + om[nb][gv][i];
             }
           }
         }

@@ -109,3 +109,129 @@ def test_groups_of_huge_values_whose_spread_is_finite(K, in_dt):
         got = host(t)[0, 0]
         assert np.all(np.isfinite(got))
         assert np.max(np.abs(got - want)) <= 2.0 ** -24 * np.abs(want).max()
+
+
+# ---------------------------------------------------------------------------------------------
+# attention over values of very different sizes
+# ---------------------------------------------------------------------------------------------
+# A weight is off by at most 2^-22 of itself, and by 2^-34 of the largest scale of V among the 16 keys beside it in
+# its group of 64 dims (2^-45 of the 32 keys with at most 4 query rows a KV head), where the largest probability is at
+# least 1.  The first is within ROW_REL.  The second moves each dim of the output by at most
+# 8 (the largest |u - 8|) x the tile's keys x 2^-34 S / Z, Z = sum exp(s - max s): slack() below, 8 = sqrt(64) times that
+# for the 64 dims of a group together.
+ROWS = [(2, 1, "bf16"), (4, 1, "f32"), (8, 1, "bf16"), (2, 8, "f32"), (16, 1, "bf16")]
+
+
+def run_decode(K, k, v, q, q_dt, L):
+    """kv_attn_decode_q4 over the quantised k, v [1,1,W,D] and the float64 result, both [T,Hq,D] on the host, and
+    Z of each row [T,Hq]."""
+    torch = _torch()
+    pk, pv = Q.q4_quantise(k), Q.q4_quantise(v)
+    T, Hq, D = q.shape
+    lengths = np.array([L], np.int32)
+    qd = dev(q.astype(np.float32), dt(q_dt))[None]
+    out = torch.full((1, T, Hq, v.shape[-1]), float("nan"), device="cuda")
+    ws = torch.zeros(K.decode_q4_workspace_bytes(1, k.shape[1], Hq, T, L, v.shape[-1]), dtype=torch.uint8, device="cuda")
+    K.kv_attn_decode_q4(qd, filled(K, *pk, *pv), dev(lengths), lengths, out, ws)
+    torch.cuda.synchronize()
+    ref = attend(qd[0].double(), dev(Q.q4_values(*pk)[0]), dev(Q.q4_values(*pv)[0]), L)
+    s = np.einsum("thd,jd->thj", host(qd[0]), Q.q4_values(*pk)[0, 0, :L]) / math.sqrt(D)
+    s = np.where(np.arange(L) < (L - T + 1 + np.arange(T))[:, None, None], s, -np.inf)
+    return host(out[0]), host(ref), np.exp(s - s.max(-1, keepdims=True)).sum(-1)
+
+
+def grouped(x):
+    return x.reshape(*x.shape[:-1], -1, 64)
+
+
+def slack(v, at, z):
+    """What the scales of slot `at` of v [1,1,W,D] may move the groups of the rows by, [T,Hq,groups]."""
+    few = z.size <= 4
+    S = Q.q4_quantise(v[0, 0, at])[1]
+    return 8.0 * 8.0 * (32 if few else 16) * 2.0 ** (-45 if few else -34) * S / z[..., None]
+
+
+def assert_groups_close(got, ref, more=0.0):
+    err = np.linalg.norm(grouped(got) - grouped(ref), axis=-1)
+    assert np.all(err <= ROW_REL * np.linalg.norm(grouped(ref), axis=-1) + more), np.max(err / np.linalg.norm(grouped(ref), axis=-1))
+
+
+@pytest.mark.parametrize("power", [-20, 20, 60])
+@pytest.mark.parametrize("G,T,q_dt", ROWS)
+def test_decode_groups_of_different_sizes(K, G, T, q_dt, power):
+    """The second 64 dims of V are 2^power times the first: each group is as precise as it would be alone."""
+    rng = seeded("groups", G, T, power)
+    L, W, D = 1203, 1204, 128
+    k, v = rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    v[..., 64:] *= 2.0 ** power
+    got, ref, _ = run_decode(K, k, v, rng.standard_normal((T, G, D)), q_dt, L)
+    assert_groups_close(got, ref)
+
+
+@pytest.mark.parametrize("at", [0, 600, 1202])
+@pytest.mark.parametrize("G,T,q_dt", ROWS)
+def test_decode_a_huge_value_that_no_token_attends(K, G, T, q_dt, at):
+    """One slot's V is 2^20 times the others' and its score, below -45, so low that its weight
+    vanishes: e^-45 2^20 is 2^-45 of one value, 2^-35 of the sum of 1200."""
+    rng = seeded("outlier", G, T, at)
+    L, W, D = 1203, 1204, 128
+    k, v = rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    v[0, 0, at] *= 2.0 ** 20
+    k[0, 0, at] = -8.0
+    q = np.abs(rng.standard_normal((T, G, D)))                 # the slot's score is -8 sum(q) / sqrt(D), about -72
+    assert q.sum(-1).min() * 8 / math.sqrt(D) > 45
+    got, ref, z = run_decode(K, k, v, q, q_dt, L)
+    assert_groups_close(got, ref, slack(v, at, z))
+
+
+@pytest.mark.parametrize("G,T,q_dt", [(1, 3, "f32"), (2, 8, "bf16"), (1, 16, "f32")])
+def test_decode_a_huge_value_that_earlier_tokens_do_not_see(K, G, T, q_dt):
+    """The last token of a block has a V 2^20 times the others': the tokens before it keep their precision."""
+    rng = seeded("hidden", G, T)
+    L, W, D = 1203, 1204, 128
+    k, v = rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    v[0, 0, L - 1] *= 2.0 ** 20
+    got, ref, z = run_decode(K, k, v, rng.standard_normal((T, G, D)), q_dt, L)
+    assert_groups_close(got, ref, slack(v, L - 1, z))
+
+
+@pytest.mark.parametrize("G,T,q_dt,lead", [(2, 1, "bf16", 13.0), (4, 1, "f32", 13.0), (8, 1, "bf16", 8.0), (2, 8, "f32", 8.0)])
+def test_decode_a_leading_key_with_a_tiny_value(K, G, T, q_dt, lead):
+    """One key takes nearly all the weight and its V is 2^-20 of the others': the output is the others', whose
+    weights are about e^-lead.  At lead 8 (2^-12) the floor 2^-34 is 2^-22 of such a weight; at 13 (2^-19), with
+    at most 4 rows, 2^-45 is 2^-26 of it."""
+    rng = seeded("sink", G, T)
+    L, W, D = 1203, 1204, 128
+    k, v = 0.3 * rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    v[0, 0, 3] *= 2.0 ** -20
+    q = np.abs(rng.standard_normal((T, G, D)))
+    q *= 100.0 / q.sum(-1, keepdims=True)                      # every row's elements sum to 100 (before rounding)
+    k[0, 0, 3] = lead * math.sqrt(D) / 100.0
+    got, ref, _ = run_decode(K, k, v, q, q_dt, L)
+    assert_groups_close(got, ref)
+
+
+@pytest.mark.parametrize("G,T,q_dt", ROWS)
+def test_decode_tiles_of_huge_values_that_no_token_attends(K, G, T, q_dt):
+    """The first 128 slots, a tile of each warp, are such slots: the tiles after them keep their precision.  1300
+    copies of the sequence, so that one CTA walks all of it."""
+    torch = _torch()
+    rng = seeded("tiles", G, T)
+    L, W, D, copies = 515, 516, 128, 1300
+    k, v = rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    v[0, 0, :128] *= 2.0 ** 20
+    k[0, 0, :128] = -8.0
+    q = np.abs(rng.standard_normal((T, G, D)))
+    assert q.sum(-1).min() * 8 / math.sqrt(D) > 45             # 128 e^-45 2^20 is 2^-27 of the sum of 387
+    pk, pv = Q.q4_quantise(k), Q.q4_quantise(v)
+    one = filled(K, *pk, *pv)
+    cache = K.KVCacheQ4(*(t.expand(copies, *t.shape[1:]).contiguous() for t in (one.k, one.v, one.k_scale, one.v_scale)))
+    lengths = np.full(copies, L, np.int32)
+    qd = dev(q.astype(np.float32), dt(q_dt)).expand(copies, T, G, D).contiguous()
+    out = torch.full((copies, T, G, D), float("nan"), device="cuda")
+    ws = torch.zeros(K.decode_q4_workspace_bytes(copies, 1, G, T, L, D), dtype=torch.uint8, device="cuda")
+    K.kv_attn_decode_q4(qd, cache, dev(lengths), lengths, out, ws)
+    torch.cuda.synchronize()
+    assert bool((out == out[:1]).all())
+    ref = attend(qd[0].double(), dev(Q.q4_values(*pk)[0]), dev(Q.q4_values(*pv)[0]), L)
+    assert_groups_close(host(out[0]), host(ref))
