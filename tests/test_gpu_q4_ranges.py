@@ -235,3 +235,129 @@ def test_decode_tiles_of_huge_values_that_no_token_attends(K, G, T, q_dt):
     assert bool((out == out[:1]).all())
     ref = attend(qd[0].double(), dev(Q.q4_values(*pk)[0]), dev(Q.q4_values(*pv)[0]), L)
     assert_groups_close(host(out[0]), host(ref))
+
+
+# ---------------------------------------------------------------------------------------------
+# long blocks and contexts
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("G,T,q_dt,Dk,Dv", [(2, 17, "bf16", 128, 128), (1, 33, "f32", 64, 64), (2, 64, "f32", 128, 128),
+                                            (4, 64, "bf16", 192, 128), (3, 63, "f32", 64, 64), (16, 64, "bf16", 128, 128),
+                                            (1, 64, "bf16", 192, 128)])
+def test_decode_blocks_up_to_the_longest(K, G, T, q_dt, Dk, Dv):
+    """Blocks of 17 to 64 tokens: of sequences longer and shorter than the block, empty and exactly as long."""
+    torch = _torch()
+    rng = seeded("blocks", G, T, q_dt, Dk)
+    Hkv, W = 2, 804
+    lengths = np.array([801, 5, 0, T, T + 1, 97], np.int32)
+    B, Hq = len(lengths), Hkv * G
+    pk, pv = random_q4(rng, B, Hkv, W, Dk), random_q4(rng, B, Hkv, W, Dv)
+    q = dev(rng.standard_normal((B, T, Hq, Dk)).astype(np.float32), dt(q_dt))
+    out = torch.full((B, T, Hq, Dv), float("nan"), device="cuda")
+    ws = torch.zeros(K.decode_q4_workspace_bytes(B, Hkv, Hq, T, W, Dv), dtype=torch.uint8, device="cuda")
+    K.kv_attn_decode_q4(q, filled(K, *pk, *pv), dev(lengths), lengths, out, ws)
+    torch.cuda.synchronize()
+    vk, vv = dev(Q.q4_values(*pk)), dev(Q.q4_values(*pv))
+    for b, L in enumerate(lengths):
+        empty = max(0, T - int(L))
+        got = host(out[b])
+        assert np.all(got[:empty] == 0), f"L={L}: rows that see nothing"
+        if empty < T:
+            ref = host(attend(q[b].double(), vk[b], vv[b], int(L)))
+            assert row_rel_err(got[empty:], ref[empty:]) <= ROW_REL, f"L={L}"
+
+
+@pytest.mark.parametrize("G,T", [(2, 1), (8, 2)])
+def test_decode_one_unit_of_very_many_parts(K, G, T):
+    """600001 slots of one KV head: more parts than the last CTA joins in one pass (256)."""
+    rng = seeded("parts", G, T)
+    L, W, D = 600001, 600004, 64
+    k, v = rng.standard_normal((1, 1, W, D)), rng.standard_normal((1, 1, W, D))
+    torch = _torch()
+    pk, pv = Q.q4_quantise(k), Q.q4_quantise(v)
+    lengths = np.array([L], np.int32)
+    q = dev(rng.standard_normal((1, T, G, D)).astype(np.float32), torch.bfloat16)
+    out = torch.full((1, T, G, D), float("nan"), device="cuda")
+    ws = torch.zeros(K.decode_q4_workspace_bytes(1, 1, G, T, L, D), dtype=torch.uint8, device="cuda")
+    K.kv_attn_decode_q4(q, filled(K, *pk, *pv), dev(lengths), lengths, out, ws)
+    torch.cuda.synchronize()
+    ref = attend(q[0].double(), dev(Q.q4_values(*pk)[0]), dev(Q.q4_values(*pv)[0]), L)
+    assert row_rel_err(host(out[0]), host(ref)) <= ROW_REL
+
+
+# ---------------------------------------------------------------------------------------------
+# long appends and far positions
+# ---------------------------------------------------------------------------------------------
+def append_and_check(K, rng, N, T, Hkv, G, Dk, Dv, in_dt, q_dt, rope, pos, norm, after, with_q):
+    """kv_cache_append_q4 of random rows against the float64 transform and quantiser's bounds.  bf16 has 8
+    significant bits: a rounding is off by at most 2^-8 of the value (half its eps of 2^-7)."""
+    torch = _torch()
+    W, first = (T + 5 + 3) // 4 * 4, 2
+    Hq = Hkv * G
+    q, k, v = (O.store(rng.standard_normal(s), in_dt) for s in ((N, T, Hq, Dk), (N, T, Hkv, Dk), (N, T, Hkv, Dv)))
+    qw, kw = ((1 + 0.2 * rng.standard_normal((N, Dk))).astype(np.float32) for _ in range(2))
+    slot = np.arange(first, first + T, dtype=np.int32)
+    cache = K.KVCacheQ4.zeros(N, Hkv, W, Dk, Dv)
+    for t in (cache.k, cache.v):
+        t.fill_(0xA5)
+    q_out = torch.full((N, T, Hq, Dk), float("nan"), dtype=dt(q_dt), device="cuda") if with_q else None
+    f = lambda x: dev(x.astype(np.float32), dt(in_dt))   # noqa: E731
+    K.kv_cache_append_q4(f(q) if with_q else None, f(k), f(v), dev(pos) if pos is not None else None, dev(slot), slot, cache,
+                         q_out, K.Rope(**rope), q_norm_w=dev(qw) if norm else None, k_norm_w=dev(kw) if norm else None,
+                         norm_after_rope=after, norm_inst_stride=Dk if norm else 0)
+    torch.cuda.synchronize()
+    kinds = dict(rope)
+    if "rot_dim" not in kinds:
+        kinds["rot_dim"] = None
+    r = O.Rope(**kinds)
+    uk, sk, mk = Q.q4_unpack(cache.k.cpu().numpy()), host(cache.k_scale)[..., 0], host(cache.k_scale)[..., 1]
+    uv, sv, mv = Q.q4_unpack(cache.v.cpu().numpy()), host(cache.v_scale)[..., 0], host(cache.v_scale)[..., 1]
+    rest = np.ones(W, bool)
+    rest[slot] = False
+    assert bool((cache.k[:, :, rest] == 0xA5).all()) and bool((cache.v[:, :, rest] == 0xA5).all())
+    for n in range(N):
+        p = pos[n] if pos is not None else None
+        if with_q:
+            want = O.qk_transform(q[n], p, qw[n] if norm else None, 1e-6, r, after)
+            off = np.abs(host(q_out[n]) - want)
+            assert np.all(off <= np.abs(want) * (2.0 ** -8 if q_dt == "bf16" else 0) + 4e-6 * np.abs(want).max(-1, keepdims=True))
+        for x, u, scale, mid, exact in ((O.qk_transform(k[n], p, kw[n] if norm else None, 1e-6, r, after), uk[n], sk[n], mk[n], False),
+                                        (v[n], uv[n], sv[n], mv[n], True)):
+            x = x.transpose(1, 0, 2)                           # [Hkv, T, D]
+            u, scale, mid = u[:, slot], scale[:, slot], mid[:, slot]
+            g = x.reshape(*x.shape[:-1], -1, 64)
+            # float32 steps before the quantiser (4e-6, as in the transforms' test); none for V
+            slack = (0.0 if exact else 4e-6) * np.abs(x).max(-1)[..., None] + 2.0 ** -22 * np.abs(mid)
+            off = np.abs(Q.q4_values(u, scale, mid).reshape(g.shape) - g)
+            assert np.all(off <= (scale / 2 + np.abs(mid) * 2.0 ** -8 + slack)[..., None])
+            spread = g.max(-1) - g.min(-1)
+            assert np.all(15 * scale <= (spread + 2 * slack) * (1 + 2.0 ** -7)) and np.all(15 * scale >= spread - 2 * slack)
+
+
+@pytest.mark.parametrize("N,T,Hkv,G,Dk,Dv,in_dt,q_dt,rope,axes,norm,after,with_q", [
+    (28, 181, 2, 2, 128, 128, "bf16", "bf16", dict(kind="1d", base=1e6), 1, True, False, True),
+    (1, 4999, 1, 3, 64, 64, "f32", "f32", dict(kind="1d", base=1e4, rot_offset=5, rot_dim=22), 1, True, False, True),
+    (2, 2501, 3, 1, 192, 128, "f32", "bf16", dict(kind="interleaved", base=1e6, rot_offset=128, rot_dim=64), 1, False, False, False),
+    (7, 701, 2, 2, 256, 64, "bf16", "f32", dict(kind="2d", base=1e4), 2, True, True, True),
+    (1, 4867, 4, 1, 128, 192, "f32", "f32", dict(kind="sections", base=1.11588e7, sections=(16, 16, 16, 16)), 4, True, True, False),
+    (3, 1627, 5, 1, 64, 256, "bf16", "bf16", dict(kind="none"), 0, True, False, True),
+])
+def test_long_appends(K, N, T, Hkv, G, Dk, Dv, in_dt, q_dt, rope, axes, norm, after, with_q):
+    """Enough tokens that a warp takes one each and a CTA eight; the last CTA of an instance is partly filled."""
+    assert N * T >= 4864 and T % 8 != 0
+    rng = seeded("long append", N, T, Dk, Dv)
+    pos = rng.integers(-2000, 130000, (N, T, axes)).astype(np.int32) if axes else None
+    append_and_check(K, rng, N, T, Hkv, G, Dk, Dv, in_dt, q_dt, rope, pos, norm, after, with_q)
+
+
+@pytest.mark.parametrize("rope,axes,Dk", [(dict(kind="1d", base=1e6), 1, 128), (dict(kind="interleaved", base=1e4), 1, 64),
+                                          (dict(kind="sections", base=1.11588e7, sections=(16, 16, 16, 16)), 4, 128),
+                                          (dict(kind="2d", base=1e4), 2, 64)])
+def test_far_and_negative_positions(K, rope, axes, Dk):
+    """Positions on both sides of +-2^20, where the angle passes from pairs of floats to float64, up to the ends of
+    32 bits.  There float64 rounds an angle of 2^31 by 2^-22, as the definition does: 2.4e-7 each."""
+    rng = seeded("far positions", rope["kind"])
+    at = np.array([0, -1, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, -(1 << 20) + 1, -(1 << 20), -(1 << 20) - 1, 12345678, -98765432,
+                   (1 << 31) - 1, -(1 << 31), 999999999], np.int64)
+    T = len(at)
+    pos = np.stack([np.roll(at, a) for a in range(axes)], -1)[None].astype(np.int32)
+    append_and_check(K, rng, 1, T, 2, 2, Dk, 64, "f32", "f32", rope, pos, False, False, True)
