@@ -535,6 +535,8 @@ def _slots(slot, slot_host, slot_inst_stride, N, T):
         shared = slot.dim() < 2 or (slot.shape[0] == 1 and N != 1)
         _want(slot, "slot", (T,) if slot.dim() < 2 else (1 if shared else N, T), (torch.int32,))
         slot_inst_stride = 0 if shared else T
+    else:
+        _want(slot, "slot", tuple(slot.shape), (torch.int32,))
     need = (N - 1) * slot_inst_stride + T if N > 0 and T > 0 else 0
     if sh.size < need or slot.numel() < need:
         raise KvaError(KVA_EINVAL, f"slot and slot_host must hold {need} slots")
