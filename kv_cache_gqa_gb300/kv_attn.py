@@ -560,12 +560,16 @@ def prepare_append_q4(q, k, v, pos, slot, slot_host, cache: KVCacheQ4, q_out, ro
         _want(q, "q", (N, T, None, cache.head_dim), (k.dtype,))
         if q_out is not None:
             _want(q_out, "q_out", tuple(q.shape), _floats())
-    if pos_inst_stride is None:
+    shared = pos_inst_stride is None
+    if shared:
         pos_inst_stride = 0 if (pos is None or pos.dim() < 3 or pos.shape[0] == 1) else pos.shape[1] * pos.shape[2]
     if rope.kind != "none" and pos is not None:
         if pos.dtype != torch.int32 or not pos.is_contiguous() or pos.shape[-1] != rope.n_axes or \
                 pos.numel() < max(0, N - 1) * pos_inst_stride + T * rope.n_axes:
             raise KvaError(KVA_EINVAL, f"pos must be contiguous int32 [N|1, {T}, {rope.n_axes}]")
+        if shared and pos.dim() == 2 and pos.shape[0] != T:    # [N, n_axes] of one token each: every instance would read the first
+            raise KvaError(KVA_EINVAL, f"pos {tuple(pos.shape)}: one of {N} instances is [{N}, {T}, {rope.n_axes}], a shared one "
+                           f"[{T}, {rope.n_axes}]")
     for w, name in ((q_norm_w, "q_norm_w"), (k_norm_w, "k_norm_w")):
         if w is not None and (w.dtype != torch.float32 or not w.is_contiguous() or
                               w.numel() < max(0, N - 1) * norm_inst_stride + cache.head_dim):
