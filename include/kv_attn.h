@@ -403,7 +403,7 @@ size_t kva_lmhead_logprobs_workspace_size(int32_t B, int32_t H, int32_t V, int32
  *     k_scale, v_scale  bf16 pairs (scale, mid), G a row
  *  Instance i starts inst_rows rows after instance i - 1 in all four arrays (0: n_kv_heads *
  *  capacity).  head_dim and head_dim_v (0: head_dim) are multiples of 64 up to 256, capacity is a
- *  multiple of 4 (else KVA_EALIGN), pointers are 16-byte aligned, inst_rows is a multiple of 4. */
+ *  multiple of 4 (else KVA_EALIGN) and at most 2^31 - 65, pointers are 16-byte aligned, inst_rows is a multiple of 4. */
 typedef struct {
   void* k;
   void* v;

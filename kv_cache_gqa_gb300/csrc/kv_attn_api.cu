@@ -207,6 +207,8 @@ kva_status check_cache_q4(kva_cache_q4& c, int n_instances) {
   if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k_scale) || !aligned16(c.v_scale))
     return fail(KVA_EALIGN, "4-bit cache pointers must be 16-byte aligned");
   if (c.n_kv_heads > 65535) return fail(KVA_EUNSUPPORTED, "4-bit cache: more than 65535 KV heads");
+  if (c.capacity > INT32_MAX - 64)                // lengths round up to stages of 32 in 32 bits
+    return fail(KVA_EUNSUPPORTED, "4-bit cache: capacity %d within 64 of 2^31", c.capacity);
   return KVA_OK;
 }
 

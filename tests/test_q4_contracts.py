@@ -4,6 +4,7 @@ import glob
 import os
 import re
 
+import numpy as np
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kv_cache_gqa_gb300", "csrc")
@@ -72,3 +73,16 @@ def test_no_kernel_reads_global_memory_before_its_dependency_wait():
         assert not early, f"{path}: {kernel} reads before the wait: {early.group(0)}"
     assert {"append_q4_kernel", "expand_q4_kernel", "decode_q4_kernel", "logprob_prep_kernel", "logprob_stream_kernel",
             "logprob_tc_kernel", "logprob_merge_kernel", "decode_mma_kernel", "verify_tc_kernel"} <= set(names)
+
+
+def test_capacities_at_the_end_of_32_bits_are_refused(K):
+    """A length just below 2^31 does not round up to whole stages in 32 bits."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("dummy addresses: runs on hosts without a GPU")
+    L, at = K.lib(), 1 << 20
+    lengths = np.array([5], np.int32)
+    cache = K._CacheQ4(at, at, at, at, 1, 64, (1 << 31) - 4, 0, 0)
+    assert L.kv_attn_decode_q4(at, 1, cache, at, lengths.ctypes.data, 1, 1, 1, 0.0, at, at, 1 << 30, None) == K.KVA_EUNSUPPORTED
+    lengths[0] = cache.capacity
+    assert L.kv_attn_decode_q4(at, 1, cache, at, lengths.ctypes.data, 1, 1, 1, 0.0, at, at, 1 << 30, None) == K.KVA_EUNSUPPORTED
