@@ -429,16 +429,7 @@ expand_q4_kernel(const __grid_constant__ ExpandQ4Args a) {
   griddep_launch_dependents();
 }
 
-int num_sms_q4() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        n <= 0)
-      n = 152;
-  }
-  return n;
-}
+constexpr int SMS = 152;          // grids are sized for the whole GPU; fewer SMs only take longer
 
 template <typename InT, typename QOutT, bool ALIGNED, int TOK>
 cudaError_t launch_t(const AppendQ4Args& a, cudaStream_t s) {
@@ -447,7 +438,7 @@ cudaError_t launch_t(const AppendQ4Args& a, cudaStream_t s) {
                        ((int64_t)a.c.Hkv * (a.c.Dv / Q4_GROUP) + 3) / 4;
   // few tokens spread their rows over CTAs, about two per SM
   const int64_t ctas = (int64_t)((a.T + TOK - 1) / TOK) * a.N, most = (sets + WARPS / TOK - 1) / (WARPS / TOK);
-  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(most, 2 * num_sms_q4() / ctas));
+  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(most, 2 * SMS / ctas));
   const dim3 grid((a.T + TOK - 1) / TOK, a.N, groups);
   if (D <= 64) return launch_pdl(append_q4_kernel<InT, QOutT, 8, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
   if (D <= 128) return launch_pdl(append_q4_kernel<InT, QOutT, 16, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
@@ -457,7 +448,7 @@ cudaError_t launch_t(const AppendQ4Args& a, cudaStream_t s) {
 // A token per warp once that leaves four CTAs per SM.
 template <typename InT, typename QOutT, bool ALIGNED>
 cudaError_t launch_w(const AppendQ4Args& a, cudaStream_t s) {
-  return (int64_t)a.T * a.N >= (int64_t)4 * TOKENS * num_sms_q4() ? launch_t<InT, QOutT, ALIGNED, TOKENS>(a, s)
+  return (int64_t)a.T * a.N >= (int64_t)4 * TOKENS * SMS ? launch_t<InT, QOutT, ALIGNED, TOKENS>(a, s)
                                                                   : launch_t<InT, QOutT, ALIGNED, 1>(a, s);
 }
 
