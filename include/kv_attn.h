@@ -373,8 +373,9 @@ size_t kva_lmhead_workspace_zero_bytes(int32_t B);
  *               (a padded row): its logprob is 0.  A target >= V has logprob NaN.
  *  out_logprob  [B] float32 (needs targets);  out_entropy, out_lse [B] float32: each may be NULL
  *  top_ids      [B,top_k] int32, top_logprobs [B,top_k] float32 or NULL; top_k = 0: neither read
- *  workspace    kva_lmhead_logprobs_workspace_size(B, H, V, top_k) bytes, of any contents.  Calls
- *               sharing one workspace must not overlap on the GPU.
+ *  workspace    kva_lmhead_logprobs_workspace_size(B, H, V, top_k) bytes, of any contents, which also
+ *               serve calls of fewer rows or alternatives over the same H and V.  Calls sharing one
+ *               workspace must not overlap on the GPU.
  *  0 <= top_k <= KVA_LOGPROBS_MAX_TOP and top_k <= V, else KVA_EINVAL.  A row with a
  *  logit of NaN or +infinity, or whose kernel gave up a wait, gives NaN in its float outputs (a
  *  negative target's 0 stays) and -1 in its ids.  Errors as lmhead_topk.  B == 0 is a no-op. */

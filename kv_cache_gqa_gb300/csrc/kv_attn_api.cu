@@ -798,7 +798,7 @@ kva_status lmhead_topk(
 
 size_t kva_lmhead_logprobs_workspace_size(int32_t B, int32_t H, int32_t V, int32_t top_k) {
   if (B <= 0 || H <= 0 || V <= 0 || top_k < 0 || top_k > LOGPROB_TOP_MAX) return 0;
-  return logprob_workspace_bytes(B, H, V, top_k);
+  return logprob_workspace_bound(B, H, V, top_k);
 }
 
 kva_status lmhead_logprobs(

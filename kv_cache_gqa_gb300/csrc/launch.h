@@ -299,7 +299,8 @@ struct LogprobArgs {
   int splits;
 };
 constexpr int LOGPROB_TOP_MAX = KVA_LOGPROBS_MAX_TOP;
-size_t logprob_workspace_bytes(int B, int H, int V, int top_k);
+size_t logprob_workspace_bytes(int B, int H, int V, int top_k);   // what one call takes
+size_t logprob_workspace_bound(int B, int H, int V, int top_k);   // and no call of fewer rows or alternatives more than this
 cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, cudaStream_t s, unsigned* n_launches);
 
 // Launch `kern` with programmatic stream serialization: its set-up overlaps the tail of the

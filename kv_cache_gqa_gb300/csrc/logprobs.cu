@@ -834,11 +834,23 @@ cudaError_t launch_k(const LogprobArgs& a, kva_dtype w_dtype, const TcPlan* p, c
 }  // namespace
 
 // Workspace: [normalised rows, float32][bf16 halves][partial statistics][partial lists]
-size_t logprob_workspace_bytes(int B, int H, int V, int top_k) {
-  int splits = stream_splits(B, V, list_len(top_k));
+static size_t parts_bytes(int B, int H, int V, int tk) {
+  int splits = stream_splits(B, V, tk);
   if (tc_supports(H)) splits = std::max(splits, 2 * tc_plan(B, V, 2).splits);
   const size_t parts = (size_t)B * splits;
-  return 2 * up256(sizeof(float) * (size_t)B * H) + up256(parts * 16) + up256(parts * 8 * list_len(top_k));
+  return up256(parts * 16) + up256(parts * 8 * tk);
+}
+size_t logprob_workspace_bytes(int B, int H, int V, int top_k) {
+  return 2 * up256(sizeof(float) * (size_t)B * H) + parts_bytes(B, H, V, list_len(top_k));
+}
+// Enough for this call and for those of fewer rows or alternatives, which may split the vocabulary more: between
+// multiples of 8 rows the blocks of either form, and with them the splits, stay the same.
+size_t logprob_workspace_bound(int B, int H, int V, int top_k) {
+  size_t most = 0;
+  for (int tk : {8, 12, 16, 24, 32})
+    if (tk <= list_len(top_k))
+      for (int b = B; b > 0; b = b <= 8 ? b - 1 : (b - 1) / 8 * 8) most = std::max(most, parts_bytes(b, H, V, tk));
+  return 2 * up256(sizeof(float) * (size_t)B * H) + most;
 }
 
 cudaError_t launch_logprobs(LogprobArgs a, kva_dtype w_dtype, void* workspace, cudaStream_t s, unsigned* n_launches) {

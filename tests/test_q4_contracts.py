@@ -86,3 +86,19 @@ def test_capacities_at_the_end_of_32_bits_are_refused(K):
     assert L.kv_attn_decode_q4(at, 1, cache, at, lengths.ctypes.data, 1, 1, 1, 0.0, at, at, 1 << 30, None) == K.KVA_EUNSUPPORTED
     lengths[0] = cache.capacity
     assert L.kv_attn_decode_q4(at, 1, cache, at, lengths.ctypes.data, 1, 1, 1, 0.0, at, at, 1 << 30, None) == K.KVA_EUNSUPPORTED
+
+
+def test_a_logprobs_workspace_serves_fewer_rows_and_alternatives(K):
+    """A server sizes it for its largest batch and list; a smaller call splits the vocabulary more."""
+    L = K.lib()
+    size = L.kva_lmhead_logprobs_workspace_size
+    for H, V in ((64, 333), (128, 9729), (72, 20000), (1024, 151936)):
+        for k in (0, 5, 12, 20, 24):
+            last = 0
+            for B in list(range(1, 300)) + [1000, 1024, 1025, 1151, 1152, 1153, 4096]:
+                now = size(B, H, V, k)
+                assert now >= last, (B, H, V, k)
+                last = now
+        for B in (1, 4, 5, 128, 129, 2000):
+            sizes = [size(B, H, V, k) for k in range(25)]
+            assert sizes == sorted(sizes), (B, H, V)
