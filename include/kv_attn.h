@@ -41,6 +41,11 @@
  *    Then q, k and q_out rows are Dk wide, v rows and attention outputs Dv wide.
  *  - GQA: query head h reads KV head h / (Hq / Hkv) (repeat-interleave grouping:
  *    Penguin-VL ncnn port, section 3 item 2).
+ *  - Workspaces: the bytes that kv_attn_decode, kv_attn_decode_step, kv_attn_verify, lmhead_argmax and
+ *    lmhead_topk want zero are more for more instances, heads or block rows, and partial results
+ *    follow them: a workspace that goes on to a wider call than before is zeroed again first (or
+ *    each shape has its own).  kv_attn_decode_q4 wants the same bytes for every shape and
+ *    lmhead_logprobs none.
  *  - Alignment: every device pointer must be 16-byte aligned, and D must be a
  *    multiple of 8 (vectorised 16-byte accesses); violations return KVA_EALIGN.
  */
@@ -367,7 +372,10 @@ size_t kva_lmhead_workspace_zero_bytes(int32_t B);
  *   tokens (B = sequences x block), and the scoring of a prompt (B = its tokens).  The logits
  *   stay on the chip: a pass over the table keeps, per row, the running maximum, the sums and a
  *   few more candidates than top_k; the target and the candidates are then scored again in
- *   twice float32 precision, which fixes their order.
+ *   twice float32 precision, which fixes their order.  Over a bf16 table with H % 64 == 0 the other
+ *   tokens' logits, which enter lse and entropy only, come from tensor-core products of two bf16
+ *   halves of a float32 or normalised row: 16 to 17 significant bits of each element, and sums
+ *   that come out up to about 6e-6 of a logit small at H = 4096.
  *  h            [B,H] of h_dtype (device);  norm_w [H] float32 or NULL;  W [V_rows,H] of w_dtype
  *  targets      [B] int32 (device) or NULL: the given tokens.  A negative target means no token
  *               (a padded row): its logprob is 0.  A target >= V has logprob NaN.

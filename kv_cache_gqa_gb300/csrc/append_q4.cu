@@ -12,10 +12,12 @@
 // dims stay in registers.  A lane's 8 values rotate as one piece where the rotated range and its
 // halves are multiples of 8 dims.
 //
-// A code is decided by a rounding, so a value that is off by an ulp of float32 becomes another code
-// once in about 10^6.  The float32 steps before it are therefore kept at one rounding each: squares
-// summed in 32 strided sums and then pairwise, products and sums of the rotation rounded apart, cosines
-// and sines within 3.5e-8 (rotation() below), quotients correctly rounded.
+// A code is decided by a rounding: a value that is off by an ulp of float32 becomes the neighbouring code
+// once in about 10^6, which is as near to it (scale / 2 either way).  The quotients are correctly rounded,
+// because bf16 values often lie on a tie exactly.  The steps before them are float32 with their usual errors: squares in 32
+// strided sums and then pairwise, a row's factor from rsqrtf (2 ulp; for rows of 192 the inverse of D is rounded too),
+// products and sums of the rotation rounded apart, cosines and sines as rotation() below says.  The order of
+// the sums is this kernel's choice; the definition fixes none.
 //
 // Bound: issue slots.  512 tokens in 28 caches (16 + 8 + 8 heads of 128, bf16): 160 MB in 93 us, 63% of the
 // slots used with three CTAs an SM (two: 131 us with the read-back instead of 113; four, at 64 registers: 113, and
@@ -68,7 +70,8 @@ __device__ __forceinline__ float sum_squares(const float* row, int D, int sl) {
 // 3.0e-8; 1 in 400 is not the correctly rounded value).  For |p| < 2^20 the angle is a pair of floats, brought
 // to r = rh + rl about within pi/4 by subtracting k pi/2 in three parts (Cody and Waite); the series of
 // cos and sin carry their first terms as pairs (Dekker's sums and products), the rest, below 0.016, in
-// float32.  Larger positions take float64 up to the reduced angle.
+// float32.  Larger positions take float64 up to the reduced angle, whose product p * inv is rounded first:
+// up to 1.2e-7 more near 2^31.
 __device__ __forceinline__ void rotation(int32_t p, float ih, float il, double inv, float* c, float* s) {
   float rh, rl;
   int k;

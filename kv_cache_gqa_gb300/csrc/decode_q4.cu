@@ -38,10 +38,10 @@
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
 // a lane's codes of K, and of V, are adjacent bytes.
 //
-// Bound: the instruction mix.  HBM would allow a 16-key tile (2304 bytes at D = 128) per SM every 52 ns;
-// its about 360 warp instructions, half of them on the logic pipe at half rate, and its 16 products of
-// mma.sync (a measured 1.05 ns each per SM) take 79 ns in all: 64 sequences of 1k to 32k tokens run at
-// 4.3 TB/s.  More warps per SM or more tiles in flight per warp do not change that.
+// Bound: no single unit.  64 sequences of 1k to 32k tokens run at 4.3 TB/s (284 us; HBM would take 180): 66% of
+// the issue slots are used, the logic pipe 57% of the time, the tensor pipe 22%, DRAM 54%.  Of a 16-key tile's about 367 warp
+// instructions a warp waits, each time, for a fixed latency (0.9 of an issue), for the pipe it needs (0.9) or for
+// its turn (1.2); for memory 0.2.  More warps per SM or more tiles in flight per warp did not change the time.
 //
 // Method: attention over the valid prefix of the cache (Youtu-VL-4B ncnn port, step 8), GQA grouping
 // (Penguin-VL ncnn port, section 3), softmax as max/subtract/exp/sum/divide (Youtu-VL-4B ncnn port,
@@ -807,6 +807,8 @@ int decode_q4_row_tile(int rows) { return rows <= 4 ? 4 : (rows <= 8 ? 8 : 16); 
 // join (61 sequences x 16 units of about 62 stages: 139 us against 146 in equal runs).  Else equal runs: as many as
 // the GPU holds at once, each with a stage per warp, and not so many that joining a unit's parts
 // (about 40 ns each, one CTA) costs more than its stages take (about 150 ns each, spread over the parts).
+// The stage per warp is counted over all units: short contexts give a CTA several units, one after another (64
+// sequences of 1 to 64 keys x 8 heads 18 us, a block of 16 tokens of one sequence of 30 keys 39 us; one of 768 keys 9).
 int decode_q4_ctas(int Dk, int rows, int64_t stages, int64_t units, int64_t longest, int64_t all_units, int* whole) {
   const int per_sm = rows <= 4 && Dk <= 128 ? 4 : (rows <= 8 || Dk <= 128 ? 3 : 2);
   const int64_t slots = DECODE_Q4_SMS * per_sm;

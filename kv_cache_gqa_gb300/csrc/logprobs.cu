@@ -1,9 +1,9 @@
 // Log probabilities over the vocabulary (lmhead_logprobs): a tcgen05 form for bf16 tables, a
 // streaming form for the others, and the merge that ends both.
 //
-// Bound: HBM for up to 128 rows or so (151936 x 1024, one row: 52 us, 88% of the copy rate, 59 us with the
-// kernels around it; 64 rows 71 us, where the two halves keep the tensor pipe 62% busy), then the L2 feed of
-// the products (1999 bf16 rows: 390 us, tensor pipe 74%).
+// Bound: HBM for up to 128 rows or so (151936 x 1024, one row: 52 us, 88% of the copy rate, 61.5 us with the
+// kernels around it; 64 rows 72 us, where the two halves keep the tensor pipe 61% busy), then the L2 feed of
+// the products (1999 bf16 rows: 390 us of 480, tensor pipe 74%).
 //
 // tcgen05 form (H a multiple of 64): D[128 batch rows x N vocabulary rows] = h W^T with the batch on the
 // TMEM lanes, so that an epilogue thread owns a batch row and every sum over the vocabulary is a sum
@@ -28,7 +28,9 @@
 // scores the given token and the TK candidates again: the lists hold TK > top_k candidates by
 // float32 (or two-bf16-halves) logits, whose rounding may exchange neighbours, while the second
 // scoring carries each product and sum with its rounding error (compensated dot product: Ogita,
-// Rump and Oishi, "Accurate sum and dot product"), about twice float32 precision, and orders them.
+// Rump and Oishi, "Accurate sum and dot product"), about twice float32 precision, and orders them.  The
+// other logits of the tcgen05 form enter the sums with 16 to 17 bits of a float32 or normalised row: a third bf16
+// part, which float32 would need, is half as many products again.
 // entropy = log s - u / s and lse = m + log s need no cancellation against m.  The candidates' terms
 // of s and u are exchanged for those of the second scoring: the tensor core drops a little of every
 // sum that it adds to (6e-6 of a logit at H = 4096), and the largest logits lose and weigh most.

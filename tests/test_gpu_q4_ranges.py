@@ -354,7 +354,7 @@ def test_long_appends(K, N, T, Hkv, G, Dk, Dv, in_dt, q_dt, rope, axes, norm, af
                                           (dict(kind="2d", base=1e4), 2, 64)])
 def test_far_and_negative_positions(K, rope, axes, Dk):
     """Positions on both sides of +-2^20, where the angle passes from pairs of floats to float64, up to the ends of
-    32 bits.  There float64 rounds an angle of 2^31 by 2^-22, as the definition does: 2.4e-7 each."""
+    32 bits.  There float64 rounds an angle near 2^31 by up to 1.2e-7, in the definition as in the kernel."""
     rng = seeded("far positions", rope["kind"])
     at = np.array([0, -1, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, -(1 << 20) + 1, -(1 << 20), -(1 << 20) - 1, 12345678, -98765432,
                    (1 << 31) - 1, -(1 << 31), 999999999], np.int64)
