@@ -400,7 +400,7 @@ size_t kva_lmhead_logprobs_workspace_size(int32_t B, int32_t H, int32_t V, int32
  * A cache held in 4 bits
  *   A row (one slot of one KV head) of D values is cut into G = D/64 groups of 64.  A group holds
  *   a scale and a midpoint, both bf16, and 64 codes u in 0..15, and stands for the values
- *     scale * (u - 8) + mid.
+ *     scale * (u - 8) + mid   (any finite scale and mid, negative scales among them).
  *   The append chooses scale = (max - min) / 15 rounded up to bf16, mid = min + 8 scale rounded to
  *   bf16 and u = 8 + (x - mid) / scale rounded (half to even) into -8..7, so that a value is off
  *   by at most scale / 2 plus half a bf16 step of mid.  A group of equal values has scale 0 and

@@ -457,7 +457,7 @@ decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
 #pragma unroll
           for (int gv = 0; gv < GV; ++gv) {
             if (TAIL && k0 + kr + 8 * hh >= k1) vp[q][hh][gv] = 0u;   // slots past the run may hold anything
-            top[gv] = fmaxf(top[gv], scale_of(vp[q][hh][gv]));
+            top[gv] = fmaxf(top[gv], fabsf(scale_of(vp[q][hh][gv])));
           }
       }
       // ---- online softmax: move the references when a score outgrows them (rare) ----

@@ -237,6 +237,25 @@ def test_decode_tiles_of_huge_values_that_no_token_attends(K, G, T, q_dt):
     assert_groups_close(host(out[0]), host(ref))
 
 
+@pytest.mark.parametrize("G,T,q_dt", ROWS)
+def test_decode_negative_scales(K, G, T, q_dt):
+    """A cache that another program wrote: a value is scale * (u - 8) + mid whatever the scale's sign."""
+    torch = _torch()
+    rng = seeded("negative", G, T)
+    L, W, D = 203, 204, 128
+    pk, pv = (Q.q4_quantise(rng.standard_normal((1, 1, W, D))) for _ in range(2))
+    q = dev(rng.standard_normal((1, T, G, D)).astype(np.float32), dt(q_dt))
+    lengths = np.array([L], np.int32)
+    ws = torch.zeros(K.decode_q4_workspace_bytes(1, 1, G, T, L, D), dtype=torch.uint8, device="cuda")
+    for sign in (-np.ones((1, 1, W, 2)), np.where(rng.random((1, 1, W, 2)) < 0.5, -1.0, 1.0)):
+        k, v = (pk[0], sign * pk[1], pk[2]), (pv[0], sign * pv[1], pv[2])
+        out = torch.full((1, T, G, D), float("nan"), device="cuda")
+        K.kv_attn_decode_q4(q, filled(K, *k, *v), dev(lengths), lengths, out, ws)
+        torch.cuda.synchronize()
+        ref = attend(q[0].double(), dev(Q.q4_values(*k)[0]), dev(Q.q4_values(*v)[0]), L)
+        assert_groups_close(host(out[0]), host(ref))
+
+
 # ---------------------------------------------------------------------------------------------
 # long blocks and contexts
 # ---------------------------------------------------------------------------------------------
