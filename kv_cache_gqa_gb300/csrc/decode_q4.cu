@@ -38,7 +38,7 @@
 // contraction runs over code positions, so the order of a row's words (kv_attn.h) only decides that
 // a lane's codes of K, and of V, are adjacent bytes.
 //
-// Bound: no single unit.  64 sequences of 1k to 32k tokens run at 4.3 TB/s (284 us; HBM would take 180): 66% of
+// Bound: no single unit.  64 sequences of 1k to 32k tokens run at 4.3 TB/s (282 us; HBM would take 180): 66% of
 // the issue slots are used, the logic pipe 57% of the time, the tensor pipe 22%, DRAM 54%.  Of a 16-key tile's about 367 warp
 // instructions a warp waits, each time, for a fixed latency (0.9 of an issue), for the pipe it needs (0.9) or for
 // its turn (1.2); for memory 0.2.  More warps per SM or more tiles in flight per warp did not change the time.

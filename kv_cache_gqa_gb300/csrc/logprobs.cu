@@ -1,7 +1,7 @@
 // Log probabilities over the vocabulary (lmhead_logprobs): a tcgen05 form for bf16 tables, a
 // streaming form for the others, and the merge that ends both.
 //
-// Bound: HBM for up to 128 rows or so (151936 x 1024, one row: 52 us, 88% of the copy rate, 61.5 us with the
+// Bound: HBM for up to 128 rows or so (151936 x 1024, one row: 52 us, 88% of the copy rate, 61 us with the
 // kernels around it; 64 rows 72 us, where the two halves keep the tensor pipe 61% busy), then the L2 feed of
 // the products (1999 bf16 rows: 390 us of 480, tensor pipe 74%).
 //
