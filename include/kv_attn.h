@@ -15,6 +15,12 @@
  *   kv_cache_append_q4, kv_cache_expand_q4, kv_attn_decode_q4
  *                                a cache held in 4 bits: its append, its read-back into a kva_cache
  *                                and the attention of new tokens over it
+ *   kv_cache_append_paged, kv_attn_paged
+ *                                a cache in pages: the append of a ragged batch of new tokens (one or
+ *                                many a sequence) and their attention
+ *   beam_select, kv_cache_reorder_paged
+ *                                beam search: the selection over beams and vocabulary, and the page
+ *                                tables and partly filled pages that follow it
  * plus workspace sizers (kva_workspace_size and the per-call ones), error strings, the
  * version, and the counter of in-kernel waits that gave up (kva_wait_timeouts).
  *
@@ -44,8 +50,8 @@
  *  - Workspaces: the bytes that kv_attn_decode, kv_attn_decode_step, kv_attn_verify, lmhead_argmax and
  *    lmhead_topk want zero are more for more instances, heads or block rows, and partial results
  *    follow them: a workspace that goes on to a wider call than before is zeroed again first (or
- *    each shape has its own).  kv_attn_decode_q4 wants the same bytes for every shape and
- *    lmhead_logprobs none.
+ *    each shape has its own).  kv_attn_decode_q4, kv_attn_paged and beam_select want the same bytes for
+ *    every shape and lmhead_logprobs none.
  *  - Alignment: every device pointer must be 16-byte aligned, and D must be a
  *    multiple of 8 (vectorised 16-byte accesses); violations return KVA_EALIGN.
  */
@@ -480,6 +486,145 @@ size_t kva_decode_q4_workspace_size(int32_t B, int32_t n_kv_heads, int32_t n_q_h
 size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t n_q_heads, int32_t T);
 
 /* ---------------------------------------------------------------------------------
+ * A cache in pages
+ *   A pool holds n_pages pages of page_size slots; sequences own pages by their page tables, so their
+ *   contexts grow without a fixed window and share what they have in common.  Slot s of sequence b is row
+ *   s % page_size of page table[b, s / page_size].
+ *  kva_paged_cache: one layer's pool.  Page p of K is [n_kv_heads, page_size, head_dim] of `dtype` at
+ *   k + p * page_stride elements, page p of V [n_kv_heads, page_size, head_dim_v] at v + p * page_stride_v
+ *   (0: packed pages; larger: a pool whose layers alternate).  head_dim_v = 0 means head_dim.
+ *   page_size is 16, 32, 64, 128 or 256; head dims are multiples of 64 up to 256; k, v and the strides' bytes are
+ *   16-byte aligned.
+ *  kva_paged_batch: B sequences with the new tokens of a step, listed one sequence after another.
+ *   table        [B, table_stride] int32 page ids (device).  Entries at or beyond ceil(L / page_size) are not read.
+ *   lengths      [B] int32 slots of a sequence, its new tokens included (device): new token i of T sits in slot L - T + i
+ *   token_start  [B + 1] int32 (device): sequence b's new tokens are token_start[b] .. token_start[b+1] - 1 of
+ *                the call's token rows; a sequence may have none.  Rows at or beyond token_start[B] are left as they were.
+ *   lengths_host, token_start_host  host mirrors: lengths_host may hold upper bounds (a captured step whose device
+ *                lengths grow); token_start_host holds the values (which sequences are short and which long is planned from it).
+ *   table_host   host mirror of the table or NULL; given, pages that lengths_host needs are checked
+ *                against the pool.  Without it a page id outside the pool costs its sequence: the append
+ *                drops its rows, the attention gives NaN for the tokens that see them. */
+#define KVA_PAGE_MIN 16
+#define KVA_PAGE_MAX 256
+typedef struct {
+  void* k;
+  void* v;
+  kva_dtype dtype;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t head_dim_v;
+  int32_t page_size;
+  int32_t n_pages;
+  int64_t page_stride;
+  int64_t page_stride_v;
+} kva_paged_cache;
+
+typedef struct {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lengths;
+  const int32_t* token_start;
+  const int32_t* table_host;
+  const int32_t* lengths_host;
+  const int32_t* token_start_host;
+  int32_t B;
+} kva_paged_batch;
+
+/* Rotary frequencies for contexts beyond the trained one.  Frequency w_j of kva_rope becomes
+ *     w_j * (c_j + (1 - c_j) / factor),  c_j = clamp((orig_len * w_j / 2 pi - low) / (high - low), 0, 1):
+ *   what turns less than `low` times within orig_len positions is slowed down by `factor`, what turns more than
+ *   `high` times stays.  orig_len = 0: every frequency is divided by factor (c_j = 0; low and high are not
+ *   read).  Cosines and sines are multiplied by `magnitude`.  factor = 0: nothing is scaled (magnitude is not read). */
+typedef struct {
+  double factor;
+  double orig_len;
+  double low;
+  double high;
+  float magnitude;
+} kva_rope_scale;
+
+/* kv_cache_append_paged: QK-Norm and RoPE of the batch's new tokens, written into their pages (the step of
+ *   kv_cache_append_rope_qknorm, one layer, T = token_start_host[B] tokens):
+ *     q_out[t,h,:] = f_q(q[t,h,:]);  K row of the token's slot, head g = store(f_k(k[t,g,:]));  V = store(v[t,g,:]).
+ *  q, k, v  [T,Hq,Dk], [T,Hkv,Dk], [T,Hkv,Dv] of in_dtype (device); q_stride, k_stride, v_stride: elements between tokens
+ *           (0: packed; larger: rows of a fused projection), multiples of 16 bytes.  q and q_out may both be NULL.
+ *  pos      [T, rope.n_axes] int32 (device);  q_out [T,Hq,Dk] of the cache's dtype, packed
+ *  norm     as for kv_cache_append_rope_qknorm (inst_stride is not read);  scale: see kva_rope_scale
+ *  Two tokens of a call must not have the same slot of the same page.
+ *  Errors: KVA_EINVAL, KVA_ECAPACITY (a length beyond the table's slots or below the sequence's new tokens, a page outside
+ *          the pool), KVA_EALIGN, KVA_EUNSUPPORTED (page sizes and head dims other than above), KVA_ECUDA.
+ *  B == 0 or T == 0 is a no-op. */
+kva_status kv_cache_append_paged(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride, kva_dtype in_dtype,
+    int32_t n_q_heads, const int32_t* pos, kva_qknorm norm, kva_rope rope, kva_rope_scale scale,
+    void* q_out, kva_paged_cache cache, kva_paged_batch batch, kva_stream stream);
+
+/* kv_attn_paged: attention of the batch's new tokens over their sequences' pages, which already hold them:
+ *     o_i = softmax_j(q_i . K[g, j] * scale, j <= L - T + i) V[g, j]      (new token i of a sequence of T)
+ *   One call takes any mix of single tokens, draft blocks and prompt chunks behind a cached prefix.
+ *  q    [T,Hq,Dk] of the cache's dtype, packed (device);  out [T,Hq,Dv] of out_dtype (device)
+ *  A token that sees no slot (a sequence shorter than its new tokens) gives a row of zeros.  Slots at or beyond L are
+ *  never used, whatever they hold.  A NaN or infinity in V of a slot that only later tokens of a sequence see may reach the earlier
+ *  tokens of the same call.  bf16 caches: softmax weights meet V as bf16 for a bf16 out and as two bf16 parts (16 bits) for a
+ *  float32 one; sums are float32.
+ *  scale      <= 0 selects 1/sqrt(Dk)
+ *  workspace  kva_paged_workspace_size(Hkv, Hq, Dv) bytes for calls of any batch; its first
+ *             kva_paged_workspace_zero_bytes() bytes are zero before the first call and left so by every call.  Calls
+ *             sharing one workspace must not overlap on the GPU.
+ *  Built for (Dk, Dv) = (64, 64), (128, 128) and (192, 128) and at most 64 query heads a KV head.
+ *  Errors as kv_cache_append_paged (a length may be below the sequence's new tokens), and KVA_EWORKSPACE. */
+kva_status kv_attn_paged(
+    const void* q, kva_dtype q_dtype, kva_paged_cache cache, kva_paged_batch batch, int32_t n_q_heads, float scale,
+    void* out, kva_dtype out_dtype, void* workspace, size_t workspace_bytes, kva_stream stream);
+size_t kva_paged_workspace_size(int32_t n_kv_heads, int32_t n_q_heads, int32_t head_dim_v);
+size_t kva_paged_workspace_zero_bytes(void);
+
+/* ---------------------------------------------------------------------------------
+ * beam_select  (one step of beam search: the best continuations over beams and vocabulary)
+ *   Beam k of group b offers token v with the total scores[b,k] + z[b,k,v] - log sum_u exp(z[b,k,u]).  The n_out largest totals of a
+ *   group, descending, equal ones toward the lower beam, then the lower token:
+ *     out_beam, out_token [B,n_out] int32, out_score [B,n_out] float32.
+ *   A finished beam offers one continuation, (end_id, its score unchanged).  A beam with score -infinity or NaN offers
+ *   none, nor does one with a logit of NaN or +infinity; a token with logit -infinity is never offered.
+ *   Places that no offer fills hold beam -1, token -1 and score -infinity.
+ *  logits     [B,K,V] of dtype (device), rows row_stride elements apart (0: V; more: a padded table; any alignment of dtype)
+ *  scores     [B,K] float32 (device);  finished [B,K] int32 (device; nonzero: finished) or NULL
+ *  end_id     0 <= end_id < V with `finished`, else not read
+ *  workspace  kva_beam_workspace_size(B, K, V) bytes, which also serve smaller calls over the same V; its first
+ *             kva_beam_workspace_zero_bytes() bytes are zero before the first call and left so by every call.
+ *  1 <= K, n_out <= KVA_BEAM_MAX, n_out <= K * V, B <= 4096.  B == 0 is a no-op. */
+#define KVA_BEAM_MAX 32
+kva_status beam_select(
+    const void* logits, kva_dtype dtype, int64_t row_stride, int32_t B, int32_t K, int32_t V,
+    const float* scores, const int32_t* finished, int32_t end_id, int32_t n_out,
+    int32_t* out_beam, int32_t* out_token, float* out_score,
+    void* workspace, size_t workspace_bytes, kva_stream stream);
+size_t kva_beam_workspace_size(int32_t B, int32_t K, int32_t V);
+size_t kva_beam_workspace_zero_bytes(void);
+
+/* kv_cache_reorder_paged: beams over a paged cache go on from the beams that beam_select chose.  Rows are B groups of K
+ *   beams.  With p = parent[b,k] and L = lengths[b,p]:
+ *     lengths_out[b,k] = L;  table_out[b,k,j] = table[b,p,j] for j < ceil(L / page_size) (other entries are left as they were).
+ *   Full pages are shared.  A partly filled last page stays with the first beam of the group that carries it on; each
+ *   later beam gets its spare page instead, into which the L % page_size filled rows of every layer are copied.
+ *   spare_out[b,k] is spare[b,k], or, where that was used, a partly filled last page that no beam of the group carries on
+ *   (the n-th such page, by beam, for the n-th beam that needed a copy), or -1 when there are no more of them.  Equally
+ *   long beams free as many pages as they use, unless some of them shared one before (the first step after a prompt).
+ *   A parent outside 0..K-1 gives a beam of length 0.  A beam whose copy has no page of the pool to go to, or
+ *   to come from, gets length -1 (which the other calls take for 0) and keeps its spare.
+ *   A partly filled page must not belong to two groups, and a spare page to no other beam.
+ *  cache      the first layer's pool; layer l is at k + l * layer_stride and v + l * layer_stride_v elements (not read for
+ *             n_layers = 1); dtype, head dims and page size are any that a kva_paged_cache takes
+ *  parent, lengths, spare [B,K] and table [B,K,table_stride] int32 (device); lengths_host: mirror or upper bounds
+ *  table_out, lengths_out, spare_out: like table, lengths, spare, and other buffers than these.
+ *  1 <= K <= KVA_BEAM_MAX.  B == 0 is a no-op. */
+kva_status kv_cache_reorder_paged(
+    kva_paged_cache cache, int32_t n_layers, int64_t layer_stride, int64_t layer_stride_v, int32_t B, int32_t K,
+    const int32_t* parent, const int32_t* table, int64_t table_stride, const int32_t* lengths, const int32_t* lengths_host,
+    const int32_t* spare, int32_t* table_out, int32_t* lengths_out, int32_t* spare_out, kva_stream stream);
+
+/* ---------------------------------------------------------------------------------
  * kva_workspace_size
  *   One sizer for every call that takes a workspace (the boundary lists a single
  *   kva_workspace_size(which, ...)); it returns what the per-call sizer above returns for
@@ -492,6 +637,8 @@ size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t
  *     KVA_WS_DECODE_Q4     kv_attn_decode_q4: B, n_kv_heads, n_q_heads, max_len, head_dim (Dv),
  *                          block (T)
  *     KVA_WS_LMHEAD_LOGPROBS  lmhead_logprobs: B, hidden, vocab, block (top_k, 0 allowed)
+ *     KVA_WS_ATTN_PAGED    kv_attn_paged: n_kv_heads, n_q_heads, head_dim (Dv)
+ *     KVA_WS_BEAM_SELECT   beam_select: B, vocab, block (K)
  *   Fields a kind does not read are ignored.  Returns 0 for an unknown kind, a NULL `dims` or
  *   a dimension that is not positive. */
 typedef enum {
@@ -500,7 +647,9 @@ typedef enum {
   KVA_WS_LMHEAD = 2,
   KVA_WS_LMHEAD_TOPK = 3,
   KVA_WS_DECODE_Q4 = 4,
-  KVA_WS_LMHEAD_LOGPROBS = 5
+  KVA_WS_LMHEAD_LOGPROBS = 5,
+  KVA_WS_ATTN_PAGED = 6,
+  KVA_WS_BEAM_SELECT = 8
 } kva_workspace_kind;
 
 typedef struct {
@@ -511,7 +660,7 @@ typedef struct {
   int32_t head_dim;  /* value head width Dv of the attention output */
   int32_t hidden;    /* lm_head hidden size H */
   int32_t vocab;     /* lm_head candidate rows V */
-  int32_t block;     /* verify block length k, decode_q4 block T, or top_k */
+  int32_t block;     /* verify block length k, decode_q4 block T, top_k, or beams K */
 } kva_workspace_dims;
 
 size_t kva_workspace_size(int32_t which, const kva_workspace_dims* dims);

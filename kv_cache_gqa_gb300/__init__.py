@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
   kv_cache_append_q4           the append into a cache held in 4 bits (KVCacheQ4)
   kv_cache_expand_q4           slots of a 4-bit cache read back into a bf16 or f32 cache
   kv_attn_decode_q4            attention of one token, or a block of tokens, over a 4-bit cache
+  kv_cache_append_paged        the append of a ragged batch of new tokens into a cache in pages (PagedKVCache, PagedBatch)
+  kv_attn_paged                attention of those tokens, one or many a sequence, over the pages
+  beam_select                  beam search: the best continuations over beams and vocabulary
+  kv_cache_reorder_paged       page tables and partly filled pages follow the selected beams
 """
 from .kv_attn import (KVCache, KVCacheQ4, KvaError, Rope, decode_workspace_bytes, kv_attn_decode,  # noqa: F401
                       kv_attn_decode_step, kv_attn_verify, kv_verify_commit, verify_workspace_bytes,
@@ -22,4 +26,7 @@ from .kv_attn import (KVCache, KVCacheQ4, KvaError, Rope, decode_workspace_bytes
                       version, wait_timeouts, workspace_bytes, PreparedCall, prepare_decode_step,
                       prepare_lmhead_argmax, decode_q4_workspace_bytes, kv_attn_decode_q4, kv_cache_append_q4,
                       kv_cache_expand_q4, lmhead_logprobs, lmhead_logprobs_workspace_bytes, prepare_append_q4,
-                      prepare_decode_q4, prepare_expand_q4, prepare_lmhead_logprobs)
+                      prepare_decode_q4, prepare_expand_q4, prepare_lmhead_logprobs, PagedBatch, PagedKVCache, RopeScale,
+                      beam_select, beam_workspace_bytes, kv_attn_paged, kv_cache_append_paged, kv_cache_reorder_paged,
+                      paged_workspace_bytes, paged_workspace_zero_bytes, beam_workspace_zero_bytes, prepare_append_paged, prepare_attn_paged, prepare_beam_select,
+                      prepare_reorder_paged)

@@ -221,6 +221,66 @@ Q4Cache q4_args(const kva_cache_q4& c) {
   return a;
 }
 
+// Checks a paged cache and resolves its defaults in place (head_dim_v, page strides).
+kva_status check_paged(kva_paged_cache& c) {
+  if (!valid_dtype(c.dtype)) return fail(KVA_EINVAL, "paged cache dtype %d unknown", (int)c.dtype);
+  if (!c.k || !c.v) return fail(KVA_EINVAL, "paged cache k/v pointer is NULL");
+  if (c.head_dim_v < 0 || c.page_stride < 0 || c.page_stride_v < 0)
+    return fail(KVA_EINVAL, "paged cache: negative head_dim_v or page stride");
+  if (c.n_kv_heads <= 0 || c.head_dim <= 0 || c.page_size <= 0 || c.n_pages <= 0)
+    return fail(KVA_EINVAL, "paged cache shape must be positive (Hkv=%d D=%d page=%d pages=%d)", c.n_kv_heads, c.head_dim,
+                c.page_size, c.n_pages);
+  if (c.head_dim_v == 0) c.head_dim_v = c.head_dim;
+  if (c.page_size < KVA_PAGE_MIN || c.page_size > KVA_PAGE_MAX || (c.page_size & (c.page_size - 1)) != 0)
+    return fail(KVA_EUNSUPPORTED, "page size %d (16, 32, 64, 128 or 256)", c.page_size);
+  if (c.head_dim % 64 != 0 || c.head_dim_v % 64 != 0 || c.head_dim > 256 || c.head_dim_v > 256)
+    return fail(KVA_EUNSUPPORTED, "paged cache head dims %d/%d are not multiples of 64 up to 256", c.head_dim, c.head_dim_v);
+  if (c.n_kv_heads > 65535) return fail(KVA_EUNSUPPORTED, "paged cache: more than 65535 KV heads");
+  const int64_t page = (int64_t)c.n_kv_heads * c.page_size * c.head_dim;
+  const int64_t page_v = (int64_t)c.n_kv_heads * c.page_size * c.head_dim_v;
+  if (c.page_stride == 0) c.page_stride = page;
+  if (c.page_stride_v == 0) c.page_stride_v = page_v;
+  if (c.page_stride < page || c.page_stride_v < page_v)
+    return fail(KVA_EINVAL, "paged cache page strides %lld/%lld < Hkv*page*D = %lld/%lld", (long long)c.page_stride,
+                (long long)c.page_stride_v, (long long)page, (long long)page_v);
+  if (!aligned16(c.k) || !aligned16(c.v)) return fail(KVA_EALIGN, "paged cache k/v not 16-byte aligned");
+  if ((c.page_stride * elem_size(c.dtype)) % 16 != 0 || (c.page_stride_v * elem_size(c.dtype)) % 16 != 0)
+    return fail(KVA_EALIGN, "paged cache page strides are not multiples of 16 bytes");
+  return KVA_OK;
+}
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+// Checks a batch of B >= 1 sequences against a checked cache; `whole`: a length covers its new tokens.
+kva_status check_batch(const kva_paged_cache& c, const kva_paged_batch& b, bool whole) {
+  if (!b.table || !b.lengths || !b.token_start || !b.lengths_host || !b.token_start_host)
+    return fail(KVA_EINVAL, "paged batch: NULL table/lengths/token_start");
+  if (b.table_stride <= 0) return fail(KVA_EINVAL, "paged batch: table_stride %lld", (long long)b.table_stride);
+  if (b.token_start_host[0] != 0) return fail(KVA_EINVAL, "token_start begins with %d", b.token_start_host[0]);
+  const int64_t slots = std::min<int64_t>(b.table_stride, INT32_MAX) * c.page_size;
+  for (int i = 0; i < b.B; ++i) {
+    const int64_t n = (int64_t)b.token_start_host[i + 1] - b.token_start_host[i];
+    const int64_t L = b.lengths_host[i];
+    if (n < 0) return fail(KVA_EINVAL, "token_start decreases at sequence %d", i);
+    if (L < 0 || L > slots || L > INT32_MAX - 512)
+      return fail(KVA_ECAPACITY, "length %lld of sequence %d outside its table's %lld slots", (long long)L, i, (long long)slots);
+    if (whole && L < n) return fail(KVA_ECAPACITY, "length %lld of sequence %d below its %lld new tokens", (long long)L, i, (long long)n);
+    if (b.table_host) {
+      const int64_t pages = (L + c.page_size - 1) / c.page_size;
+      for (int64_t j = 0; j < pages; ++j) {
+        const int32_t p = b.table_host[(int64_t)i * b.table_stride + j];
+        if (p < 0 || p >= c.n_pages)
+          return fail(KVA_ECAPACITY, "page %d of sequence %d is %d, outside the pool's %d", (int)j, i, p, c.n_pages);
+      }
+    }
+  }
+  return KVA_OK;
+}
+
 // Slots of one instance: inside the cache and, when `once`, none of them twice.
 kva_status check_slots(const int32_t* slots, int n, int T, int capacity, bool once) {
   bool ascending = true;
@@ -369,6 +429,8 @@ size_t kva_workspace_size(int32_t which, const kva_workspace_dims* d) {
     case KVA_WS_DECODE_Q4:
       return kva_decode_q4_workspace_size(d->B, d->n_kv_heads, d->n_q_heads, d->block, d->max_len, d->head_dim);
     case KVA_WS_LMHEAD_LOGPROBS: return kva_lmhead_logprobs_workspace_size(d->B, d->hidden, d->vocab, d->block);
+    case KVA_WS_ATTN_PAGED: return kva_paged_workspace_size(d->n_kv_heads, d->n_q_heads, d->head_dim);
+    case KVA_WS_BEAM_SELECT: return kva_beam_workspace_size(d->B, d->block, d->vocab);
   }
   return 0;
 }
@@ -1001,6 +1063,217 @@ kva_status kv_attn_decode_q4(
   const cudaError_t e = launch_decode_q4(a, q_dtype, (cudaStream_t)stream);
   if (e == cudaSuccess) count_launches(1);
   return cuda_status(e, "4-bit decode launch");
+}
+
+kva_status kv_cache_append_paged(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride, kva_dtype in_dtype,
+    int32_t n_q_heads, const int32_t* pos, kva_qknorm norm, kva_rope rope, kva_rope_scale scale,
+    void* q_out, kva_paged_cache cache, kva_paged_batch batch, kva_stream stream) {
+  if (batch.B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", batch.B);
+  if (batch.B == 0) return KVA_OK;
+  if (!valid_dtype(in_dtype)) return fail(KVA_EINVAL, "unknown dtype");
+  kva_status st = check_paged(cache);
+  if (st != KVA_OK || (st = check_batch(cache, batch, true)) != KVA_OK) return st;
+  const int Dk = cache.head_dim, Dv = cache.head_dim_v, Hkv = cache.n_kv_heads, T = batch.token_start_host[batch.B];
+  if (T == 0) return KVA_OK;
+  if ((q != nullptr) != (q_out != nullptr)) return fail(KVA_EINVAL, "q and q_out must both be given or both be NULL");
+  if (q && (n_q_heads <= 0 || n_q_heads % Hkv != 0))
+    return fail(KVA_EINVAL, "n_q_heads %d must be a positive multiple of n_kv_heads %d", n_q_heads, Hkv);
+  if (!k || !v) return fail(KVA_EINVAL, "NULL k/v");
+  if (rope.kind != KVA_ROPE_NONE && !pos) return fail(KVA_EINVAL, "RoPE needs positions");
+  if ((norm.q_w == nullptr) != (norm.k_w == nullptr))
+    return fail(KVA_EINVAL, "q and k norm weights must both be given or both be NULL");
+  if (norm.q_w && !(norm.eps >= 0.f)) return fail(KVA_EINVAL, "QK-Norm eps must be >= 0");
+  int rot_off = 0, rot_w = Dk;
+  if (rope.kind != KVA_ROPE_NONE && (st = rope_range(rope, Dk, &rot_off, &rot_w)) != KVA_OK) return st;
+  const int64_t wide[3] = {(int64_t)(q ? n_q_heads : 0) * Dk, (int64_t)Hkv * Dk, (int64_t)Hkv * Dv};
+  int64_t stride[3] = {q ? q_stride : 0, k_stride, v_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] == 0) stride[i] = wide[i];
+    if (stride[i] < wide[i])
+      return fail(KVA_EINVAL, "token stride %lld below a token's %lld elements", (long long)stride[i], (long long)wide[i]);
+    if ((stride[i] * elem_size(in_dtype)) % 16 != 0) return fail(KVA_EALIGN, "token strides are not multiples of 16 bytes");
+  }
+  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))))
+    return fail(KVA_EALIGN, "q/k/v/q_out must be 16-byte aligned");
+  if (norm.q_w && (!aligned16(norm.q_w) || !aligned16(norm.k_w))) return fail(KVA_EALIGN, "norm weights must be 16-byte aligned");
+  AppendPagedArgs a{};
+  if ((st = build_rope_table(rope, rot_w, &a.rope)) != KVA_OK) return st;
+  a.magnitude = 1.f;
+  if (scale.factor != 0.0) {
+    if (!(scale.factor >= 1.0) || !std::isfinite(scale.factor) || !(scale.orig_len >= 0.0) || !std::isfinite(scale.orig_len))
+      return fail(KVA_EINVAL, "rope scale: factor %g must be >= 1 (or 0: none), orig_len %g >= 0", scale.factor, scale.orig_len);
+    if (scale.orig_len > 0.0 && !(scale.high > scale.low && std::isfinite(scale.high - scale.low)))
+      return fail(KVA_EINVAL, "rope scale: high %g must be above low %g", scale.high, scale.low);
+    if (!std::isfinite(scale.magnitude)) return fail(KVA_EINVAL, "rope scale: magnitude is not finite");
+    a.magnitude = scale.magnitude;
+    for (int j = 0; j < rot_w / 2 && rope.kind != KVA_ROPE_NONE; ++j) {
+      const double w = a.rope.inv[j];
+      double c = 0.0;
+      if (scale.orig_len > 0.0)
+        c = std::min(1.0, std::max(0.0, (scale.orig_len * w / 6.283185307179586 - scale.low) / (scale.high - scale.low)));
+      a.rope.inv[j] = w * (c + (1.0 - c) / scale.factor);
+      a.rope.inv_hi[j] = (float)a.rope.inv[j];
+      a.rope.inv_lo[j] = (float)(a.rope.inv[j] - (double)a.rope.inv_hi[j]);
+    }
+  }
+  a.q = q; a.k = k; a.v = v; a.q_stride = stride[0]; a.k_stride = stride[1]; a.v_stride = stride[2];
+  a.q_out = q_out; a.kc = cache.k; a.vc = cache.v; a.pos = pos;
+  a.table = batch.table; a.lengths = batch.lengths; a.start = batch.token_start;
+  a.table_stride = batch.table_stride; a.page_shift = log2_of(cache.page_size);
+  a.slots = batch.table_stride << a.page_shift;
+  a.page_stride = cache.page_stride; a.page_stride_v = cache.page_stride_v; a.n_pages = cache.n_pages;
+  a.q_w = norm.q_w; a.k_w = norm.k_w; a.eps = norm.eps; a.after_rope = norm.after_rope ? 1 : 0;
+  a.B = batch.B; a.T = T; a.Hq = q ? n_q_heads : 0; a.Hkv = Hkv; a.Dk = Dk; a.Dv = Dv;
+  a.rot_offset = rot_off; a.rot_dim = rot_w;
+  const cudaError_t e = launch_append_paged(a, in_dtype, cache.dtype, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "paged append launch");
+}
+
+// A workspace begins with its counters, as many whatever the call's shape.
+size_t kva_paged_workspace_zero_bytes(void) { return round_up(sizeof(unsigned) * PAGED_MAX_RUNS, 256); }
+
+size_t kva_paged_workspace_size(int32_t n_kv_heads, int32_t n_q_heads, int32_t head_dim_v) {
+  if (n_kv_heads <= 0 || n_q_heads <= 0 || head_dim_v <= 0 || n_q_heads % n_kv_heads != 0) return 0;
+  return kva_paged_workspace_zero_bytes() + round_up(sizeof(float) * PAGED_PART_ROWS * 2, 256) +
+         sizeof(float) * PAGED_PART_ROWS * head_dim_v;
+}
+
+kva_status kv_attn_paged(
+    const void* q, kva_dtype q_dtype, kva_paged_cache cache, kva_paged_batch batch, int32_t n_q_heads, float scale,
+    void* out, kva_dtype out_dtype, void* workspace, size_t workspace_bytes, kva_stream stream) {
+  if (batch.B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", batch.B);
+  if (batch.B == 0) return KVA_OK;
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return fail(KVA_EINVAL, "unknown dtype");
+  kva_status st = check_paged(cache);
+  if (st != KVA_OK || (st = check_batch(cache, batch, false)) != KVA_OK) return st;
+  const int Dk = cache.head_dim, Dv = cache.head_dim_v, Hkv = cache.n_kv_heads, T = batch.token_start_host[batch.B];
+  if (T == 0) return KVA_OK;
+  if (n_q_heads <= 0 || n_q_heads % Hkv != 0)
+    return fail(KVA_EINVAL, "n_q_heads %d must be a positive multiple of n_kv_heads %d", n_q_heads, Hkv);
+  if (q_dtype != cache.dtype) return fail(KVA_EINVAL, "q dtype must equal the cache's");
+  if (!attn_paged_supports(Dk, Dv))
+    return fail(KVA_EUNSUPPORTED, "paged attention: head dims %d/%d (built: 64/64, 128/128, 192/128)", Dk, Dv);
+  const int G = n_q_heads / Hkv;
+  if (G > 64) return fail(KVA_EUNSUPPORTED, "paged attention: %d query heads a KV head (at most 64)", G);
+  if ((int64_t)T * G > INT32_MAX - 512) return fail(KVA_EUNSUPPORTED, "paged attention: too many query rows");
+  if (!q || !out) return fail(KVA_EINVAL, "NULL q/out");
+  if (!aligned16(q) || !aligned16(out)) return fail(KVA_EALIGN, "q/out must be 16-byte aligned");
+  if (!workspace) return fail(KVA_EWORKSPACE, "paged attention: workspace is NULL");
+  if (!aligned16(workspace)) return fail(KVA_EALIGN, "workspace must be 16-byte aligned");
+  const size_t need = kva_paged_workspace_size(Hkv, n_q_heads, Dv);
+  if (workspace_bytes < need) return fail(KVA_EWORKSPACE, "paged attention workspace %zu bytes < %zu needed", workspace_bytes, need);
+  PagedArgs a{};
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.counters = reinterpret_cast<unsigned*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + kva_paged_workspace_zero_bytes());
+  a.part_acc = a.part_ml + round_up(sizeof(float) * PAGED_PART_ROWS * 2, 256) / sizeof(float);
+  a.q = q; a.k = cache.k; a.v = cache.v; a.out = out; a.out_bf16 = out_dtype == KVA_BF16;
+  a.table = batch.table; a.lengths = batch.lengths; a.start = batch.token_start;
+  a.table_stride = batch.table_stride; a.page_shift = log2_of(cache.page_size);
+  a.slots = std::min<int64_t>(batch.table_stride << a.page_shift, INT32_MAX - 512);
+  a.page_stride = cache.page_stride; a.page_stride_v = cache.page_stride_v; a.n_pages = cache.n_pages;
+  a.B = batch.B; a.T = T; a.Hq = n_q_heads; a.Hkv = Hkv;
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)Dk);
+  a.scale_log2 = sc * 1.4426950408889634f;
+  unsigned n_launch = 0;
+  const cudaError_t e = launch_attn_paged(a, Dk, Dv, cache.dtype, batch.lengths_host, batch.token_start_host,
+                                          (cudaStream_t)stream, &n_launch);
+  count_launches(n_launch);
+  return cuda_status(e, "paged attention launch");
+}
+
+size_t kva_beam_workspace_zero_bytes(void) { return round_up(sizeof(unsigned) * BEAM_MAX_GROUPS, 256); }
+
+size_t kva_beam_workspace_size(int32_t B, int32_t K, int32_t V) {
+  if (B <= 0 || K <= 0 || V <= 0 || K > BEAM_MAX || B > BEAM_MAX_GROUPS) return 0;
+  const size_t parts = (size_t)beam_parts_bound(B * K);
+  return kva_beam_workspace_zero_bytes() + round_up(parts * 2 * sizeof(float), 256) + parts * BEAM_MAX * sizeof(unsigned long long);
+}
+
+kva_status beam_select(
+    const void* logits, kva_dtype dtype, int64_t row_stride, int32_t B, int32_t K, int32_t V,
+    const float* scores, const int32_t* finished, int32_t end_id, int32_t n_out,
+    int32_t* out_beam, int32_t* out_token, float* out_score,
+    void* workspace, size_t workspace_bytes, kva_stream stream) {
+  if (B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", B);
+  if (B == 0) return KVA_OK;
+  if (!valid_dtype(dtype)) return fail(KVA_EINVAL, "unknown dtype");
+  if (K < 1 || K > BEAM_MAX) return fail(KVA_EINVAL, "K=%d outside [1, %d]", K, BEAM_MAX);
+  if (n_out < 1 || n_out > BEAM_MAX) return fail(KVA_EINVAL, "n_out=%d outside [1, %d]", n_out, BEAM_MAX);
+  if (V <= 0) return fail(KVA_EINVAL, "V=%d must be positive", V);
+  if (n_out > (int64_t)K * V) return fail(KVA_EINVAL, "n_out=%d exceeds K * V = %lld", n_out, (long long)K * V);
+  if (row_stride == 0) row_stride = V;
+  if (row_stride < V) return fail(KVA_EINVAL, "row_stride %lld < V=%d", (long long)row_stride, V);
+  if (!logits || !scores || !out_beam || !out_token || !out_score) return fail(KVA_EINVAL, "NULL logits/scores/outputs");
+  if (finished && (end_id < 0 || end_id >= V)) return fail(KVA_EINVAL, "end_id %d outside [0, %d)", end_id, V);
+  if (B > BEAM_MAX_GROUPS || (int64_t)B * K > 65535)
+    return fail(KVA_EUNSUPPORTED, "beam_select: B=%d, K=%d (B <= %d, B * K <= 65535)", B, K, BEAM_MAX_GROUPS);
+  if (V > INT32_MAX - 65536) return fail(KVA_EUNSUPPORTED, "beam_select: V=%d", V);
+  if (reinterpret_cast<uintptr_t>(logits) % elem_size(dtype) != 0) return fail(KVA_EALIGN, "logits are not aligned to their type");
+  if (!workspace) return fail(KVA_EWORKSPACE, "beam_select: workspace is NULL");
+  if (!aligned16(workspace)) return fail(KVA_EALIGN, "workspace must be 16-byte aligned");
+  BeamArgs a{};
+  a.splits = beam_splits(B * K, V);
+  const size_t parts = (size_t)a.splits * B * K, zero = kva_beam_workspace_zero_bytes();
+  const size_t stat = round_up(parts * 2 * sizeof(float), 256), need = zero + stat + parts * n_out * sizeof(unsigned long long);
+  if (workspace_bytes < need) return fail(KVA_EWORKSPACE, "beam_select workspace %zu bytes < %zu needed", workspace_bytes, need);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.counters = reinterpret_cast<unsigned*>(ws);
+  a.part_stat = reinterpret_cast<float*>(ws + zero);
+  a.part_key = reinterpret_cast<unsigned long long*>(ws + zero + stat);
+  a.logits = logits; a.row_stride = row_stride; a.scores = scores; a.finished = finished;
+  a.out_beam = out_beam; a.out_token = out_token; a.out_score = out_score;
+  a.B = B; a.K = K; a.V = V; a.n = n_out; a.end_id = end_id;
+  const cudaError_t e = launch_beam_select(a, dtype, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "beam selection launch");
+}
+
+kva_status kv_cache_reorder_paged(
+    kva_paged_cache cache, int32_t n_layers, int64_t layer_stride, int64_t layer_stride_v, int32_t B, int32_t K,
+    const int32_t* parent, const int32_t* table, int64_t table_stride, const int32_t* lengths, const int32_t* lengths_host,
+    const int32_t* spare, int32_t* table_out, int32_t* lengths_out, int32_t* spare_out, kva_stream stream) {
+  if (B < 0) return fail(KVA_EINVAL, "B=%d must be >= 0", B);
+  if (B == 0) return KVA_OK;
+  kva_status st = check_paged(cache);
+  if (st != KVA_OK) return st;
+  if (K < 1 || K > BEAM_MAX) return fail(KVA_EINVAL, "K=%d outside [1, %d]", K, BEAM_MAX);
+  if (n_layers < 1) return fail(KVA_EINVAL, "n_layers=%d must be positive", n_layers);
+  if (layer_stride < 0 || layer_stride_v < 0) return fail(KVA_EINVAL, "negative layer stride");
+  if (!parent || !table || !lengths || !lengths_host || !spare || !table_out || !lengths_out || !spare_out)
+    return fail(KVA_EINVAL, "NULL parent/table/lengths/spare");
+  if (table == table_out || lengths == lengths_out || spare == spare_out)
+    return fail(KVA_EINVAL, "table, lengths and spare need outputs of their own");
+  if (table_stride <= 0) return fail(KVA_EINVAL, "table_stride %lld", (long long)table_stride);
+  const int es = elem_size(cache.dtype);
+  if (n_layers > 1) {
+    const int64_t page = (int64_t)cache.n_kv_heads * cache.page_size;
+    if (layer_stride < page * cache.head_dim || layer_stride_v < page * cache.head_dim_v)
+      return fail(KVA_EINVAL, "layer strides %lld/%lld below a page", (long long)layer_stride, (long long)layer_stride_v);
+    if ((layer_stride * es) % 16 != 0 || (layer_stride_v * es) % 16 != 0)
+      return fail(KVA_EALIGN, "layer strides are not multiples of 16 bytes");
+  }
+  if ((int64_t)B * K > INT32_MAX || (int64_t)n_layers * 2 * cache.n_kv_heads > INT32_MAX)
+    return fail(KVA_EUNSUPPORTED, "reorder: too many beams or layers");
+  const int64_t slots = std::min<int64_t>(table_stride, INT32_MAX) * cache.page_size;
+  for (int64_t i = 0; i < (int64_t)B * K; ++i)
+    if (lengths_host[i] > slots || lengths_host[i] > INT32_MAX - 512)
+      return fail(KVA_ECAPACITY, "length %d of beam %lld outside its table's %lld slots", lengths_host[i], (long long)i, (long long)slots);
+  ReorderPagedArgs a{};
+  a.k = cache.k; a.v = cache.v;
+  a.page_stride = cache.page_stride * es; a.page_stride_v = cache.page_stride_v * es;
+  a.layer_stride = layer_stride * es; a.layer_stride_v = layer_stride_v * es;
+  a.parent = parent; a.table = table; a.lengths = lengths; a.spare = spare;
+  a.table_out = table_out; a.lengths_out = lengths_out; a.spare_out = spare_out;
+  a.table_stride = table_stride;
+  a.B = B; a.K = K; a.layers = n_layers; a.Hkv = cache.n_kv_heads;
+  a.row_k = cache.head_dim * es; a.row_v = cache.head_dim_v * es;
+  a.page_shift = log2_of(cache.page_size); a.n_pages = cache.n_pages;
+  const cudaError_t e = launch_reorder_paged(a, (cudaStream_t)stream);
+  if (e == cudaSuccess) count_launches(1);
+  return cuda_status(e, "paged reorder launch");
 }
 
 }  // extern "C"

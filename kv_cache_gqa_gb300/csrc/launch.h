@@ -278,6 +278,95 @@ int decode_q4_ctas(int Dk, int rows, int64_t stages, int64_t units, int64_t long
 cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStream_t s);
 
 // ---------------------------------------------------------------------------------
+// The paged cache (layout: kva_paged_cache and kva_paged_batch in kv_attn.h).
+struct PagedArgs {
+  const void* q;                      // [T, Hq, Dk]
+  const void* k;                      // [n_pages, Hkv, page, Dk], pages page_stride elements apart
+  const void* v;
+  const int32_t* table;               // [B, table_stride]
+  const int32_t* lengths;             // [B]
+  const int32_t* start;               // [B + 1]
+  void* out;                          // [T, Hq, Dv]
+  unsigned int* counters;             // [PAGED_MAX_RUNS], by a shared unit's first run; zero on entry, zero on exit
+  float* part_acc;                    // [runs, 2, rows, Dv]
+  float* part_ml;                     // [runs, 2, rows, 2]
+  int64_t table_stride, slots;        // slots = table_stride * page
+  int64_t page_stride, page_stride_v;
+  int B, T, Hq, Hkv, page_shift, n_pages, out_bf16;
+  int rows_lo, rows_hi;               // this launch takes sequences of rows_lo < T * Hq / Hkv <= rows_hi query rows
+  float scale_log2;
+};
+constexpr int PAGED_SMS = 152;        // grids are sized for the whole GPU
+constexpr int PAGED_MAX_RUNS = PAGED_SMS * 4;
+constexpr int PAGED_ROWS = 16;        // query rows of a unit on the CUDA cores and in mma.sync tiles
+constexpr size_t PAGED_PART_ROWS = (size_t)PAGED_SMS * 2 * 256;    // rows of partial results: two shared units a run
+static_assert(PAGED_PART_ROWS >= (size_t)PAGED_MAX_RUNS * 2 * PAGED_ROWS, "partial rows of 16-row units");
+bool attn_paged_supports(int Dk, int Dv);
+// Plans and launches a call's kernels; *n_launches receives how many.
+cudaError_t launch_attn_paged(const PagedArgs& a, int Dk, int Dv, kva_dtype dtype, const int32_t* lengths_host,
+                              const int32_t* start_host, cudaStream_t s, unsigned* n_launches);
+cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, kva_dtype dtype, int runs, cudaStream_t s);
+
+struct AppendPagedArgs {
+  const void* q;                      // [T, Hq, Dk], tokens q_stride elements apart (Hq = 0: no queries)
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  void* q_out;                        // [T, Hq, Dk] of the cache's type
+  void* kc;
+  void* vc;
+  const int32_t* pos;                 // [T, n_axes]
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* start;
+  int64_t table_stride, slots, page_stride, page_stride_v;
+  const float* q_w;
+  const float* k_w;
+  float eps, magnitude;               // magnitude: factor of the cosines and sines
+  int after_rope;
+  int B, T, Hq, Hkv, Dk, Dv, page_shift, n_pages;
+  int rot_offset, rot_dim;
+  RopeTable rope;
+};
+cudaError_t launch_append_paged(const AppendPagedArgs& a, kva_dtype in_dtype, kva_dtype cache_dtype, cudaStream_t s);
+
+// Beams over a paged cache: rows are B groups of K beams.
+struct ReorderPagedArgs {
+  void* k;
+  void* v;
+  int64_t page_stride, page_stride_v, layer_stride, layer_stride_v;   // bytes
+  const int32_t* parent;              // [B, K] beam of the group
+  const int32_t* table;               // [B, K, table_stride]
+  const int32_t* lengths;             // [B, K]
+  const int32_t* spare;               // [B, K]
+  int32_t* table_out;
+  int32_t* lengths_out;
+  int32_t* spare_out;
+  int64_t table_stride;
+  int B, K, layers, Hkv, row_k, row_v, page_shift, n_pages;           // row_k, row_v: bytes of a slot's row of one head
+};
+constexpr int BEAM_MAX = KVA_BEAM_MAX;
+cudaError_t launch_reorder_paged(const ReorderPagedArgs& a, cudaStream_t s);
+
+struct BeamArgs {
+  const void* logits;                 // [B, K, V], rows row_stride elements apart
+  int64_t row_stride;
+  const float* scores;                // [B, K]
+  const int32_t* finished;            // [B, K] or null
+  int32_t* out_beam;                  // [B, n]
+  int32_t* out_token;
+  float* out_score;
+  unsigned int* counters;             // [BEAM_MAX_GROUPS] zero on entry, zero on exit
+  float* part_stat;                   // [B * K, splits, 2]: maximum, sum
+  unsigned long long* part_key;       // [B * K, splits, n]
+  int B, K, V, n, end_id, splits;
+};
+constexpr int BEAM_MAX_GROUPS = 4096;
+int beam_splits(int rows, int V);
+int beam_parts_bound(int rows);       // rows * splits of no call of at most so many rows is above it
+cudaError_t launch_beam_select(const BeamArgs& a, kva_dtype dtype, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------
 struct LogprobArgs {
   const void* h;                      // [B, H]
   int h_dtype;                        // kva_dtype

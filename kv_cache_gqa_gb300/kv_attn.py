@@ -52,12 +52,30 @@ class _Norm(C.Structure):
                 ("eps", C.c_float), ("after_rope", C.c_int32)]
 
 
+class _PagedCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("head_dim_v", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("page_stride", C.c_int64), ("page_stride_v", C.c_int64)]
+
+
+class _PagedBatch(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_stride", C.c_int64), ("lengths", C.c_void_p),
+                ("token_start", C.c_void_p), ("table_host", C.c_void_p), ("lengths_host", C.c_void_p),
+                ("token_start_host", C.c_void_p), ("B", C.c_int32)]
+
+
+class _RopeScale(C.Structure):
+    _fields_ = [("factor", C.c_double), ("orig_len", C.c_double), ("low", C.c_double), ("high", C.c_double),
+                ("magnitude", C.c_float)]
+
+
 class _WorkspaceDims(C.Structure):
     _fields_ = [("B", C.c_int32), ("n_kv_heads", C.c_int32), ("n_q_heads", C.c_int32), ("max_len", C.c_int32),
                 ("head_dim", C.c_int32), ("hidden", C.c_int32), ("vocab", C.c_int32), ("block", C.c_int32)]
 
 
-WORKSPACE_KINDS = {"decode": 0, "verify": 1, "lmhead": 2, "lmhead_topk": 3, "decode_q4": 4, "lmhead_logprobs": 5}
+WORKSPACE_KINDS = {"decode": 0, "verify": 1, "lmhead": 2, "lmhead_topk": 3, "decode_q4": 4, "lmhead_logprobs": 5,
+                   "attn_paged": 6, "beam_select": 8}
 Q4_GROUP = 64                       # values of a 4-bit cache row that share a scale and a midpoint
 
 _lib = None
@@ -109,6 +127,23 @@ def lib() -> C.CDLL:
         L.kva_decode_q4_workspace_size.restype = sz
         L.kva_decode_q4_workspace_zero_bytes.argtypes = [i32, i32, i32, i32]
         L.kva_decode_q4_workspace_zero_bytes.restype = sz
+        L.kv_cache_append_paged.argtypes = [vp, i64, vp, i64, vp, i64, C.c_int, i32, vp, _Norm, _Rope, _RopeScale, vp,
+                                            _PagedCache, _PagedBatch, vp]
+        L.kv_cache_append_paged.restype = C.c_int
+        L.kv_attn_paged.argtypes = [vp, C.c_int, _PagedCache, _PagedBatch, i32, C.c_float, vp, C.c_int, vp, sz, vp]
+        L.kv_attn_paged.restype = C.c_int
+        L.kva_paged_workspace_size.argtypes = [i32, i32, i32]
+        L.kva_paged_workspace_size.restype = sz
+        L.kva_paged_workspace_zero_bytes.argtypes = []
+        L.kva_paged_workspace_zero_bytes.restype = sz
+        L.beam_select.argtypes = [vp, C.c_int, i64, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.beam_select.restype = C.c_int
+        L.kva_beam_workspace_size.argtypes = [i32, i32, i32]
+        L.kva_beam_workspace_size.restype = sz
+        L.kva_beam_workspace_zero_bytes.argtypes = []
+        L.kva_beam_workspace_zero_bytes.restype = sz
+        L.kv_cache_reorder_paged.argtypes = [_PagedCache, i32, i64, i64, i32, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.kv_cache_reorder_paged.restype = C.c_int
         L.kva_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         L.kva_decode_workspace_size.restype = sz
         L.kva_decode_workspace_zero_bytes.argtypes = [i32, i32]
@@ -369,7 +404,7 @@ def lmhead_workspace_bytes(B: int, H: int = 1024) -> int:
 def workspace_bytes(kind: str, B: int = 0, n_kv_heads: int = 0, n_q_heads: int = 0, max_len: int = 0,
                     head_dim: int = 0, hidden: int = 0, vocab: int = 0, block: int = 0) -> int:
     """kva_workspace_size: the workspace of the call `kind` names ('decode', 'verify', 'lmhead',
-    'lmhead_topk', 'decode_q4', 'lmhead_logprobs'); 0 for dimensions that are not positive."""
+    'lmhead_topk', 'decode_q4', 'lmhead_logprobs', 'attn_paged', 'beam_select'); 0 for dimensions that are not positive."""
     d = _WorkspaceDims(B, n_kv_heads, n_q_heads, max_len, head_dim, hidden, vocab, block)
     return int(lib().kva_workspace_size(WORKSPACE_KINDS[kind], C.byref(d)))
 
@@ -685,6 +720,296 @@ def lmhead_logprobs(h, W, workspace, targets=None, out_logprob=None, out_entropy
     prepare_lmhead_logprobs(h, W, workspace, targets=targets, out_logprob=out_logprob, out_entropy=out_entropy,
                             out_lse=out_lse, top_ids=top_ids, top_logprobs=top_logprobs, norm_w=norm_w, eps=eps, V=V,
                             stream=stream)()
+
+
+@dataclasses.dataclass
+class PagedKVCache:
+    """A pool of pages: k [n_pages, Hkv, page_size, Dk] and v [n_pages, Hkv, page_size, Dv] torch CUDA tensors (f32 or
+    bf16); the pages may lie apart (a view of a larger pool), a page itself is contiguous.  With a
+    leading dimension, [layers, n_pages, ..], the pools of all layers: layer(i) is one of them."""
+    k: object
+    v: object
+
+    @classmethod
+    def zeros(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, head_dim_v: Optional[int] = None,
+              layers: Optional[int] = None, dtype=None, device="cuda") -> "PagedKVCache":
+        torch = _t()
+        lead = (n_pages,) if layers is None else (layers, n_pages)
+        make = lambda d: torch.zeros(lead + (n_kv_heads, page_size, d), dtype=dtype or torch.bfloat16, device=device)  # noqa: E731
+        return cls(make(head_dim), make(head_dim if head_dim_v is None else head_dim_v))
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_struct", None)        # rebuilt on the next call
+
+    @property
+    def layers(self) -> int:
+        return self.k.shape[0] if self.k.dim() == 5 else 1
+
+    def layer(self, i: int) -> "PagedKVCache":
+        return PagedKVCache(self.k[i], self.v[i])
+
+    @property
+    def struct(self) -> _PagedCache:
+        st = getattr(self, "_struct", None)
+        if st is None:
+            st = self._build_struct()
+            object.__setattr__(self, "_struct", st)
+        return st
+
+    def _build_struct(self) -> _PagedCache:
+        k, v = self.k, self.v
+        if k.dim() not in (4, 5) or v.dim() != k.dim() or v.shape[:-1] != k.shape[:-1] or v.dtype != k.dtype:
+            raise KvaError(KVA_EINVAL, "paged cache k/v must be [(layers,) n_pages, Hkv, page, Dk] / [.., Dv] tensors of one dtype")
+        for t in (k, v):
+            want = 1
+            for d in (-1, -2, -3):
+                if t.shape[d] != 1 and t.stride(d) != want:
+                    raise KvaError(KVA_EINVAL, "a page of the cache must be contiguous")
+                want *= t.shape[d]
+            if _ptr(t) is None or t.device.index != _t().cuda.current_device():
+                raise KvaError(KVA_EINVAL, f"paged cache is on {t.device}, not on the current device")
+        n, Hkv, page, D = k.shape[-4:]
+        apart = lambda t: t.stride(-4) if n > 1 else 0  # noqa: E731
+        return _PagedCache(_ptr(k), _ptr(v), _dtype_code(k), Hkv, D, v.shape[-1], page, n, apart(k), apart(v))
+
+    @property
+    def n_pages(self):
+        return self.k.shape[-4]
+
+    @property
+    def n_kv_heads(self):
+        return self.k.shape[-3]
+
+    @property
+    def page_size(self):
+        return self.k.shape[-2]
+
+    @property
+    def head_dim(self):
+        return self.k.shape[-1]
+
+    @property
+    def head_dim_v(self):
+        return self.v.shape[-1]
+
+
+@dataclasses.dataclass
+class PagedBatch:
+    """The sequences of a step and their new tokens (kva_paged_batch in include/kv_attn.h): table [B, pages] int32
+    CUDA page ids, lengths [B] int32 CUDA slots with the new tokens, token_start [B+1] int32 CUDA: sequence b's new
+    tokens are rows token_start[b] .. token_start[b+1]-1 of the call; host mirrors lengths_host (or upper bounds),
+    token_start_host, and table_host where page ids are to be checked."""
+    table: object
+    lengths: object
+    token_start: object
+    lengths_host: object
+    token_start_host: object
+    table_host: object = None
+
+    def __setattr__(self, name, value):
+        if name.endswith("_host") and value is not None:
+            value = _host_i32(value)
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_struct", None)        # rebuilt on the next call
+
+    @property
+    def struct(self) -> _PagedBatch:
+        st = getattr(self, "_struct", None)
+        if st is None:
+            st = self._build_struct()
+            object.__setattr__(self, "_struct", st)
+        return st
+
+    @property
+    def tokens(self) -> int:
+        return int(self.token_start_host[-1])
+
+    def _build_struct(self) -> _PagedBatch:
+        torch = _t()
+        B = self.lengths.shape[0]
+        i32 = (torch.int32,)
+        _want(self.table, "table", (B, None), i32)
+        _want(self.lengths, "lengths", (B,), i32)
+        _want(self.token_start, "token_start", (B + 1,), i32)
+        th, lh, sh = self.table_host, self.lengths_host, self.token_start_host
+        if lh.shape != (B,) or sh.shape != (B + 1,) or (th is not None and th.shape != tuple(self.table.shape)):
+            raise KvaError(KVA_EINVAL, "host mirrors must have the shapes of lengths, token_start and table")
+        return _PagedBatch(_ptr(self.table), self.table.shape[1], _ptr(self.lengths), _ptr(self.token_start), _ptr(th),
+                           _ptr(lh), _ptr(sh), B)
+
+
+@dataclasses.dataclass(frozen=True)
+class RopeScale:
+    """Frequencies for contexts beyond the trained one (kva_rope_scale in include/kv_attn.h): what turns less than `low`
+    times within orig_len positions is slowed down by `factor`, what turns more than `high` times stays, the ones
+    between are interpolated; orig_len 0: all of them by `factor`.  `magnitude` multiplies cosines and sines."""
+    factor: float = 1.0
+    orig_len: float = 0.0
+    low: float = 1.0
+    high: float = 32.0
+    magnitude: float = 1.0
+
+    @property
+    def struct(self) -> _RopeScale:
+        return _RopeScale(self.factor, self.orig_len, self.low, self.high, self.magnitude)
+
+
+def _token_rows(t, name, shape, dtypes):
+    """Elements between the tokens of [T, heads, D] rows that are contiguous but may lie apart."""
+    torch = _t()
+    if t is None or isinstance(t, np.ndarray) or not t.is_cuda:
+        raise KvaError(KVA_EINVAL, f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise KvaError(KVA_EINVAL, f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 3 or any(w is not None and int(g) != int(w) for g, w in zip(t.shape, shape)):
+        raise KvaError(KVA_EINVAL, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise KvaError(KVA_EINVAL, f"{name} is on {t.device}, not on the current device")
+    T, H, D = t.shape
+    if (D != 1 and t.stride(2) != 1) or (H != 1 and t.stride(1) != D):
+        raise KvaError(KVA_EINVAL, f"{name}: a token's heads must be contiguous")
+    if T > 1 and t.stride(0) < H * D:
+        raise KvaError(KVA_EINVAL, f"{name}: tokens overlap")
+    return t.stride(0) if T > 1 else 0
+
+
+def prepare_append_paged(q, k, v, pos, cache: PagedKVCache, batch: PagedBatch, q_out, rope: Rope,
+                         rope_scale: Optional[RopeScale] = None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6,
+                         norm_after_rope: bool = False, stream=None) -> PreparedCall:
+    """kv_cache_append_paged with its arguments marshalled once (see PreparedCall)."""
+    torch = _t()
+    if cache.k.dim() != 4:
+        raise KvaError(KVA_EINVAL, "the append takes one layer's pool: cache.layer(i)")
+    T, Hkv = batch.tokens, cache.n_kv_heads
+    ks = _token_rows(k, "k", (T, Hkv, cache.head_dim), _floats())
+    vs = _token_rows(v, "v", (T, Hkv, cache.head_dim_v), (k.dtype,))
+    Hq = qs = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _token_rows(q, "q", (T, None, cache.head_dim), (k.dtype,))
+        if q_out is not None:
+            _want(q_out, "q_out", (T, Hq, cache.head_dim), (cache.k.dtype,))
+    if rope.kind != "none" and pos is not None:
+        _want(pos, "pos", (T, rope.n_axes), (torch.int32,))
+    for w, name in ((q_norm_w, "q_norm_w"), (k_norm_w, "k_norm_w")):
+        if w is not None:
+            _want(w, name, (cache.head_dim,), (torch.float32,))
+    norm = _Norm(_ptr(q_norm_w), _ptr(k_norm_w), 0, eps, 1 if norm_after_rope else 0)
+    scale = rope_scale.struct if rope_scale is not None else _RopeScale()
+    args = (_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _dtype_code(k), Hq, _ptr(pos), norm, rope.struct, scale, _ptr(q_out),
+            cache.struct, batch.struct, _stream(stream))
+    return PreparedCall(lib().kv_cache_append_paged, args, (q, k, v, pos, cache, batch, q_out, rope, q_norm_w, k_norm_w))
+
+
+def kv_cache_append_paged(q, k, v, pos, cache: PagedKVCache, batch: PagedBatch, q_out, rope: Rope,
+                          rope_scale: Optional[RopeScale] = None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6,
+                          norm_after_rope: bool = False, stream=None):
+    """QK-Norm, RoPE and cache write of a batch's new tokens: q [T,Hq,Dk], k [T,Hkv,Dk], v [T,Hkv,Dv] (CUDA, f32|bf16, one
+    dtype; tokens may lie apart, as in a fused projection's rows), pos [T,n_axes] int32 CUDA, q_out [T,Hq,Dk] of the
+    cache's dtype, packed; q and q_out may be None.  Norm weights [Dk] f32."""
+    prepare_append_paged(q, k, v, pos, cache, batch, q_out, rope, rope_scale=rope_scale, q_norm_w=q_norm_w,
+                         k_norm_w=k_norm_w, eps=eps, norm_after_rope=norm_after_rope, stream=stream)()
+
+
+def paged_workspace_bytes(n_kv_heads: int, n_q_heads: int, head_dim_v: int) -> int:
+    return int(lib().kva_paged_workspace_size(n_kv_heads, n_q_heads, head_dim_v))
+
+
+def paged_workspace_zero_bytes() -> int:
+    return int(lib().kva_paged_workspace_zero_bytes())
+
+
+def prepare_attn_paged(q, cache: PagedKVCache, batch: PagedBatch, out, workspace, scale: float = 0.0,
+                       stream=None) -> PreparedCall:
+    """kv_attn_paged with its arguments marshalled once (see PreparedCall)."""
+    if cache.k.dim() != 4:
+        raise KvaError(KVA_EINVAL, "the attention takes one layer's pool: cache.layer(i)")
+    T = batch.tokens
+    _want(q, "q", (T, None, cache.head_dim), (cache.k.dtype,))
+    _want(out, "out", (T, q.shape[1], cache.head_dim_v), _floats())
+    args = (_ptr(q), _dtype_code(q), cache.struct, batch.struct, q.shape[1], float(scale), _ptr(out), _dtype_code(out),
+            *_workspace_args(workspace), _stream(stream))
+    return PreparedCall(lib().kv_attn_paged, args, (q, cache, batch, out, workspace))
+
+
+def kv_attn_paged(q, cache: PagedKVCache, batch: PagedBatch, out, workspace, scale: float = 0.0, stream=None):
+    """Attention of a batch's new tokens, q [T,Hq,Dk] of the cache's dtype (one or many a sequence), over their
+    sequences' pages, which already hold them; out [T,Hq,Dv] f32|bf16; workspace: uint8 CUDA, zeroed once."""
+    prepare_attn_paged(q, cache, batch, out, workspace, scale=scale, stream=stream)()
+
+
+def beam_workspace_bytes(B: int, K: int, V: int) -> int:
+    return int(lib().kva_beam_workspace_size(B, K, V))
+
+
+def beam_workspace_zero_bytes() -> int:
+    return int(lib().kva_beam_workspace_zero_bytes())
+
+
+def prepare_beam_select(logits, scores, out_beam, out_token, out_score, workspace, finished=None, end_id: int = 0,
+                        stream=None) -> PreparedCall:
+    """beam_select with its arguments marshalled once (see PreparedCall)."""
+    torch = _t()
+    if logits is None or isinstance(logits, np.ndarray) or not logits.is_cuda or logits.dim() != 3:
+        raise KvaError(KVA_EINVAL, "logits: expected a CUDA tensor [B, K, V]")
+    B, K, V = logits.shape
+    if logits.dtype not in _floats():
+        raise KvaError(KVA_EINVAL, f"logits: unsupported dtype {logits.dtype}")
+    if logits.device.index != torch.cuda.current_device():
+        raise KvaError(KVA_EINVAL, f"logits are on {logits.device}, not on the current device")
+    row = logits.stride(1) if K > 1 else (logits.stride(0) if B > 1 else 0)
+    if (V > 1 and logits.stride(2) != 1) or (K > 1 and B > 1 and logits.stride(0) != K * row) or (B * K > 1 and row < V):
+        raise KvaError(KVA_EINVAL, "logits: rows must be contiguous and equally far apart")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _want(scores, "scores", (B, K), f32)
+    if finished is not None:
+        _want(finished, "finished", (B, K), i32)
+    n = out_beam.shape[-1] if out_beam is not None and out_beam.dim() else 0
+    _want(out_beam, "out_beam", (B, n), i32)
+    _want(out_token, "out_token", (B, n), i32)
+    _want(out_score, "out_score", (B, n), f32)
+    args = (_ptr(logits), _dtype_code(logits), row, B, K, V, _ptr(scores), _ptr(finished), int(end_id), n, _ptr(out_beam),
+            _ptr(out_token), _ptr(out_score), *_workspace_args(workspace), _stream(stream))
+    return PreparedCall(lib().beam_select, args, (logits, scores, out_beam, out_token, out_score, workspace, finished))
+
+
+def beam_select(logits, scores, out_beam, out_token, out_score, workspace, finished=None, end_id: int = 0, stream=None):
+    """The n best continuations of each group over its beams and vocabulary: logits [B,K,V] f32|bf16 CUDA (rows may lie
+    apart), scores [B,K] f32; out_beam, out_token [B,n] int32, out_score [B,n] f32; finished [B,K] int32 CUDA or None: a
+    finished beam offers (end_id, its score) alone; workspace: uint8 CUDA, zeroed once."""
+    prepare_beam_select(logits, scores, out_beam, out_token, out_score, workspace, finished=finished, end_id=end_id,
+                        stream=stream)()
+
+
+def prepare_reorder_paged(cache: PagedKVCache, parent, table, lengths, lengths_host, spare, table_out, lengths_out,
+                          spare_out, stream=None) -> PreparedCall:
+    """kv_cache_reorder_paged with its arguments marshalled once (see PreparedCall)."""
+    torch = _t()
+    i32 = (torch.int32,)
+    _want(parent, "parent", (None, None), i32)
+    B, K = parent.shape
+    _want(table, "table", (B, K, None), i32)
+    _want(table_out, "table_out", tuple(table.shape), i32)
+    for t, name in ((lengths, "lengths"), (spare, "spare"), (lengths_out, "lengths_out"), (spare_out, "spare_out")):
+        _want(t, name, (B, K), i32)
+    lh = _host_i32(lengths_host)
+    if lh.size != B * K:
+        raise KvaError(KVA_EINVAL, f"lengths_host must hold {B * K} lengths")
+    many = cache.layers > 1
+    args = (cache.struct, cache.layers, cache.k.stride(0) if many else 0, cache.v.stride(0) if many else 0, B, K,
+            _ptr(parent), _ptr(table), table.shape[2], _ptr(lengths), lh.ctypes.data, _ptr(spare), _ptr(table_out),
+            _ptr(lengths_out), _ptr(spare_out), _stream(stream))
+    return PreparedCall(lib().kv_cache_reorder_paged, args,
+                        (cache, parent, table, lengths, lh, spare, table_out, lengths_out, spare_out))
+
+
+def kv_cache_reorder_paged(cache: PagedKVCache, parent, table, lengths, lengths_host, spare, table_out, lengths_out,
+                           spare_out, stream=None):
+    """Beams go on from their parents: parent, lengths, spare [B,K] and table [B,K,pages] int32 CUDA (lengths_host: host
+    copy), over the pools of one layer or of all ([layers, ..]); outputs like table, lengths and spare."""
+    prepare_reorder_paged(cache, parent, table, lengths, lengths_host, spare, table_out, lengths_out, spare_out,
+                          stream=stream)()
 
 
 def launch_count() -> int:
