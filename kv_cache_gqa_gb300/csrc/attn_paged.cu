@@ -1,35 +1,101 @@
 // Plan of kv_attn_paged: which kernels a batch needs and how many runs each gets.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "launch.h"
 
 namespace kva {
 
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// Steps and units of the sequences of lo < T * G <= hi rows, in tiles of `tile` rows and steps of `keys` slots.
+struct Load {
+  int64_t steps = 0, units = 0;
+};
+Load load_of(const PagedArgs& a, const int32_t* lengths, const int32_t* start, int64_t lo, int64_t hi, int tile, int keys) {
+  const int G = a.Hq / a.Hkv;
+  Load w;
+  for (int b = 0; b < a.B; ++b) {
+    const int64_t rows = (int64_t)(start[b + 1] - start[b]) * G;
+    if (rows <= lo || rows > hi) continue;
+    const int64_t n = (rows + tile - 1) / tile * a.Hkv;
+    w.units += n;
+    w.steps += n * std::max(1, (lengths[b] + keys - 1) / keys);
+  }
+  return w;
+}
+
+// As many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps.
+int runs_of(const Load& w, int slots) {
+  const int64_t most = std::min<int64_t>(slots, (int64_t)(2.0 * std::sqrt((double)w.steps * (double)w.units)));
+  return (int)std::max<int64_t>(1, std::min(most, w.steps));
+}
+
+}  // namespace
+
 bool attn_paged_supports(int Dk, int Dv) {
   return (Dk == 64 && Dv == 64) || (Dk == 128 && Dv == 128) || (Dk == 192 && Dv == 128);
 }
 
+// A bf16 pool as (width, slot of a page, KV head, page): boxes of [rows x 64 columns] with 128-byte swizzle.
+cudaError_t paged_pool_map(CUtensorMap* map, const void* base, const PagedArgs& a, int width, int64_t page_stride, int rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t page = 1u << a.page_shift;
+  const cuuint64_t dims[4] = {(cuuint64_t)width, page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)width * 2, page * width * 2, (cuuint64_t)page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_attn_paged(const PagedArgs& args, int Dk, int Dv, kva_dtype dtype, const int32_t* lengths,
                               const int32_t* start, cudaStream_t s, unsigned* n_launches) {
-  const int G = args.Hq / args.Hkv;
-  int64_t steps = 0, units = 0;
-  for (int b = 0; b < args.B; ++b) {
-    const int64_t rows = (int64_t)(start[b + 1] - start[b]) * G;
-    if (rows == 0) continue;
-    const int64_t n = (rows + PAGED_ROWS - 1) / PAGED_ROWS * args.Hkv;
-    units += n;
-    steps += n * std::max(1, (lengths[b] + 127) / 128);
-  }
   PagedArgs a = args;
-  a.rows_lo = 0;
-  a.rows_hi = INT32_MAX;
-  // as many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps
-  const int64_t most = std::min<int64_t>(PAGED_SMS * 3, (int64_t)(2.0 * std::sqrt((double)steps * (double)units)));
-  const int runs = (int)std::max<int64_t>(1, std::min(most, steps));
+  cudaError_t e = cudaSuccess;
   (void)Dv;
-  const cudaError_t e = launch_attn_paged_simt(a, Dk, dtype, runs, s);
-  if (e == cudaSuccess) *n_launches = 1;
+  a.rows_lo = 0;
+  if (dtype == KVA_BF16) {                       // few rows a sequence: mma.sync tiles
+    int rows = 0;
+    for (int b = 0; b < a.B; ++b) {
+      const int64_t n = (int64_t)(start[b + 1] - start[b]) * (a.Hq / a.Hkv);
+      if (n <= PAGED_ROWS) rows = std::max(rows, (int)n);
+    }
+    a.rows_hi = PAGED_ROWS;
+    if (rows > 0) {
+      const Load w = load_of(a, lengths, start, 0, PAGED_ROWS, PAGED_ROWS, 64);
+      e = launch_attn_paged_step(a, Dk, rows, runs_of(w, PAGED_SMS * 2), s);
+      if (e != cudaSuccess) return e;
+      ++*n_launches;
+    }
+    a.rows_lo = PAGED_ROWS;
+  }
+  a.rows_hi = INT32_MAX;
+  const Load w = load_of(a, lengths, start, a.rows_lo, a.rows_hi, PAGED_ROWS, 128);
+  if (w.units == 0) return e;
+  e = launch_attn_paged_simt(a, Dk, dtype, runs_of(w, PAGED_SMS * 3), s);
+  if (e == cudaSuccess) ++*n_launches;
   return e;
 }
 

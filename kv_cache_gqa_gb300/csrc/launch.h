@@ -305,6 +305,9 @@ bool attn_paged_supports(int Dk, int Dv);
 // Plans and launches a call's kernels; *n_launches receives how many.
 cudaError_t launch_attn_paged(const PagedArgs& a, int Dk, int Dv, kva_dtype dtype, const int32_t* lengths_host,
                               const int32_t* start_host, cudaStream_t s, unsigned* n_launches);
+cudaError_t paged_pool_map(CUtensorMap* map, const void* base, const PagedArgs& a, int width, int64_t page_stride, int rows);
+// Sequences of at most PAGED_ROWS query rows a KV head, `rows` at most (bf16 caches).
+cudaError_t launch_attn_paged_step(const PagedArgs& a, int Dk, int rows, int runs, cudaStream_t s);
 cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, kva_dtype dtype, int runs, cudaStream_t s);
 
 struct AppendPagedArgs {
