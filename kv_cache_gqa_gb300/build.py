@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkv_attn.so")
-SOURCES = ["kv_attn_api.cu", "append.cu", "append_general.cu", "append_paged.cu", "append_q4.cu", "attn_paged.cu", "attn_paged_simt.cu", "attn_paged_step.cu", "beam.cu", "decode.cu", "decode_mma.cu", "decode_q4.cu",
+SOURCES = ["kv_attn_api.cu", "append.cu", "append_general.cu", "append_paged.cu", "append_q4.cu", "attn_paged.cu", "attn_paged_chunk.cu", "attn_paged_simt.cu", "attn_paged_step.cu", "beam.cu", "decode.cu", "decode_mma.cu", "decode_q4.cu",
            "decode_static.cu", "lmhead.cu", "lmhead_tc.cu", "lmhead_topk.cu", "logprobs.cu", "prefill_simt.cu", "prefill_tc.cu", "reorder_paged.cu", "verify_mma.cu", "verify_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

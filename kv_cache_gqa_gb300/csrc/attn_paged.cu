@@ -70,32 +70,57 @@ cudaError_t paged_pool_map(CUtensorMap* map, const void* base, const PagedArgs& 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The queries as (width, head, token): boxes of [tokens x heads x 64 columns], rows in (token, head) order.
+cudaError_t paged_query_map(CUtensorMap* map, const PagedArgs& a, int width, int heads, int tokens) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)a.Hq, (cuuint64_t)a.T, 1};
+  const cuuint64_t row = (cuuint64_t)width * 2;
+  const cuuint64_t strides[3] = {row, row * a.Hq, row * a.Hq * a.T};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// float32 caches: CUDA cores.  bf16 caches: mma.sync tiles of 16 rows for sequences of up to 16 rows a KV head, and for all of
+// them where the output is float32 (the only form that holds its weights and sums to 24 bits); tcgen05 for the others.
 cudaError_t launch_attn_paged(const PagedArgs& args, int Dk, int Dv, kva_dtype dtype, const int32_t* lengths,
                               const int32_t* start, cudaStream_t s, unsigned* n_launches) {
   PagedArgs a = args;
+  const int G = a.Hq / a.Hkv;
   cudaError_t e = cudaSuccess;
-  (void)Dv;
   a.rows_lo = 0;
-  if (dtype == KVA_BF16) {                       // few rows a sequence: mma.sync tiles
-    int rows = 0;
-    for (int b = 0; b < a.B; ++b) {
-      const int64_t n = (int64_t)(start[b + 1] - start[b]) * (a.Hq / a.Hkv);
-      if (n <= PAGED_ROWS) rows = std::max(rows, (int)n);
-    }
-    a.rows_hi = PAGED_ROWS;
-    if (rows > 0) {
-      const Load w = load_of(a, lengths, start, 0, PAGED_ROWS, PAGED_ROWS, 64);
-      e = launch_attn_paged_step(a, Dk, rows, runs_of(w, PAGED_SMS * 2), s);
-      if (e != cudaSuccess) return e;
-      ++*n_launches;
-    }
-    a.rows_lo = PAGED_ROWS;
-  }
   a.rows_hi = INT32_MAX;
-  const Load w = load_of(a, lengths, start, a.rows_lo, a.rows_hi, PAGED_ROWS, 128);
-  if (w.units == 0) return e;
-  e = launch_attn_paged_simt(a, Dk, dtype, runs_of(w, PAGED_SMS * 3), s);
-  if (e == cudaSuccess) ++*n_launches;
+  if (dtype == KVA_F32) {
+    const Load w = load_of(a, lengths, start, 0, INT32_MAX, PAGED_ROWS, 128);
+    e = launch_attn_paged_simt(a, Dk, dtype, runs_of(w, PAGED_SMS * 3), s);
+    if (e == cudaSuccess) ++*n_launches;
+    return e;
+  }
+  if (a.out_bf16) a.rows_hi = PAGED_ROWS;
+  int rows = 0;                                  // the most rows of a sequence in the class
+  Load more;
+  for (int b = 0; b < a.B; ++b) {
+    const int T = start[b + 1] - start[b];
+    if ((int64_t)T * G <= a.rows_hi) rows = std::max(rows, T * G);
+    else attn_paged_chunk_load(T, lengths[b], G, &more.steps, &more.units);
+  }
+  if (rows > 0) {
+    const Load w = load_of(a, lengths, start, 0, a.rows_hi, PAGED_ROWS, 64);
+    e = launch_attn_paged_step(a, Dk, rows, runs_of(w, PAGED_SMS * 2), s);
+    if (e != cudaSuccess) return e;
+    ++*n_launches;
+  }
+  if (more.units > 0) {
+    more.steps *= a.Hkv;
+    more.units *= a.Hkv;
+    a.rows_lo = PAGED_ROWS;
+    a.rows_hi = INT32_MAX;
+    e = launch_attn_paged_chunk(a, Dk, Dv, runs_of(more, PAGED_SMS), s, n_launches);
+  }
   return e;
 }
 

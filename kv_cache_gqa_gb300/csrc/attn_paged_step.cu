@@ -1,7 +1,7 @@
-// Attention of few new tokens a sequence over a paged bf16 cache (kv_attn_paged): single tokens and short draft
-// blocks, up to 16 query rows (token, head of the group) a KV head.
+// Attention over a paged bf16 cache in tiles of up to 16 query rows (kv_attn_paged): single tokens and short draft blocks (up
+// to 16 rows (token, head of the group) a KV head), and chunks of any length where the output is float32.
 //
-// A unit is (sequence, KV head), a step 64 slots: 16 for each of the CTA's four warps, which are independent until
+// A unit is a row tile of a (sequence, KV head), a step 64 slots: 16 for each of the CTA's four warps, which are independent until
 // the unit's end.  A warp streams its 16-key tiles through a ring of NS shared-memory stages: lane 0 issues TMA copies,
 // [16 keys x 64 dims] boxes with 128-byte swizzle, whose page the warp has looked up 32 tiles ahead (a page
 // holds whole tiles), and ldmatrix reads them without bank conflicts.  Per tile mma.sync m16n8k16 forms S = q K^T,
@@ -91,8 +91,8 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
 
   for (; p.b < a.B && p.at < run.x1; p.next(a, cut)) {
     const int st0 = (int)max((int64_t)0, run.x0 - p.at), st1 = (int)min((int64_t)p.n_steps, run.x1 - p.at);
-    const int rows = p.s.T * G;                 // one tile of rows (the class of this launch)
-    const int lim_all = p.s.L;                  // slots that the last token sees
+    const int64_t rows = (int64_t)p.s.T * G - (int64_t)p.rt * ROWS;    // of this tile and the ones behind it
+    const int lim_all = cut.visible(p.s, p.rt); // slots that the tile's last row sees
     const int first = (st0 * WARPS + warp) * KT;                  // first key of this warp's first tile
     const int n_mine = !ok ? 0 : max(0, min(st1 - st0, (lim_all - first + KT * WARPS - 1) / (KT * WARPS)));
     const int32_t* pages = a.table + (int64_t)p.b * a.table_stride;
@@ -129,11 +129,11 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
     int lim_min = lim_all;                      // and what every row sees
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const int row = r + 8 * h;
-      const bool on = row < rows;
+      const bool on = r + 8 * h < rows;
+      const int row = on ? p.rt * ROWS + r + 8 * h : 0;
       lim[h] = on ? min(max(p.s.L - p.s.T + row / G + 1, 0), p.s.L) : lim_all;
       const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) +
-                          ((int64_t)(p.s.t0 + (on ? row / G : 0)) * a.Hq + p.g * G + (on ? row % G : 0)) * DK + 2 * t;
+                          ((int64_t)(p.s.t0 + row / G) * a.Hq + p.g * G + row % G) * DK + 2 * t;
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
         qa[h][kk][0] = on ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * kk)) : 0u;

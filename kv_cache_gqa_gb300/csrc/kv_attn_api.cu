@@ -1136,8 +1136,8 @@ size_t kva_paged_workspace_zero_bytes(void) { return round_up(sizeof(unsigned) *
 
 size_t kva_paged_workspace_size(int32_t n_kv_heads, int32_t n_q_heads, int32_t head_dim_v) {
   if (n_kv_heads <= 0 || n_q_heads <= 0 || head_dim_v <= 0 || n_q_heads % n_kv_heads != 0) return 0;
-  return kva_paged_workspace_zero_bytes() + round_up(sizeof(float) * PAGED_PART_ROWS * 2, 256) +
-         sizeof(float) * PAGED_PART_ROWS * head_dim_v;
+  return kva_paged_workspace_zero_bytes() + round_up(sizeof(PagedJoin) * PAGED_SMS, 256) +
+         round_up(sizeof(float) * PAGED_PART_ROWS * 2, 256) + sizeof(float) * PAGED_PART_ROWS * head_dim_v;
 }
 
 kva_status kv_attn_paged(
@@ -1157,7 +1157,7 @@ kva_status kv_attn_paged(
     return fail(KVA_EUNSUPPORTED, "paged attention: head dims %d/%d (built: 64/64, 128/128, 192/128)", Dk, Dv);
   const int G = n_q_heads / Hkv;
   if (G > 64) return fail(KVA_EUNSUPPORTED, "paged attention: %d query heads a KV head (at most 64)", G);
-  if ((int64_t)T * G > INT32_MAX - 512) return fail(KVA_EUNSUPPORTED, "paged attention: too many query rows");
+  if ((int64_t)T * n_q_heads > INT32_MAX - 512) return fail(KVA_EUNSUPPORTED, "paged attention: too many query rows");
   if (!q || !out) return fail(KVA_EINVAL, "NULL q/out");
   if (!aligned16(q) || !aligned16(out)) return fail(KVA_EALIGN, "q/out must be 16-byte aligned");
   if (!workspace) return fail(KVA_EWORKSPACE, "paged attention: workspace is NULL");
@@ -1167,7 +1167,8 @@ kva_status kv_attn_paged(
   PagedArgs a{};
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.counters = reinterpret_cast<unsigned*>(ws);
-  a.part_ml = reinterpret_cast<float*>(ws + kva_paged_workspace_zero_bytes());
+  a.joins = reinterpret_cast<PagedJoin*>(ws + kva_paged_workspace_zero_bytes());
+  a.part_ml = reinterpret_cast<float*>(ws + kva_paged_workspace_zero_bytes() + round_up(sizeof(PagedJoin) * PAGED_SMS, 256));
   a.part_acc = a.part_ml + round_up(sizeof(float) * PAGED_PART_ROWS * 2, 256) / sizeof(float);
   a.q = q; a.k = cache.k; a.v = cache.v; a.out = out; a.out_bf16 = out_dtype == KVA_BF16;
   a.table = batch.table; a.lengths = batch.lengths; a.start = batch.token_start;

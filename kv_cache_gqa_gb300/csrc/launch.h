@@ -279,6 +279,10 @@ cudaError_t launch_decode_q4(const DecodeQ4Args& a, kva_dtype q_dtype, cudaStrea
 
 // ---------------------------------------------------------------------------------
 // The paged cache (layout: kva_paged_cache and kva_paged_batch in kv_attn.h).
+struct PagedJoin {                     // a unit of two row tiles that begins in a run and goes on in others (last < 0: none)
+  int first, last;                    // its first part, and the run of its last one
+  int t0, T, g, rt, halves;
+};
 struct PagedArgs {
   const void* q;                      // [T, Hq, Dk]
   const void* k;                      // [n_pages, Hkv, page, Dk], pages page_stride elements apart
@@ -287,6 +291,7 @@ struct PagedArgs {
   const int32_t* lengths;             // [B]
   const int32_t* start;               // [B + 1]
   void* out;                          // [T, Hq, Dv]
+  PagedJoin* joins;                   // [PAGED_SMS]
   unsigned int* counters;             // [PAGED_MAX_RUNS], by a shared unit's first run; zero on entry, zero on exit
   float* part_acc;                    // [runs, 2, rows, Dv]
   float* part_ml;                     // [runs, 2, rows, 2]
@@ -308,6 +313,10 @@ cudaError_t launch_attn_paged(const PagedArgs& a, int Dk, int Dv, kva_dtype dtyp
 cudaError_t paged_pool_map(CUtensorMap* map, const void* base, const PagedArgs& a, int width, int64_t page_stride, int rows);
 // Sequences of at most PAGED_ROWS query rows a KV head, `rows` at most (bf16 caches).
 cudaError_t launch_attn_paged_step(const PagedArgs& a, int Dk, int rows, int runs, cudaStream_t s);
+// Sequences of more rows, bf16 caches and outputs.
+cudaError_t paged_query_map(CUtensorMap* map, const PagedArgs& a, int width, int heads, int tokens);
+cudaError_t launch_attn_paged_chunk(const PagedArgs& a, int Dk, int Dv, int runs, cudaStream_t s, unsigned* n_launches);
+void attn_paged_chunk_load(int T, int L, int G, int64_t* steps, int64_t* units);
 cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, kva_dtype dtype, int runs, cudaStream_t s);
 
 struct AppendPagedArgs {
