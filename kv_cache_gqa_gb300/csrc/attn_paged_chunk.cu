@@ -13,8 +13,9 @@
 //             maximum (O is rescaled when a score exceeds it by 2^8), P = exp2(S - m) written back over S as bf16.
 //   8, 10     TMA of Q and K, and of V.  A key tile is a box for each page it touches; the warp holds the next page ids a lane
 //             each.  Slots of a tile at or beyond L are zeroed in V (they may hold anything, and 0 * NaN is NaN).
-//   9         issues the products from a converged warp (one elected lane): O_s += P_s V for a tile, then S_s of the slot's
-//             next tile into the same columns, while the other slot's softmax runs.
+//   9, 11     issue the products of slots 0 and 1 from converged warps (one elected lane): O += P V for a tile, in two halves as
+//             the softmax hands them over, then S of the slot's next tile into the same columns.  One warp for both slots was busy
+//             all the time with its waits, descriptors and commits (4100 cycles a step; the products take 2048).
 // Tensor memory: S of slot s at columns [128 s, 128 s + 128), O at [256 + 128 s, ..).  Every wait is bounded; one that
 // gives up ends the CTA's work, and its rows become NaN.
 //
@@ -37,7 +38,7 @@ using paged::Seq;
 
 constexpr int BM = 128, BN = 128;          // query rows of a slot, keys of a tile
 constexpr int SOFTMAX_WARPS = 8;
-constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // warp 11 completes its warpgroup and idles
+constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // and MMA_WARP + 2 for slot 1
 constexpr int THREADS = 384;
 // Registers: 168 a thread at launch; the control warpgroup gives up 48, which the two softmax warpgroups take.
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 192, REGS_CONTROL = 120;
@@ -220,16 +221,16 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + LY::BAR_OFF);
   uint64_t* k_full = bars + 0;     // [NK] K tile landed
-  uint64_t* k_free = bars + 2;     // [NK] its products done
+  uint64_t* k_free = bars + 2;     // [NK] both slots are through with it
   uint64_t* v_full = bars + 4;     // [NV]
   uint64_t* v_free = bars + 6;     // [NV]
   uint64_t* s_full = bars + 8;     // [slot] S ready
-  uint64_t* p_full = bars + 10;    // [slot] P written by the slot's 4 warps
-  uint64_t* pv_done = bars + 12;   // [slot] P V of the slot's tile done
+  uint64_t* p_half = bars + 10;    // [slot] P of the tile's first 64 keys written by the slot's 4 warps
+  uint64_t* p_full = bars + 12;    // [slot] and of the other 64
   uint64_t* o_full = bars + 14;    // [slot] the piece's last P V done
   uint64_t* o_free = bars + 16;    // [slot] O copied out (by 4 warps)
   uint64_t* q_full = bars + 18;    // the piece's Q landed
-  uint64_t* q_free = bars + 19;    // the piece's last Q K^T done
+  uint64_t* q_free = bars + 19;    // both slots' last Q K^T of the piece done
   uint64_t* v_clean = bars + 20;   // [NV] the tile that holds L has its V cleaned
   uint64_t* ml_full = bars + 22;   // slot 1's maxima and sums of a halves piece published (4 warps)
   uint64_t* ml_free = bars + 23;   // and read by slot 0 (4 warps)
@@ -243,11 +244,11 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   if (warp == MMA_WARP) tc::tmem_alloc(s_taddr, TMEM_COLS);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1); mbar_init(&k_free[i], 1); mbar_init(&v_full[i], 1); mbar_init(&v_free[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], SOFTMAX_WARPS / 2); mbar_init(&pv_done[i], 1);
+      mbar_init(&k_full[i], 1); mbar_init(&k_free[i], 2); mbar_init(&v_full[i], 1); mbar_init(&v_free[i], 2);
+      mbar_init(&s_full[i], 1); mbar_init(&p_half[i], SOFTMAX_WARPS / 2); mbar_init(&p_full[i], SOFTMAX_WARPS / 2);
       mbar_init(&o_full[i], 1); mbar_init(&o_free[i], SOFTMAX_WARPS / 2); mbar_init(&v_clean[i], 1);
     }
-    mbar_init(q_full, 1); mbar_init(q_free, 1);
+    mbar_init(q_full, 1); mbar_init(q_free, 2);
     mbar_init(ml_full, SOFTMAX_WARPS / 2); mbar_init(ml_free, SOFTMAX_WARPS / 2);
     *s_abort = 0;
     fence_mbar_init();
@@ -323,68 +324,90 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       }
       if (!ok) *s_abort = 1;
       for (int e = max(0, it - NV); e < it; ++e) (void)warp_wait(&v_full[e % NV], e / NV);
-    } else if (warp == MMA_WARP) {
-      // ------------------------------------------------------------ products
+    } else {
+      // ------------------------------------------------------------ products of slot s
+      const int s = warp == MMA_WARP ? 0 : 1;
       const uint64_t q_desc = tc::desc_at(DESC_KMAJ, smem_u32(sm + LY::Q_OFF));
       const uint64_t k_desc = tc::desc_at(DESC_KMAJ, smem_u32(sm + LY::K_OFF));
       const uint64_t v_desc = tc::desc_at(DESC_VMN, smem_u32(sm + LY::V_OFF));
       // descriptor start addresses advance by constant offsets (addresses stay below 2^18)
       constexpr uint64_t BOX = (uint64_t)SUB >> 4;
-      int k_seen = 0, v_seen = 0;               // entries waited for
       int tails[2] = {0, 0};                    // cleaned tiles of a V stage so far
-      int tiles[2] = {0, 0}, used[2] = {0, 0};  // a slot's tiles, and pieces with any, so far
+      int tiles = 0, used = 0;                  // the slot's tiles, and pieces with any, so far
       for (; ok && p.b < a.B && p.at < run.x1; p.next(a, cut), ++np) {
         const Piece pc = piece_of(cut, p, run);
-        ok = warp_wait(q_full, np);
-        tc::fence_after_sync();
-        int left = pc.c[0] + pc.c[1];           // S products to come
-        auto issue_s = [&](int s, int k) {      // S of the slot's k-th tile
-          const int e = it + pc.entry(s, k);
-          if (e >= k_seen) {
-            if (!warp_wait(&k_full[e % NK], e / NK)) { ok = false; return; }
-            k_seen = e + 1;
-            tc::fence_after_sync();
+        const int c = pc.c[s];
+        int kc = it, vc = it;                   // the next K and V entries to see: every entry is seen, in order, by both warps
+        auto pass_k = [&](int e) {              // entries before e are the other slot's alone
+          for (; kc < e && ok; ++kc) {
+            ok = warp_wait(&k_full[kc % NK], kc / NK);
+            if (ok && lane == 0) mbar_arrive(&k_free[kc % NK]);
           }
-          const uint64_t qd = q_desc + (uint64_t)(pc.halves ? 0 : s) * NSUB * BOX;
-          const uint64_t kd = k_desc + (uint64_t)(e % NK) * NSUB * BOX;
-#pragma unroll
-          for (int c = 0; c < NSUB; ++c)
-            tc::mma_ss_x4_elect(tmem + s * BN, qd + c * BOX, kd + c * BOX, IDESC_S, c > 0);
-          tc::mma_commit_elect(&s_full[s]);
-          if (pc.halves || s == 1) tc::mma_commit_elect(&k_free[e % NK]);   // both slots are through with it
-          if (--left == 0) tc::mma_commit_elect(q_free);
         };
-        for (int s = 0; s < 2 && ok; ++s)
-          if (pc.c[s] > 0) issue_s(s, 0);
-        const int most = max(pc.c[0], pc.c[1]);
-        for (int k = 0; k < most && ok; ++k) {
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (k >= pc.c[s]) continue;
-            const int e = it + pc.entry(s, k);
-            if (!warp_wait(&p_full[s], tiles[s] + k)) { ok = false; break; }
-            if (e >= v_seen) {
-              if (!warp_wait(&v_full[e % NV], e / NV)) { ok = false; break; }
-              if (e - it == pc.tail && !warp_wait(&v_clean[e % NV], tails[e % NV]++)) { ok = false; break; }
-              v_seen = e + 1;
-            }
-            // the first P V of a piece overwrites O: the one before must have been read
-            if (k == 0 && used[s] > 0 && !warp_wait(&o_free[s], used[s] - 1)) { ok = false; break; }
-            tc::fence_after_sync();
-            const uint64_t vd = v_desc + (uint64_t)(e % NV) * NSUBV * BOX;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              mma_ts_x4_elect(tmem + 256 + s * 128, tmem + s * BN + h * 32, vd + (uint64_t)h * 512, IDESC_PV, k > 0 || h > 0);
-            tc::mma_commit_elect(&pv_done[s]);
-            if (k == pc.c[s] - 1) tc::mma_commit_elect(&o_full[s]);
-            if (pc.halves || s == 1) tc::mma_commit_elect(&v_free[e % NV]);
-            if (k + 1 < pc.c[s]) issue_s(s, k + 1);
+        auto pass_v = [&](int e) {
+          for (; vc < e && ok; ++vc) {
+            ok = warp_wait(&v_full[vc % NV], vc / NV);
+            if (ok && lane == 0) mbar_arrive(&v_free[vc % NV]);
           }
+        };
+        auto issue_s = [&](int k) {             // S of the slot's k-th tile
+          const int e = it + pc.entry(s, k), st = e % NK;
+          const uint64_t qd = q_desc + (uint64_t)(pc.halves ? 0 : s) * NSUB * BOX;
+          const uint64_t kd = k_desc + (uint64_t)st * NSUB * BOX;
+#pragma unroll
+          for (int h = 0; h < NSUB; ++h)
+            tc::mma_ss_x4_elect(tmem + s * BN, qd + h * BOX, kd + h * BOX, IDESC_S, h > 0);
+          tc::mma_commit_elect(&s_full[s]);     // P V of the tile before is done then, too
+          tc::mma_commit_elect(&k_free[st]);
+          if (k == c - 1) tc::mma_commit_elect(q_free);
+          kc = e + 1;
+        };
+        auto wait_k = [&](int k) {
+          const int e = it + pc.entry(s, k);
+          pass_k(e);
+          ok = ok && warp_wait(&k_full[e % NK], e / NK);
+        };
+        ok = warp_wait(q_full, np);
+        if (c > 0) {
+          wait_k(0);
+          tc::fence_after_sync();
+          if (ok) issue_s(0);
+        } else if (ok && lane == 0) {
+          mbar_arrive(q_free);
+        }
+        for (int k = 0; k < c && ok; ++k) {
+          const int e = it + pc.entry(s, k), st = e % NV;
+          // what is not waiting for the softmax comes first (with one K stage the next K waits for the other slot's S)
+          if (NK > 1 && k + 1 < c) wait_k(k + 1);
+          pass_v(e);
+          ok = ok && warp_wait(&v_full[st], e / NV);
+          if (e - it == pc.tail) ok = ok && warp_wait(&v_clean[st], tails[st]);
+          // the first P V of a piece overwrites O: the one before must have been read
+          if (k == 0 && used > 0) ok = ok && warp_wait(&o_free[s], used - 1);
+          if (!ok) break;
+          const uint64_t vd = v_desc + (uint64_t)st * NSUBV * BOX;
+          if (!warp_wait(&p_half[s], tiles + k)) { ok = false; break; }
+          tc::fence_after_sync();
+          mma_ts_x4_elect(tmem + 256 + s * 128, tmem + s * BN, vd, IDESC_PV, k > 0);
+          if (!warp_wait(&p_full[s], tiles + k)) { ok = false; break; }
+          tc::fence_after_sync();
+          mma_ts_x4_elect(tmem + 256 + s * 128, tmem + s * BN + 32, vd + 512, IDESC_PV, 1);
+          tc::mma_commit_elect(&v_free[st]);
+          vc = e + 1;
+          if (NK == 1 && k + 1 < c) {
+            wait_k(k + 1);
+            tc::fence_after_sync();
+            if (!ok) break;
+          }
+          if (k + 1 < c) issue_s(k + 1);
+          else tc::mma_commit_elect(&o_full[s]);
         }
         it += pc.n;
-        for (int s = 0; s < 2; ++s) {
-          tiles[s] += pc.c[s];
-          used[s] += pc.c[s] > 0;
-        }
+        pass_k(it);
+        pass_v(it);
+        if (pc.tail >= 0) ++tails[(it - pc.n + pc.tail) % NV];
+        tiles += c;
+        used += c > 0;
         if (*s_abort) ok = false;
       }
       if (!ok) *s_abort = 1;
@@ -452,9 +475,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         const bool grow = !first && m_tile > m + RESCALE_LOG2;
         if (first) m = fmaxf(m, m_tile);
         if (__any_sync(FULL_MASK, grow)) {
-          // rescale those rows of O once the P V before has landed (the whole warp takes part; others by 1)
-          if (!warp_wait(&pv_done[s], kk - 1)) { ok = false; break; }
-          tc::fence_after_sync();
+          // rescale those rows of O, which holds the P V before (the whole warp takes part; others by 1)
           const float alpha = grow ? ex2(m - m_tile) : 1.0f;
 #pragma unroll
           for (int q = 0; q < DV / 16; ++q) {
@@ -486,6 +507,12 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
             for (int e = 0; e < 16; ++e) w[e] = 0u;
           }
           tmem_st16(lane_base + s_col + q * 16, w);
+          if (q == 1) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[s]);
+          }
         }
         l += f32x2_lo(lsum) + f32x2_hi(lsum);
         tc::tmem_wait_st();
