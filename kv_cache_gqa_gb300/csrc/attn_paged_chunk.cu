@@ -45,7 +45,7 @@ constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 192, REGS_CONTROL = 120;
 static_assert(2 * REGS_SOFTMAX + REGS_CONTROL <= 3 * REGS_LAUNCH, "register split exceeds the launch total");
 static_assert(REGS_LAUNCH * THREADS <= 65536, "launch registers");
 constexpr int SUB = BM * 128;              // one [128 rows x 64 bf16] swizzled box column
-constexpr int ST_BYTES = 32 * 64;          // a warp's staging tile: 32 rows x 32 bf16
+constexpr int ST_BYTES = 32 * 32;          // a warp's staging tile: 32 rows x 16 bf16
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 
@@ -60,7 +60,7 @@ struct Layout {
   static constexpr int ML_OFF = ST_OFF + SOFTMAX_WARPS * ST_BYTES;   // slot 1's (maximum, sum) of halves units
   static constexpr int BAR_OFF = ML_OFF + BM * 8;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;        // + slack to align the base to 1024
-  static_assert(SMEM <= 232448, "shared memory per CTA");
+  static_assert(SMEM + 1536 <= 232448, "shared memory per CTA, with the static part");
 };
 
 constexpr uint64_t DESC_KMAJ = tc::desc_template(16, 1024, tc::SWIZZLE_128B);
@@ -192,13 +192,31 @@ __device__ __forceinline__ void load_tile(const PagedArgs& a, const CUtensorMap*
   __syncwarp();
 }
 
-// A wait gave up: the rows of this thread from the piece `p` on become NaN.  Out of line: never in a healthy launch.
+// A warp's way through its run, in shared memory (its registers are taken): the unit and its piece.
+struct Walk {
+  Place p;
+  Piece q;
+  int more;
+};
+__device__ __forceinline__ bool enter(Walk& w, const PagedArgs& a, const CutPairs& cut, const Run& run, bool first, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    if (!first) w.p.next(a, cut);
+    w.more = w.p.b < a.B && w.p.at < run.x1;
+    if (w.more) w.q = piece_of(cut, w.p, run);
+  }
+  __syncwarp();
+  return w.more != 0;
+}
+
+// A wait gave up: the rows of this thread from the walk's piece on become NaN.  Out of line: never in a healthy launch.
 template <int DV>
-__device__ __noinline__ void nan_rows(const PagedArgs& a, const CutPairs& cut, Place p, const Run& run, int s, int t) {
-  for (; p.b < a.B && p.at < run.x1; p.next(a, cut)) {
-    const bool halves = cut.halves(p.s, p.rt);
-    if (halves && s == 1) continue;
-    if (p.at < run.x0 || p.at + p.n_steps > run.x1)                    // a part: whoever joins it finds NaN
+__device__ __noinline__ void nan_rows(Walk& w, const PagedArgs& a, const CutPairs& cut, const Run& run, int s, int t) {
+  bool more = w.more != 0;
+  for (; more; more = enter(w, a, cut, run, false, t & 31)) {
+    const Place& p = w.p;
+    if (w.q.halves && s == 1) continue;
+    if (!w.q.whole)                                                    // a part: whoever joins it finds NaN
       reinterpret_cast<float2*>(a.part_ml)[((int64_t)(blockIdx.x * 2 + (run.x0 >= p.at ? 0 : 1)) * 2 + s) * BM + t] =
           make_float2(M_NONE, NAN);
     const int token = (2 * p.rt + s) * cut.tpt + t / cut.G;
@@ -234,9 +252,12 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   uint64_t* v_clean = bars + 20;   // [NV] the tile that holds L has its V cleaned
   uint64_t* ml_full = bars + 22;   // slot 1's maxima and sums of a halves piece published (4 warps)
   uint64_t* ml_free = bars + 23;   // and read by slot 0 (4 warps)
-  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 24);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 25);
+  uint64_t* turn = bars + 24;      // [slot] the slot's products of a round have been issued
+  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 26);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 27);
   __shared__ int64_t scratch[THREADS / 32 + 4];
+  __shared__ Run run;
+  __shared__ Walk walks[THREADS / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
@@ -247,6 +268,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       mbar_init(&k_full[i], 1); mbar_init(&k_free[i], 2); mbar_init(&v_full[i], 1); mbar_init(&v_free[i], 2);
       mbar_init(&s_full[i], 1); mbar_init(&p_half[i], SOFTMAX_WARPS / 2); mbar_init(&p_full[i], SOFTMAX_WARPS / 2);
       mbar_init(&o_full[i], 1); mbar_init(&o_free[i], SOFTMAX_WARPS / 2); mbar_init(&v_clean[i], 1);
+      mbar_init(&turn[i], 1);
     }
     mbar_init(q_full, 1); mbar_init(q_free, 2);
     mbar_init(ml_full, SOFTMAX_WARPS / 2); mbar_init(ml_free, SOFTMAX_WARPS / 2);
@@ -260,10 +282,19 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   const uint32_t tmem = *s_taddr;
   griddep_wait();                               // inputs of this launch are complete from here on
   griddep_launch_dependents();
-  Place p;
-  const Run run = paged::first_place<THREADS>(a, cut, scratch, &p);
-  if (tid == 0) a.joins[blockIdx.x].last = -1;
+  Walk& walk = walks[warp];
+  {
+    Place first;
+    const Run mine = paged::first_place<THREADS>(a, cut, scratch, &first);
+    if (lane == 0) walk.p = first;
+    if (tid == 0) {
+      run = mine;
+      a.joins[blockIdx.x].last = -1;
+    }
+  }
   __syncthreads();
+  const Place& p = walk.p;
+  const Piece& pc = walk.q;
 
   if (warp >= SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS_CONTROL));
@@ -272,8 +303,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     int np = 0;                                 // pieces so far
     if (warp == K_WARP) {
       // ------------------------------------------------------------ Q and K copies
-      for (; ok && p.b < a.B && p.at < run.x1; p.next(a, cut)) {
-        const Piece pc = piece_of(cut, p, run);
+      for (bool first = true; ok && enter(walk, a, cut, run, first, lane); first = false) {
         if (np > 0 && !warp_wait(q_free, np - 1)) { ok = false; break; }
         if (lane == 0) {
           const int slots = pc.halves ? 1 : 2;
@@ -300,8 +330,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       if (np > 0 && !ok) (void)warp_wait(q_full, np - 1);
     } else if (warp == V_WARP) {
       // ------------------------------------------------------------ V copies
-      for (; ok && p.b < a.B && p.at < run.x1; p.next(a, cut)) {
-        const Piece pc = piece_of(cut, p, run);
+      for (bool first = true; ok && enter(walk, a, cut, run, first, lane); first = false) {
         Pages pg{a.table + (int64_t)p.b * a.table_stride, pages_of(a, p.s.L), -64, 0};
         for (int i = 0; i < pc.n; ++i, ++it) {
           const int st = it % NV;
@@ -334,8 +363,8 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       constexpr uint64_t BOX = (uint64_t)SUB >> 4;
       int tails[2] = {0, 0};                    // cleaned tiles of a V stage so far
       int tiles = 0, used = 0;                  // the slot's tiles, and pieces with any, so far
-      for (; ok && p.b < a.B && p.at < run.x1; p.next(a, cut), ++np) {
-        const Piece pc = piece_of(cut, p, run);
+      int rounds = 0;                           // turns taken so far
+      for (bool first = true; ok && enter(walk, a, cut, run, first, lane); first = false, ++np) {
         const int c = pc.c[s];
         int kc = it, vc = it;                   // the next K and V entries to see: every entry is seen, in order, by both warps
         auto pass_k = [&](int e) {              // entries before e are the other slot's alone
@@ -367,15 +396,31 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           pass_k(e);
           ok = ok && warp_wait(&k_full[e % NK], e / NK);
         };
+        // The slots take turns, slot 0 first: the tensor core runs one slot's products whole while the other's softmax runs.  Without,
+        // both slots' products went through it interleaved and ended together, and both softmaxes then had it idle.
+        auto my_turn = [&]() { return s == 1 ? warp_wait(&turn[0], rounds) : (rounds == 0 || warp_wait(&turn[1], rounds - 1)); };
+        auto pass_turn = [&]() {
+          if (lane == 0) mbar_arrive(&turn[s]);
+          ++rounds;
+        };
         ok = warp_wait(q_full, np);
         if (c > 0) {
           wait_k(0);
           tc::fence_after_sync();
+          ok = ok && my_turn();
           if (ok) issue_s(0);
-        } else if (ok && lane == 0) {
-          mbar_arrive(q_free);
+        } else {
+          ok = ok && my_turn();
+          if (ok && lane == 0) mbar_arrive(q_free);
         }
-        for (int k = 0; k < c && ok; ++k) {
+        pass_turn();
+        const int both = max(pc.c[0], pc.c[1]);
+        for (int k = 0; k < both && ok; ++k) {
+          if (k >= c) {
+            ok = my_turn();
+            pass_turn();
+            continue;
+          }
           const int e = it + pc.entry(s, k), st = e % NV;
           // what is not waiting for the softmax comes first (with one K stage the next K waits for the other slot's S)
           if (NK > 1 && k + 1 < c) wait_k(k + 1);
@@ -387,6 +432,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           if (!ok) break;
           const uint64_t vd = v_desc + (uint64_t)st * NSUBV * BOX;
           if (!warp_wait(&p_half[s], tiles + k)) { ok = false; break; }
+          if (!my_turn()) { ok = false; break; }
           tc::fence_after_sync();
           mma_ts_x4_elect(tmem + 256 + s * 128, tmem + s * BN, vd, IDESC_PV, k > 0);
           if (!warp_wait(&p_full[s], tiles + k)) { ok = false; break; }
@@ -401,6 +447,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           }
           if (k + 1 < c) issue_s(k + 1);
           else tc::mma_commit_elect(&o_full[s]);
+          pass_turn();
         }
         it += pc.n;
         pass_k(it);
@@ -423,8 +470,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     const bool in_tile = t < cut.tpt * G;
     bool ok = true;
     int tiles = 0, used = 0, shared = 0;        // this slot's tiles, pieces with any, halves pieces so far
-    for (; ok && p.b < a.B && p.at < run.x1; p.next(a, cut)) {
-      const Piece pc = piece_of(cut, p, run);
+    for (bool begin = true; ok && enter(walk, a, cut, run, begin, lane); begin = false) {
       const int rt = pc.halves ? 2 * p.rt : 2 * p.rt + s;
       const int token = rt * cut.tpt + t / G;
       const bool row_ok = in_tile && token < p.s.T;
@@ -573,34 +619,34 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           }
         }
         if (pc.whole) {
-          // O / l in 32-column chunks, transposed through the staging tile so that a store instruction writes 8 rows x 64
-          // contiguous bytes (piece k of row r at position k ^ ((r >> 1) & 3): no bank conflicts)
+          // O / l in 16-column chunks, transposed through the staging tile so that a store instruction writes whole sectors of
+          // 16 rows (piece k of row r at position k ^ ((r >> 2) & 1): no bank conflicts)
           const float inv = l == 0.f ? 0.f : 1.0f / l;
           const int my_row = row_ok ? (p.s.t0 + token) * a.Hq + p.g * G + t % G : -1;
-          uint16_t* orow[4];
+          uint16_t* orow[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = __shfl_sync(FULL_MASK, my_row, (lane >> 2) + 8 * i);
-            orow[i] = rr < 0 ? nullptr : reinterpret_cast<uint16_t*>(a.out) + (int64_t)rr * DV + (lane & 3) * 8;
+          for (int i = 0; i < 2; ++i) {
+            const int rr = __shfl_sync(FULL_MASK, my_row, (lane >> 1) + 16 * i);
+            orow[i] = rr < 0 ? nullptr : reinterpret_cast<uint16_t*>(a.out) + (int64_t)rr * DV + (lane & 1) * 8;
           }
 #pragma unroll
-          for (int q = 0; q < DV / 32; ++q) {
+          for (int q = 0; q < DV / 16; ++q) {
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
+            for (int k2 = 0; k2 < 2; ++k2) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float y0 = x[32 * q + 8 * k4 + 2 * e], y1 = x[32 * q + 8 * k4 + 2 * e + 1];
+                const float y0 = x[16 * q + 8 * k2 + 2 * e], y1 = x[16 * q + 8 * k2 + 2 * e + 1];
                 w[e] = l == 0.f ? 0u : pack_bf16x2(y0 * inv, y1 * inv);
               }
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((k4 ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 32 + ((k2 ^ ((lane >> 2) & 1)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = (lane >> 2) + 8 * i, k4 = lane & 3;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((k4 ^ ((rr >> 1) & 3)) << 4));
-              if (orow[i] != nullptr) *reinterpret_cast<uint4*>(orow[i] + 32 * q) = v;
+            for (int i = 0; i < 2; ++i) {
+              const int rr = (lane >> 1) + 16 * i, k2 = lane & 1;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((k2 ^ ((rr >> 2) & 1)) << 4));
+              if (orow[i] != nullptr) *reinterpret_cast<uint4*>(orow[i] + 16 * q) = v;
             }
             __syncwarp();
           }
@@ -624,11 +670,11 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       tiles += c;
       used += c > 0;
       shared += pc.halves;
-      if (*s_abort) { ok = false; p.next(a, cut); break; }
+      if (*s_abort) { ok = false; break; }      // (a piece that is through is written again: NaN)
     }
     if (!ok) {
       *s_abort = 1;
-      if (p.b < a.B) nan_rows<DV>(a, cut, p, run, s, t);
+      nan_rows<DV>(walk, a, cut, run, s, t);
     }
   }
   tc::fence_before_sync();
