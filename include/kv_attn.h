@@ -504,7 +504,8 @@ size_t kva_decode_q4_workspace_zero_bytes(int32_t B, int32_t n_kv_heads, int32_t
  *                lengths grow); token_start_host holds the values (which sequences are short and which long is planned from it).
  *   table_host   host mirror of the table or NULL; given, pages that lengths_host needs are checked
  *                against the pool.  Without it a page id outside the pool costs its sequence: the append
- *                drops its rows, the attention gives NaN for the tokens that see them. */
+ *                drops its rows, the attention gives NaN for the tokens that see it (and may for the sequence's other
+ *                new tokens). */
 #define KVA_PAGE_MIN 16
 #define KVA_PAGE_MAX 256
 typedef struct {

@@ -165,13 +165,22 @@ struct Pages {
   const int32_t* row;                       // the sequence's page table
   int last, base;                           // pages below `last` hold slots below L; the 32 ids from page `base` on
   int id;
+  bool bad;                                 // an id of them is outside the pool
   __device__ __forceinline__ void load(const PagedArgs& a, int from, int lane) {
     base = from;
     id = a.n_pages;                         // beyond L, or outside the pool: copies read zeros
+    bad = false;
     if (from + lane < last) {
       const int x = row[from + lane];
-      if ((unsigned)x < (unsigned)a.n_pages) id = x;
+      bad = (unsigned)x >= (unsigned)a.n_pages;
+      if (!bad) id = x;
     }
+    bad = __any_sync(FULL_MASK, bad);
+  }
+  // the ids of key tile j's pages
+  __device__ __forceinline__ void need(const PagedArgs& a, int j, int lane) {
+    const int n = a.page_shift < 7 ? 128 >> a.page_shift : 1, page = (j * BN) >> a.page_shift;
+    if (page + n > base + 32) load(a, page, lane);
   }
 };
 // Copies key tile j of KV head g into `dst` ([NS columns][128 rows x 128 bytes]).  Whole warp.
@@ -179,7 +188,7 @@ template <int NS>
 __device__ __forceinline__ void load_tile(const PagedArgs& a, const CUtensorMap* map, Pages& pg, int j, int g, uint8_t* dst,
                                           uint64_t* bar, int lane) {
   const int shift = a.page_shift, n = shift < 7 ? 128 >> shift : 1, page = (j * BN) >> shift;   // pages of a tile, the first one
-  if (page + n > pg.base + 32) pg.load(a, page, lane);
+  pg.need(a, j, lane);
   if (lane == 0) mbar_arrive_expect_tx(bar, NS * SUB);
   __syncwarp();
   const int id = __shfl_sync(FULL_MASK, pg.id, (page - pg.base + (lane & (n - 1))) & 31);
@@ -255,6 +264,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   uint64_t* turn = bars + 24;      // [slot] the slot's products of a round have been issued
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 27);
+  volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(bars + 28);   // pieces (modulo 32) with a page id outside the pool
   __shared__ int64_t scratch[THREADS / 32 + 4];
   __shared__ Run run;
   __shared__ Walk walks[THREADS / 32];
@@ -273,6 +283,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     mbar_init(q_full, 1); mbar_init(q_free, 2);
     mbar_init(ml_full, SOFTMAX_WARPS / 2); mbar_init(ml_free, SOFTMAX_WARPS / 2);
     *s_abort = 0;
+    *s_bad = 0u;
     fence_mbar_init();
   }
   if (warp == K_WARP && lane == 0) { tc::tma_prefetch_desc(&tmK); tc::tma_prefetch_desc(&tmV); tc::tma_prefetch_desc(&tmQ); }
@@ -316,10 +327,15 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         }
         ++np;
         __syncwarp();
-        Pages pg{a.table + (int64_t)p.b * a.table_stride, pages_of(a, p.s.L), -64, 0};
+        bool bad = false;
+        Pages pg{a.table + (int64_t)p.b * a.table_stride, pages_of(a, p.s.L), -64, 0, false};
         for (int i = 0; i < pc.n; ++i, ++it) {
           const int st = it % NK;
           if (it >= NK && !warp_wait(&k_free[st], it / NK - 1)) { ok = false; break; }
+          pg.need(a, pc.j0 + i, lane);
+          bad |= pg.bad;
+          if (lane == 0 && i == pc.n - 1)       // before its last tile; this warp is at most a few pieces ahead of the softmax
+            *s_bad = (*s_bad & ~(1u << ((np + 15) & 31))) | ((bad ? 1u : 0u) << ((np - 1) & 31));
           load_tile<NSUB>(a, &tmK, pg, pc.j0 + i, p.g, sm + LY::K_OFF + st * NSUB * SUB, &k_full[st], lane);
         }
         if (*s_abort) ok = false;
@@ -331,7 +347,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     } else if (warp == V_WARP) {
       // ------------------------------------------------------------ V copies
       for (bool first = true; ok && enter(walk, a, cut, run, first, lane); first = false) {
-        Pages pg{a.table + (int64_t)p.b * a.table_stride, pages_of(a, p.s.L), -64, 0};
+        Pages pg{a.table + (int64_t)p.b * a.table_stride, pages_of(a, p.s.L), -64, 0, false};
         for (int i = 0; i < pc.n; ++i, ++it) {
           const int st = it % NV;
           if (it >= NV && !warp_wait(&v_free[st], it / NV - 1)) { ok = false; break; }
@@ -379,6 +395,11 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
             if (ok && lane == 0) mbar_arrive(&v_free[vc % NV]);
           }
         };
+        auto my_turn = [&]() { return s == 1 ? warp_wait(&turn[0], rounds) : (rounds == 0 || warp_wait(&turn[1], rounds - 1)); };
+        auto pass_turn = [&]() {
+          if (lane == 0) mbar_arrive(&turn[s]);
+          ++rounds;
+        };
         auto issue_s = [&](int k) {             // S of the slot's k-th tile
           const int e = it + pc.entry(s, k), st = e % NK;
           const uint64_t qd = q_desc + (uint64_t)(pc.halves ? 0 : s) * NSUB * BOX;
@@ -386,6 +407,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
 #pragma unroll
           for (int h = 0; h < NSUB; ++h)
             tc::mma_ss_x4_elect(tmem + s * BN, qd + h * BOX, kd + h * BOX, IDESC_S, h > 0);
+          pass_turn();
           tc::mma_commit_elect(&s_full[s]);     // P V of the tile before is done then, too
           tc::mma_commit_elect(&k_free[st]);
           if (k == c - 1) tc::mma_commit_elect(q_free);
@@ -398,11 +420,6 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         };
         // The slots take turns, slot 0 first: the tensor core runs one slot's products whole while the other's softmax runs.  Without,
         // both slots' products went through it interleaved and ended together, and both softmaxes then had it idle.
-        auto my_turn = [&]() { return s == 1 ? warp_wait(&turn[0], rounds) : (rounds == 0 || warp_wait(&turn[1], rounds - 1)); };
-        auto pass_turn = [&]() {
-          if (lane == 0) mbar_arrive(&turn[s]);
-          ++rounds;
-        };
         ok = warp_wait(q_full, np);
         if (c > 0) {
           wait_k(0);
@@ -412,8 +429,8 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         } else {
           ok = ok && my_turn();
           if (ok && lane == 0) mbar_arrive(q_free);
+          pass_turn();
         }
-        pass_turn();
         const int both = max(pc.c[0], pc.c[1]);
         for (int k = 0; k < both && ok; ++k) {
           if (k >= c) {
@@ -445,9 +462,12 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
             tc::fence_after_sync();
             if (!ok) break;
           }
-          if (k + 1 < c) issue_s(k + 1);
-          else tc::mma_commit_elect(&o_full[s]);
-          pass_turn();
+          if (k + 1 < c) {
+            issue_s(k + 1);
+          } else {
+            pass_turn();
+            tc::mma_commit_elect(&o_full[s]);
+          }
         }
         it += pc.n;
         pass_k(it);
@@ -470,20 +490,12 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     const bool in_tile = t < cut.tpt * G;
     bool ok = true;
     int tiles = 0, used = 0, shared = 0;        // this slot's tiles, pieces with any, halves pieces so far
+    int pieces = 0;
     for (bool begin = true; ok && enter(walk, a, cut, run, begin, lane); begin = false) {
       const int rt = pc.halves ? 2 * p.rt : 2 * p.rt + s;
       const int token = rt * cut.tpt + t / G;
       const bool row_ok = in_tile && token < p.s.T;
       const int lim = row_ok ? min(max(p.s.L - p.s.T + token + 1, 0), p.s.L) : 0;   // slots that the row sees
-      // page ids outside the pool among the tiles that this slot sees: no result
-      bool bad = false;
-      {
-        const int first = (pc.j0 * BN) >> a.page_shift;
-        const int end = min(cut.visible(p.s, pc.halves ? 2 * p.rt : 2 * p.rt + s), (pc.j0 + pc.n) * BN);
-        const int last = pages_of(a, end);
-        for (int i = first + lane; i < last; i += 32)
-          bad |= (unsigned)a.table[(int64_t)p.b * a.table_stride + i] >= (unsigned)a.n_pages;
-      }
       const int c = pc.c[s];
       float m = M_NONE, l = 0.f;
       float x[128];
@@ -567,7 +579,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         if (lane == 0) mbar_arrive(&p_full[s]);
       }
       if (!ok) break;
-      if (__any_sync(FULL_MASK, bad)) l = NAN;
+      if ((*s_bad >> (pieces & 31)) & 1u) l = NAN;                      // a page id outside the pool: no result
       if (c > 0 && !warp_wait(&o_full[s], used)) { ok = false; break; }
       tc::fence_after_sync();
       if (pc.halves && s == 1) {
@@ -670,6 +682,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       tiles += c;
       used += c > 0;
       shared += pc.halves;
+      ++pieces;
       if (*s_abort) { ok = false; break; }      // (a piece that is through is written again: NaN)
     }
     if (!ok) {
