@@ -152,10 +152,8 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Every lane waits; the vote keeps the warp converged for what follows.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, int count) {
-  return __all_sync(FULL_MASK, mbar_wait_bounded(bar, (uint32_t)(count & 1)));
-}
+// Phase `count` of a barrier, by all lanes; the vote keeps the warp converged for what follows.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int count) { return paged::warp_wait(bar, (uint32_t)(count & 1)); }
 
 // Pages that hold n slots.
 __device__ __forceinline__ int pages_of(const PagedArgs& a, int n) { return (n + (1 << a.page_shift) - 1) >> a.page_shift; }

@@ -153,11 +153,11 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
     for (int h = 0; h < H; ++h) { m[h] = M_NONE; l[h] = 0.f; }
 
     for (int u = 0; u < n_mine; ++u) {
-      if (!__all_sync(FULL_MASK, mbar_wait_bounded(&bar[slot], phase))) {
+      if (!paged::warp_wait(&bar[slot], phase)) {
         ok = false;                             // gave up: the copies still in flight land first (bounded)
         for (int v = u + 1; v < n_mine && v < u + NS; ++v) {
           if (++slot == NS) { slot = 0; phase ^= 1; }
-          (void)mbar_wait_bounded(&bar[slot], phase);
+          (void)paged::warp_wait(&bar[slot], phase);
         }
         break;
       }

@@ -17,6 +17,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A whole warp waits for the phase of this parity, up to WAIT_LIMIT_NS; false if it gave up.  With a hint the hardware suspends
+// the warp for up to so many nanoseconds and wakes it when the phase ends.  Without, it looks again every few hundred cycles,
+// and the issue slots that takes were the softmax warps' (a 2048-token chunk behind 30000 slots: 821 us, with the hint 657).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  constexpr uint32_t HINT_NS = 1000000;
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(HINT_NS) : "memory");
+    if (__all_sync(FULL_MASK, ok != 0)) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(FULL_MASK, now - t0 > WAIT_LIMIT_NS)) {
+      atomicAdd(&g_wait_timeouts, 1u);
+      return false;
+    }
+  }
+}
+
 // New tokens [t0, t0 + T) of sequence b and its L slots, forced into the buffers' bounds: a device copy that
 // disagrees with its host mirror gives other results, but no access outside.
 struct Seq {
