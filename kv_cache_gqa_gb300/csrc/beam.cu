@@ -1,16 +1,17 @@
 // Beam search's selection over beams and vocabulary (beam_select).
 //
-// A CTA takes a slice of one beam's logits.  A lane keeps its own running maximum and sum of exponentials; a warp
-// keeps the best n of its logits as sorted 64-bit keys, a lane each (value, then lower id first), against whose
-// last one a batch of 16 values a lane is checked by its maximum alone.  A batch with many better values (the first
-// one) is sorted in lane maxima at a time, one with few inserts them one by one.  The CTA joins its warps' lists and
-// sums and writes them; the last CTA of a group joins the slices: a warp per beam, then the best n of the beams'
-// sorted lists, a lane per beam, by totals in 64 bits (beams that are nearly even keep their order).
+// A CTA takes a slice of one beam's logits in batches of 16 values a thread, the next batch on its way.  A thread keeps its own
+// maximum, its sum of exponentials, the best of its batch maxima and the second best.  At the slice's end a warp sorts its threads'
+// maxima; the n-th of them, the largest over the warps, is a bound that at least n values of the slice reach and few others do.  The
+// threads that reach it read the one batch again that holds their maximum (all of theirs where the second best reaches it, too), and
+// the values at or above the bound are sorted: about n to 3 n of them.  Where they do not fit a list of 1024 (rows of equal or
+// sorted values), warps keep sorted lists over the whole slice instead.  The last CTA of a group joins the slices: a warp per
+// beam, then the best n of the beams' sorted lists, a lane per beam, by totals in 64 bits (beams that are nearly even keep their order).
 // A beam that is done, or whose score is -infinity, is not read.
 //
-// Sums are float32 per lane and slice, 64 bits where they are joined.  Which lane takes an element depends on its index
-// alone, so equal rows give equal totals.  x - m is exact or nearly so where its exponential counts, which
-// x * log2 e - m * log2 e is not.
+// Sums are float32 per thread and slice, 64 bits where they are joined.  Which thread takes an element depends on its index
+// alone, so equal rows give equal totals.  exp(x - m) is 2^(x log2 e - c), c = m log2 e rounded, with log2 e in two parts, and the sum is
+// put right for c's rounding at the end.
 //
 // The runtime's own options (HunyuanOCR v1.5 ncnn port, section 3.6) stop at top_k; it has no beams.
 #include <algorithm>
@@ -31,6 +32,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 using Key = unsigned long long;
@@ -68,29 +75,78 @@ __device__ __forceinline__ Key insert(Key list, Key k, int lane) {      // k: th
   return lane < at ? list : (lane == at ? k : up);
 }
 
-// 16 values from index i on of a row of V values (-infinity past its end).
+// 16 values of a row as they lie in memory, and as floats (-infinity past its end).
+template <typename T> struct Batch {
+  uint4 r[sizeof(T) * PER / 16];
+  float edge[PER];                               // a batch at the row's end, or of a row that is not aligned
+  bool whole;
+  __device__ __forceinline__ void load(const T* row, int i, int V, bool aligned) {
+    whole = aligned && i + PER <= V;
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < (int)sizeof(T) * PER / 16; ++e) r[e] = __ldg(reinterpret_cast<const uint4*>(row + i) + e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) edge[e] = i + e < V ? load1(row + i + e) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[PER]) const {
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < (int)sizeof(T) * PER / 16; ++e) {
+        const uint32_t w[4] = {r[e].x, r[e].y, r[e].z, r[e].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(T) == 2) { x[8 * e + 2 * k] = bf16_lo(w[k]); x[8 * e + 2 * k + 1] = bf16_hi(w[k]); }
+          else x[4 * e + k] = __uint_as_float(w[k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) x[e] = edge[e];
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void load_values(const T* row, int i, int V, bool aligned, float (&x)[PER]) {
-  if (aligned && i + PER <= V) {
+  Batch<T> b;
+  b.load(row, i, V, aligned);
+  b.values(x);
+}
+
+// The best keys among a warp's values x of ids first + lane * PER + e into its list; last: the list's n-th (0: not full).
+__device__ __forceinline__ void warp_best(const float (&x)[PER], int i0, int n, int lane, Key& list, Key& last) {
+  Key left = ~0ull;                              // keys below this one are not taken yet
+  for (;;) {
+    Key k = 0;
 #pragma unroll
-    for (int e = 0; e < PER; e += 8) {
-      float y[8];
-      load8(row + i + e, y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[e + j] = y[j];
+    for (int e = 0; e < PER; ++e) {
+      const Key c = key_of(x[e], i0 + e);
+      if (x[e] > -INFINITY && c > last && c < left && c > k) k = c;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < PER; ++e) x[e] = i + e < V ? load1(row + i + e) : -INFINITY;
+    const unsigned more = __ballot_sync(FULL_MASK, k != 0);
+    if (more == 0) return;
+    left = k != 0 ? k : left;
+    if (__popc(more) > 4) {
+      list = join(list, sort_down(k, lane), lane);
+    } else {
+      for (unsigned b = more; b; b &= b - 1) list = insert(list, __shfl_sync(FULL_MASK, k, __ffs(b) - 1), lane);
+    }
+    last = __shfl_sync(FULL_MASK, list, n - 1);
   }
 }
+
+constexpr int LIST = 1024;                       // candidates of a slice that are sorted at once
+constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;       // log2 e = HI + LO
+constexpr float HUGE_M = 1e30f;                  // beyond it m log2 e could overflow
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
 beam_select_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ Key s_cand[LIST];
   __shared__ Key s_list[WARPS][32];
-  __shared__ float s_m[WARPS], s_s[WARPS];
-  __shared__ int s_last;
+  __shared__ float s_m[WARPS], s_s[WARPS], s_bound[WARPS];
+  __shared__ int s_count, s_last;
   __shared__ double s_base[BEAM_MAX], s_top[BEAM_MAX];   // score - log sum of a beam (NaN: it offers nothing), its maximum
   __shared__ Key s_best[BEAM_MAX][33];
   const int row = blockIdx.y, split = blockIdx.x, b = row / a.K;
@@ -104,75 +160,104 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     const bool aligned = (reinterpret_cast<uintptr_t>(z) & 15u) == 0;
     const int batches = (a.V + BATCH - 1) / BATCH;
     const int b0 = (int)((int64_t)batches * split / gridDim.x), b1 = (int)((int64_t)batches * (split + 1) / gridDim.x);
-    float m = LOW, s = 0.f;
-    Key list = 0, last = 0;                        // last: the list's n-th (0: not full)
-    float thr = -INFINITY;                         // its value
-    auto renew = [&]() {
-      last = __shfl_sync(FULL_MASK, list, n - 1);
-      thr = last ? key_value(last) : -INFINITY;
-    };
+    if (tid == 0) s_count = 0;
+    float m = LOW, c = 0.f, s = 0.f;               // s: sum of 2^(x log2 e - c), or of exp(x - m) where |m| >= HUGE_M
+    float best = -INFINITY, second = -INFINITY;    // of the batches' maxima
+    int best_at = b0;
+    Batch<T> next;
+    if (b0 < b1) next.load(z, b0 * BATCH + tid * PER, a.V, aligned);
     for (int bt = b0; bt < b1; ++bt) {
       float x[PER];
-      const int i0 = bt * BATCH + tid * PER;
-      load_values(z, i0, a.V, aligned, x);
-      float top = x[0];
+      next.values(x);
+      if (bt + 1 < b1) next.load(z, (bt + 1) * BATCH + tid * PER, a.V, aligned);
+      float top = fmaxf(x[0], x[1]);
 #pragma unroll
-      for (int e = 1; e < PER; ++e) top = fmaxf(top, x[e]);
-      if (top > m) { s *= ex2((m - top) * LOG2E); m = top; }
+      for (int e = 2; e < PER; e += 2) top = fmax3(top, x[e], x[e + 1]);
+      if (top > best) { second = best; best = top; best_at = bt; }
+      else second = fmaxf(second, top);
+      if (top > m) {
+        const float to = top * L2E_HI;
+        s *= ex2(fabsf(m) < HUGE_M && fabsf(top) < HUGE_M ? c - to : (m - top) * L2E_HI);
+        m = top;
+        c = to;
+      }
+      if (fabsf(m) < HUGE_M) {
+        const uint64_t hi2 = pack_f32x2(L2E_HI, L2E_HI), lo2 = pack_f32x2(L2E_LO, L2E_LO), c2 = pack_f32x2(-c, -c);
+        uint64_t sum = 0ull;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) s += ex2((x[e] - m) * LOG2E);
-      // a warp's ids grow from batch to batch: a later value equal to the n-th is not better
-      unsigned better = __ballot_sync(FULL_MASK, top > thr);
-      if (better == 0) continue;
-      if (__popc(better) > 4) {
-        // lane maxima, sorted, until none of what is left is better than the list's n-th
-        Key left = ~0ull;                          // keys below this one are not taken yet
-        for (;;) {
-          Key k = 0;
-#pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            const Key c = key_of(x[e], i0 + e);
-            if (x[e] >= thr && x[e] > -INFINITY && c > last && c < left && c > k) k = c;
-          }
-          if (__ballot_sync(FULL_MASK, k != 0) == 0) break;
-          left = k != 0 ? k : left;
-          list = join(list, sort_down(k, lane), lane);
-          renew();
+        for (int e = 0; e < PER; e += 2) {
+          const uint64_t x2 = pack_f32x2(x[e], x[e + 1]), t = fma_f32x2(x2, lo2, fma_f32x2(x2, hi2, c2));
+          sum = add_f32x2(sum, pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t))));
         }
+        s += f32x2_lo(sum) + f32x2_hi(sum);
       } else {
-        for (; better; better &= better - 1) {
-          const int src = __ffs(better) - 1;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            const float v = __shfl_sync(FULL_MASK, x[e], src);
-            const Key k = key_of(v, bt * BATCH + (tid - lane + src) * PER + e);
-            if (v >= thr && k > last && v > -INFINITY) {
-              list = insert(list, k, lane);
-              renew();
-            }
+        for (int e = 0; e < PER; ++e) s += ex2((x[e] - m) * L2E_HI);
+      }
+    }
+    if (fabsf(m) < HUGE_M) s *= ex2(fmaf(-m, L2E_LO, fmaf(-m, L2E_HI, c)));    // now of exp(x - m)
+    // the warp's sums, and its n-th best maximum of a thread
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
+    s *= ex2((m - M) * L2E_HI);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
+    float ordered = best;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+      for (int o = size >> 1; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(FULL_MASK, ordered, o);
+        ordered = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(ordered, other) : fminf(ordered, other);
+      }
+    ordered = __shfl_sync(FULL_MASK, ordered, n - 1);
+    if (lane == 0) { s_m[warp] = M; s_s[warp] = s; s_bound[warp] = ordered; }
+    __syncthreads();
+    float bound = s_bound[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) bound = fmaxf(bound, s_bound[w]);
+    // the values that reach it
+    if (best >= bound && best > -INFINITY) {
+      const bool all = second >= bound && second > -INFINITY;
+      for (int bt = all ? b0 : best_at; bt < (all ? b1 : best_at + 1); ++bt) {
+        const int i0 = bt * BATCH + tid * PER;
+        for (int e = 0; e < PER && i0 + e < a.V; ++e) {
+          const float v = load1(z + i0 + e);
+          if (v >= bound && v > -INFINITY) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < LIST) s_cand[at] = key_of(v, i0 + e);
           }
         }
       }
     }
-    // the warp's sums, then the CTA's
-    float M = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-    s *= ex2((m - M) * LOG2E);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
-    if (lane == 0) { s_m[warp] = M; s_s[warp] = s; }
+    __syncthreads();
+    const int count = s_count;
+    Key list = 0, last = 0;
+    if (count <= LIST) {
+      for (int i = warp * 32; i < count; i += THREADS) {
+        const Key k = i + lane < count ? s_cand[i + lane] : 0;
+        list = join(list, sort_down(k, lane), lane);
+      }
+    } else {
+      for (int bt = b0; bt < b1; ++bt) {
+        float x[PER];
+        load_values(z, bt * BATCH + tid * PER, a.V, aligned, x);
+        warp_best(x, bt * BATCH + tid * PER, n, lane, list, last);
+      }
+    }
     s_list[warp][lane] = lane < n ? list : 0;
     __syncthreads();
     if (warp == 0) {
+      const int lists = count <= LIST ? min(WARPS, (count + 31) / 32) : WARPS;
       Key k = s_list[0][lane];
-      for (int w = 1; w < WARPS; ++w) k = join(k, s_list[w][lane], lane);
+      for (int w = 1; w < lists; ++w) k = join(k, s_list[w][lane], lane);
       const int64_t part = (int64_t)row * gridDim.x + split;
       if (lane < n) a.part_key[part * n + lane] = k;
       if (lane == 0) {
         float CM = LOW, S = 0.f;
         for (int w = 0; w < WARPS; ++w) CM = fmaxf(CM, s_m[w]);
-        for (int w = 0; w < WARPS; ++w) S = fmaf(s_s[w], ex2((s_m[w] - CM) * LOG2E), S);
+        for (int w = 0; w < WARPS; ++w) S = fmaf(s_s[w], ex2((s_m[w] - CM) * L2E_HI), S);
         a.part_stat[2 * part] = CM;
         a.part_stat[2 * part + 1] = S;
       }
@@ -189,13 +274,24 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     const int r = b * a.K + k;
     const float sc = a.scores[r];
     const bool is_done = a.finished != nullptr && a.finished[r] != 0;
-    Key list = 0;
+    Key list = 0, last = 0;
     double base = NAN, top = 0.0;
     if (is_done) {
       base = (double)sc;
       if (lane == 0) list = key_of(0.f, a.end_id);
     } else if (sc > -INFINITY) {
       const int64_t part = (int64_t)r * gridDim.x;
+      const int keys = (int)gridDim.x * n;
+      constexpr int KPL = 8;                         // keys of a lane at a time
+      Key ahead[KPL];
+      auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < KPL; ++u) {
+          const int i = i0 + u * 32 + lane;
+          ahead[u] = i < keys ? __ldcg(a.part_key + part * n + i) : 0;
+        }
+      };
+      fetch(0);
       float M = LOW;
       for (int i = lane; i < (int)gridDim.x; i += 32) M = fmaxf(M, __ldcg(a.part_stat + 2 * (part + i)));
 #pragma unroll
@@ -211,22 +307,24 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       if (good) {
         base = (double)sc - log(S);
         top = (double)M;
-        Key thr = 0;
-        for (int j = 0; j < n; ++j) {              // all slices' best, then their second best, ...
-          bool any = false;
-          for (int i0 = 0; i0 < (int)gridDim.x; i0 += 32) {
-            Key c = i0 + lane < (int)gridDim.x ? __ldcg(a.part_key + (part + i0 + lane) * n + j) : 0;
-            if (c <= thr) c = 0;
-            unsigned better = __ballot_sync(FULL_MASK, c != 0);
-            any |= better != 0;
-            if (__popc(better) > 4) {
-              list = join(list, sort_down(c, lane), lane);
+        for (int i0 = 0; i0 < keys; i0 += 32 * KPL) {
+          if (i0 > 0) fetch(i0);
+          Key left = ~0ull;                          // keys below this one are not taken yet
+          for (;;) {
+            Key best = 0;
+#pragma unroll
+            for (int u = 0; u < KPL; ++u)
+              if (ahead[u] > last && ahead[u] < left && ahead[u] > best) best = ahead[u];
+            const unsigned more = __ballot_sync(FULL_MASK, best != 0);
+            if (more == 0) break;
+            left = best != 0 ? best : left;
+            if (__popc(more) > 4) {
+              list = join(list, sort_down(best, lane), lane);
             } else {
-              for (; better; better &= better - 1) list = insert(list, __shfl_sync(FULL_MASK, c, __ffs(better) - 1), lane);
+              for (unsigned x = more; x; x &= x - 1) list = insert(list, __shfl_sync(FULL_MASK, best, __ffs(x) - 1), lane);
             }
-            thr = __shfl_sync(FULL_MASK, list, n - 1);
+            last = __shfl_sync(FULL_MASK, list, n - 1);
           }
-          if (!any) break;
         }
       }
     }
@@ -268,12 +366,12 @@ constexpr int SMS = 152;          // grids are sized for the whole GPU
 
 }  // namespace
 
-// Slices of a row: about four CTAs an SM over all rows, a batch each at least.
+// Slices of a row: about eight CTAs an SM over all rows, a batch each at least.
 int beam_splits(int rows, int V) {
   const int batches = (V + BATCH - 1) / BATCH;
-  return std::max(1, std::min(batches, (4 * SMS + rows - 1) / rows));
+  return std::max(1, std::min(batches, (8 * SMS + rows - 1) / rows));
 }
-int beam_parts_bound(int rows) { return 4 * SMS + rows; }
+int beam_parts_bound(int rows) { return 8 * SMS + rows; }
 
 cudaError_t launch_beam_select(const BeamArgs& a, kva_dtype dtype, cudaStream_t s) {
   const dim3 grid(a.splits, a.B * a.K);
