@@ -77,33 +77,32 @@ __device__ __forceinline__ Key insert(Key list, Key k, int lane) {      // k: th
 
 // 16 values of a row as they lie in memory, and as floats (-infinity past its end).
 template <typename T> struct Batch {
-  uint4 r[sizeof(T) * PER / 16];
-  float edge[PER];                               // a batch at the row's end, or of a row that is not aligned
-  bool whole;
+  static constexpr int WORDS = sizeof(T) * PER / 4;
+  uint32_t r[WORDS];
   __device__ __forceinline__ void load(const T* row, int i, int V, bool aligned) {
-    whole = aligned && i + PER <= V;
-    if (whole) {
+    if (aligned && i + PER <= V) {
 #pragma unroll
-      for (int e = 0; e < (int)sizeof(T) * PER / 16; ++e) r[e] = __ldg(reinterpret_cast<const uint4*>(row + i) + e);
-    } else {
+      for (int e = 0; e < WORDS / 4; ++e) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i) + e);
+        r[4 * e] = w.x; r[4 * e + 1] = w.y; r[4 * e + 2] = w.z; r[4 * e + 3] = w.w;
+      }
+    } else {                                       // the row's end, or a row that is not aligned
 #pragma unroll
-      for (int e = 0; e < PER; ++e) edge[e] = i + e < V ? load1(row + i + e) : -INFINITY;
+      for (int e = 0; e < WORDS; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t lo = i + 2 * e < V ? row[i + 2 * e].bits : 0xff80u, hi = i + 2 * e + 1 < V ? row[i + 2 * e + 1].bits : 0xff80u;
+          r[e] = lo | hi << 16;
+        } else {
+          r[e] = i + e < V ? __float_as_uint(row[i + e]) : 0xff800000u;
+        }
+      }
     }
   }
   __device__ __forceinline__ void values(float (&x)[PER]) const {
-    if (whole) {
 #pragma unroll
-      for (int e = 0; e < (int)sizeof(T) * PER / 16; ++e) {
-        const uint32_t w[4] = {r[e].x, r[e].y, r[e].z, r[e].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (sizeof(T) == 2) { x[8 * e + 2 * k] = bf16_lo(w[k]); x[8 * e + 2 * k + 1] = bf16_hi(w[k]); }
-          else x[4 * e + k] = __uint_as_float(w[k]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < PER; ++e) x[e] = edge[e];
+    for (int e = 0; e < WORDS; ++e) {
+      if constexpr (sizeof(T) == 2) { x[2 * e] = bf16_lo(r[e]); x[2 * e + 1] = bf16_hi(r[e]); }
+      else x[e] = __uint_as_float(r[e]);
     }
   }
 };
@@ -222,11 +221,13 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       const bool all = second >= bound && second > -INFINITY;
       for (int bt = all ? b0 : best_at; bt < (all ? b1 : best_at + 1); ++bt) {
         const int i0 = bt * BATCH + tid * PER;
-        for (int e = 0; e < PER && i0 + e < a.V; ++e) {
-          const float v = load1(z + i0 + e);
-          if (v >= bound && v > -INFINITY) {
+        float x[PER];
+        load_values(z, i0, a.V, aligned, x);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          if (x[e] >= bound && x[e] > -INFINITY) {
             const int at = atomicAdd(&s_count, 1);
-            if (at < LIST) s_cand[at] = key_of(v, i0 + e);
+            if (at < LIST) s_cand[at] = key_of(x[e], i0 + e);
           }
         }
       }
@@ -337,18 +338,20 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
   int at = 0;
   const bool beam = lane < a.K;
   const double base = beam ? s_base[lane] : NAN, top = beam ? s_top[lane] : 0.0;   // done: a value of 0, less 0
+  int wide = 1;                                    // lanes that hold the beams
+  while (wide < a.K) wide <<= 1;
   for (int j = 0; j < n; ++j) {
     const Key head = beam && at < 32 ? s_best[lane][at] : 0;
     double total = -INFINITY;
     if (head != 0 && base == base) total = ((double)key_value(head) - top) + base;   // the difference first: both may be huge
     double best = total;
     int who = lane;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = wide >> 1; o > 0; o >>= 1) {
       const double t = __shfl_xor_sync(FULL_MASK, best, o);
       const int w = __shfl_xor_sync(FULL_MASK, who, o);
       if (t > best || (t == best && w < who)) { best = t; who = w; }
     }
+    who = __shfl_sync(FULL_MASK, who, 0);
     const int id = __shfl_sync(FULL_MASK, key_id(head), who);
     if (lane == who) ++at;
     if (lane == 0) {
