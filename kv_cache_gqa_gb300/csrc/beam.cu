@@ -1,17 +1,19 @@
 // Beam search's selection over beams and vocabulary (beam_select).
 //
-// A CTA takes a slice of one beam's logits in batches of 16 values a thread, the next batch on its way.  A thread keeps its own
+// A CTA takes a slice of one beam's logits in batches of 64 bytes a thread, the next batch on its way.  A thread keeps its own
 // maximum, its sum of exponentials, the best of its batch maxima and the second best.  At the slice's end a warp sorts its threads'
 // maxima; the n-th of them, the largest over the warps, is a bound that at least n values of the slice reach and few others do.  The
 // threads that reach it read the one batch again that holds their maximum (all of theirs where the second best reaches it, too), and
 // the values at or above the bound are sorted: about n to 3 n of them.  Where they do not fit a list of 1024 (rows of equal or
 // sorted values), warps keep sorted lists over the whole slice instead.  The last CTA of a group joins the slices: a warp per
-// beam, then the best n of the beams' sorted lists, a lane per beam, by totals in 64 bits (beams that are nearly even keep their order).
+// beam, then a thread per offer, which counts the offers of the other beams before its own (binary searches), by totals in 64 bits
+// (beams that are nearly even keep their order).
 // A beam that is done, or whose score is -infinity, is not read.
 //
 // Sums are float32 per thread and slice, 64 bits where they are joined.  Which thread takes an element depends on its index
 // alone, so equal rows give equal totals.  exp(x - m) is 2^(x log2 e - c), c = m log2 e rounded, with log2 e in two parts, and the sum is
-// put right for c's rounding at the end.
+// put right for c's rounding at the end.  Slices hand over sums of 2^(x log2 e - k) with whole k, which join without an exponential:
+// 64-bit arithmetic is slow here (exp 2.6 us, log 1.2 us).
 //
 // The runtime's own options (HunyuanOCR v1.5 ncnn port, section 3.6) stop at top_k; it has no beams.
 #include <algorithm>
@@ -24,8 +26,7 @@ namespace kva {
 namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int PER = 16;                          // values of a lane in a batch
-constexpr int BATCH = THREADS * PER;             // of a CTA
+constexpr int PER = 16;                          // values that a thread works on at a time
 constexpr float LOW = -3.402823466e38f;          // a maximum of nothing (finite: no infinity minus infinity)
 
 __device__ __forceinline__ float ex2(float x) {
@@ -75,12 +76,12 @@ __device__ __forceinline__ Key insert(Key list, Key k, int lane) {      // k: th
   return lane < at ? list : (lane == at ? k : up);
 }
 
-// 16 values of a row as they lie in memory, and as floats (-infinity past its end).
+// 64 bytes of a row as they lie in memory (-infinity past its end), taken as GROUPS times 16 floats.
 template <typename T> struct Batch {
-  static constexpr int WORDS = sizeof(T) * PER / 4;
+  static constexpr int GROUPS = 4 / sizeof(T), WIDE = PER * GROUPS, WORDS = 16;     // WIDE: values
   uint32_t r[WORDS];
   __device__ __forceinline__ void load(const T* row, int i, int V, bool aligned) {
-    if (aligned && i + PER <= V) {
+    if (aligned && i + WIDE <= V) {
 #pragma unroll
       for (int e = 0; e < WORDS / 4; ++e) {
         const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i) + e);
@@ -98,20 +99,15 @@ template <typename T> struct Batch {
       }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[PER]) const {
+  __device__ __forceinline__ void values(int g, float (&x)[PER]) const {
 #pragma unroll
-    for (int e = 0; e < WORDS; ++e) {
-      if constexpr (sizeof(T) == 2) { x[2 * e] = bf16_lo(r[e]); x[2 * e + 1] = bf16_hi(r[e]); }
-      else x[e] = __uint_as_float(r[e]);
+    for (int e = 0; e < WORDS / GROUPS; ++e) {
+      const uint32_t w = r[g * (WORDS / GROUPS) + e];
+      if constexpr (sizeof(T) == 2) { x[2 * e] = bf16_lo(w); x[2 * e + 1] = bf16_hi(w); }
+      else x[e] = __uint_as_float(w);
     }
   }
 };
-template <typename T>
-__device__ __forceinline__ void load_values(const T* row, int i, int V, bool aligned, float (&x)[PER]) {
-  Batch<T> b;
-  b.load(row, i, V, aligned);
-  b.values(x);
-}
 
 // The best keys among a warp's values x of ids first + lane * PER + e into its list; last: the list's n-th (0: not full).
 __device__ __forceinline__ void warp_best(const float (&x)[PER], int i0, int n, int lane, Key& list, Key& last) {
@@ -140,14 +136,14 @@ constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;       // log2 e =
 constexpr float HUGE_M = 1e30f;                  // beyond it m log2 e could overflow
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 4)
 beam_select_kernel(const __grid_constant__ BeamArgs a) {
   __shared__ Key s_cand[LIST];
   __shared__ Key s_list[WARPS][32];
   __shared__ float s_m[WARPS], s_s[WARPS], s_bound[WARPS];
   __shared__ int s_count, s_last;
-  __shared__ double s_base[BEAM_MAX], s_top[BEAM_MAX];   // score - log sum of a beam (NaN: it offers nothing), its maximum
-  __shared__ Key s_best[BEAM_MAX][33];
+  __shared__ Key s_best[BEAM_MAX][33];             // a beam's offers
+  __shared__ Key s_total[BEAM_MAX][33];            // and their totals, ordered as whole numbers (0: no offer)
   const int row = blockIdx.y, split = blockIdx.x, b = row / a.K;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n;
   griddep_wait();                               // inputs of this launch are complete from here on
@@ -157,42 +153,50 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
   if (!done && score > -INFINITY) {
     const T* z = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
     const bool aligned = (reinterpret_cast<uintptr_t>(z) & 15u) == 0;
+    using Part = Batch<T>;
+    constexpr int BATCH = THREADS * Part::WIDE;
     const int batches = (a.V + BATCH - 1) / BATCH;
     const int b0 = (int)((int64_t)batches * split / gridDim.x), b1 = (int)((int64_t)batches * (split + 1) / gridDim.x);
     if (tid == 0) s_count = 0;
     float m = LOW, c = 0.f, s = 0.f;               // s: sum of 2^(x log2 e - c), or of exp(x - m) where |m| >= HUGE_M
     float best = -INFINITY, second = -INFINITY;    // of the batches' maxima
     int best_at = b0;
-    Batch<T> next;
-    if (b0 < b1) next.load(z, b0 * BATCH + tid * PER, a.V, aligned);
+    Part next;
+    if (b0 < b1) next.load(z, b0 * BATCH + tid * Part::WIDE, a.V, aligned);
     for (int bt = b0; bt < b1; ++bt) {
-      float x[PER];
-      next.values(x);
-      if (bt + 1 < b1) next.load(z, (bt + 1) * BATCH + tid * PER, a.V, aligned);
-      float top = fmaxf(x[0], x[1]);
+      const Part now = next;
+      if (bt + 1 < b1) next.load(z, (bt + 1) * BATCH + tid * Part::WIDE, a.V, aligned);
+      float high = -INFINITY;
 #pragma unroll
-      for (int e = 2; e < PER; e += 2) top = fmax3(top, x[e], x[e + 1]);
-      if (top > best) { second = best; best = top; best_at = bt; }
-      else second = fmaxf(second, top);
-      if (top > m) {
-        const float to = top * L2E_HI;
-        s *= ex2(fabsf(m) < HUGE_M && fabsf(top) < HUGE_M ? c - to : (m - top) * L2E_HI);
-        m = top;
-        c = to;
-      }
-      if (fabsf(m) < HUGE_M) {
-        const uint64_t hi2 = pack_f32x2(L2E_HI, L2E_HI), lo2 = pack_f32x2(L2E_LO, L2E_LO), c2 = pack_f32x2(-c, -c);
-        uint64_t sum = 0ull;
+      for (int g = 0; g < Part::GROUPS; ++g) {
+        float x[PER];
+        now.values(g, x);
+        float top = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-          const uint64_t x2 = pack_f32x2(x[e], x[e + 1]), t = fma_f32x2(x2, lo2, fma_f32x2(x2, hi2, c2));
-          sum = add_f32x2(sum, pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t))));
+        for (int e = 2; e < PER; e += 2) top = fmax3(top, x[e], x[e + 1]);
+        high = fmaxf(high, top);
+        if (top > m) {
+          const float to = top * L2E_HI;
+          s *= ex2(fabsf(m) < HUGE_M && fabsf(top) < HUGE_M ? c - to : (m - top) * L2E_HI);
+          m = top;
+          c = to;
         }
-        s += f32x2_lo(sum) + f32x2_hi(sum);
-      } else {
+        if (fabsf(m) < HUGE_M) {
+          const uint64_t hi2 = pack_f32x2(L2E_HI, L2E_HI), lo2 = pack_f32x2(L2E_LO, L2E_LO), c2 = pack_f32x2(-c, -c);
+          uint64_t sum = 0ull;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) s += ex2((x[e] - m) * L2E_HI);
+          for (int e = 0; e < PER; e += 2) {
+            const uint64_t x2 = pack_f32x2(x[e], x[e + 1]), t = fma_f32x2(x2, lo2, fma_f32x2(x2, hi2, c2));
+            sum = add_f32x2(sum, pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t))));
+          }
+          s += f32x2_lo(sum) + f32x2_hi(sum);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) s += ex2((x[e] - m) * L2E_HI);
+        }
       }
+      if (high > best) { second = best; best = high; best_at = bt; }
+      else second = fmaxf(second, high);
     }
     if (fabsf(m) < HUGE_M) s *= ex2(fmaf(-m, L2E_LO, fmaf(-m, L2E_HI, c)));    // now of exp(x - m)
     // the warp's sums, and its n-th best maximum of a thread
@@ -220,14 +224,18 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     if (best >= bound && best > -INFINITY) {
       const bool all = second >= bound && second > -INFINITY;
       for (int bt = all ? b0 : best_at; bt < (all ? b1 : best_at + 1); ++bt) {
-        const int i0 = bt * BATCH + tid * PER;
-        float x[PER];
-        load_values(z, i0, a.V, aligned, x);
+        const int i0 = bt * BATCH + tid * Part::WIDE;
+        next.load(z, i0, a.V, aligned);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          if (x[e] >= bound && x[e] > -INFINITY) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < LIST) s_cand[at] = key_of(x[e], i0 + e);
+        for (int g = 0; g < Part::GROUPS; ++g) {
+          float x[PER];
+          next.values(g, x);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            if (x[e] >= bound && x[e] > -INFINITY) {
+              const int at = atomicAdd(&s_count, 1);
+              if (at < LIST) s_cand[at] = key_of(x[e], i0 + g * PER + e);
+            }
           }
         }
       }
@@ -242,9 +250,15 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       }
     } else {
       for (int bt = b0; bt < b1; ++bt) {
-        float x[PER];
-        load_values(z, bt * BATCH + tid * PER, a.V, aligned, x);
-        warp_best(x, bt * BATCH + tid * PER, n, lane, list, last);
+        const int i0 = bt * BATCH + tid * Part::WIDE;
+        next.load(z, i0, a.V, aligned);
+#pragma unroll 1
+        for (int g = 0; g < Part::GROUPS; ++g) {
+          float x[PER];
+          if (g == 0) next.values(0, x);
+          else next.values(Part::GROUPS - 1, x);
+          warp_best(x, i0 + g * PER, n, lane, list, last);
+        }
       }
     }
     s_list[warp][lane] = lane < n ? list : 0;
@@ -259,8 +273,12 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
         float CM = LOW, S = 0.f;
         for (int w = 0; w < WARPS; ++w) CM = fmaxf(CM, s_m[w]);
         for (int w = 0; w < WARPS; ++w) S = fmaf(s_s[w], ex2((s_m[w] - CM) * L2E_HI), S);
-        a.part_stat[2 * part] = CM;
-        a.part_stat[2 * part + 1] = S;
+        // exp(CM) = 2^(CM log2 e): a whole power k, and the rest goes into the sum.  Huge values: the maximum as it is, and the
+        // sum with a minus.
+        const float k = rintf(CM * L2E_HI);
+        const bool plain = fabsf(CM) < HUGE_M;
+        a.part_stat[2 * part] = plain ? k : CM;
+        a.part_stat[2 * part + 1] = plain ? S * ex2(fmaf(CM, L2E_LO, fmaf(CM, L2E_HI, -k))) : -S;
       }
     }
   }
@@ -276,14 +294,14 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     const float sc = a.scores[r];
     const bool is_done = a.finished != nullptr && a.finished[r] != 0;
     Key list = 0, last = 0;
-    double base = NAN, top = 0.0;
+    double base = NAN, top = 0.0;                    // an offer's total is (value - top) + base
     if (is_done) {
       base = (double)sc;
       if (lane == 0) list = key_of(0.f, a.end_id);
     } else if (sc > -INFINITY) {
       const int64_t part = (int64_t)r * gridDim.x;
       const int keys = (int)gridDim.x * n;
-      constexpr int KPL = 8;                         // keys of a lane at a time
+      constexpr int KPL = 12;                        // keys of a lane at a time
       Key ahead[KPL];
       auto fetch = [&](int i0) {
 #pragma unroll
@@ -293,21 +311,40 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
         }
       };
       fetch(0);
-      float M = LOW;
-      for (int i = lane; i < (int)gridDim.x; i += 32) M = fmaxf(M, __ldcg(a.part_stat + 2 * (part + i)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-      double S = 0.0;
+      // the largest power of the slices, and the largest maximum of those of huge values, which count among themselves
+      float power = -INFINITY, huge = -INFINITY;
+      bool odd = false;
       for (int i = lane; i < (int)gridDim.x; i += 32) {
         const float2 st = __ldcg(reinterpret_cast<const float2*>(a.part_stat) + part + i);
-        S += (double)st.y * exp((double)st.x - (double)M);
+        odd |= !(fabsf(st.y) < INFINITY);
+        if (st.y > 0.f) power = fmaxf(power, st.x);
+        if (st.y < 0.f) huge = fmaxf(huge, st.x);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(FULL_MASK, S, o);
-      const bool good = S > 0.0 && S < 1e300;      // not a row of -infinity, nor one with NaN or +infinity
-      if (good) {
-        base = (double)sc - log(S);
-        top = (double)M;
+      for (int o = 16; o > 0; o >>= 1) {
+        power = fmaxf(power, __shfl_xor_sync(FULL_MASK, power, o));
+        huge = fmaxf(huge, __shfl_xor_sync(FULL_MASK, huge, o));
+      }
+      const bool plain = !(huge > 0.f) && power > -INFINITY;
+      float S = 0.f, rest = 0.f;                     // a sum and what its additions rounded away
+      auto add = [&](float y, float more) {
+        const float t = S + y, u = t - S;
+        rest += (S - (t - u)) + (y - u) + more;
+        S = t;
+      };
+      for (int i = lane; i < (int)gridDim.x; i += 32) {
+        const float2 st = __ldcg(reinterpret_cast<const float2*>(a.part_stat) + part + i);
+        if (plain && st.y > 0.f) add(st.y * ex2(fmaxf(st.x - power, -120.f)), 0.f);      // a whole power: exact
+        if (!plain && st.y < 0.f && st.x == huge) add(-st.y, 0.f);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) add(__shfl_xor_sync(FULL_MASK, S, o), __shfl_xor_sync(FULL_MASK, rest, o));
+      odd = __any_sync(FULL_MASK, odd);
+      if (!odd && S > 0.f) {                         // neither a row of -infinity, nor one with NaN or +infinity
+        constexpr double LN2 = 0.69314718055994530942;
+        base = (double)sc - log((double)S + (double)rest);
+        if (plain) base -= (double)power * LN2;
+        else top = (double)huge;
         for (int i0 = 0; i0 < keys; i0 += 32 * KPL) {
           if (i0 > 0) fetch(i0);
           Key left = ~0ull;                          // keys below this one are not taken yet
@@ -329,52 +366,68 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
         }
       }
     }
-    s_best[k][lane] = lane < n ? list : 0;
-    if (lane == 0) { s_base[k] = base; s_top[k] = top; }
+    if (lane >= n) list = 0;
+    Key total = 0;
+    if (list != 0 && base == base) {
+      const double v = ((double)key_value(list) - top) + base;         // the difference first: both may be huge
+      const unsigned long long bits = (unsigned long long)__double_as_longlong(v + 0.0);
+      if (v > -INFINITY) total = bits >> 63 ? ~bits : bits | (1ull << 63);
+    }
+    s_best[k][lane] = list;
+    s_total[k][lane] = total;
   }
   __syncthreads();
-  if (warp != 0) return;
-  // a lane per beam with its list's head; n times the best of them, the lower beam among equals
-  int at = 0;
-  const bool beam = lane < a.K;
-  const double base = beam ? s_base[lane] : NAN, top = beam ? s_top[lane] : 0.0;   // done: a value of 0, less 0
-  int wide = 1;                                    // lanes that hold the beams
-  while (wide < a.K) wide <<= 1;
-  for (int j = 0; j < n; ++j) {
-    const Key head = beam && at < 32 ? s_best[lane][at] : 0;
-    double total = -INFINITY;
-    if (head != 0 && base == base) total = ((double)key_value(head) - top) + base;   // the difference first: both may be huge
-    double best = total;
-    int who = lane;
-    for (int o = wide >> 1; o > 0; o >>= 1) {
-      const double t = __shfl_xor_sync(FULL_MASK, best, o);
-      const int w = __shfl_xor_sync(FULL_MASK, who, o);
-      if (t > best || (t == best && w < who)) { best = t; who = w; }
+  // a thread per offer: its place is the number of offers before it
+  int offers = 0;
+  for (int k = 0; k < a.K; ++k) {                   // how many there are, by binary search for the first 0
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_total[k][mid] != 0) lo = mid + 1; else hi = mid;
     }
-    who = __shfl_sync(FULL_MASK, who, 0);
-    const int id = __shfl_sync(FULL_MASK, key_id(head), who);
-    if (lane == who) ++at;
-    if (lane == 0) {
-      const bool none = !(best > -INFINITY);
-      const int64_t o = (int64_t)b * n + j;
-      a.out_beam[o] = none ? -1 : who;
-      a.out_token[o] = none ? -1 : id;
-      a.out_score[o] = none ? -INFINITY : (float)best;
-    }
+    offers += lo;
   }
-  if (lane == 0) a.counters[b] = 0u;
+  for (int i = tid; i < a.K * n; i += THREADS) {
+    const int k = i / n, j = i - k * n;
+    const Key total = s_total[k][j];
+    if (total == 0) continue;
+    int place = j;
+    for (int q = 0; q < a.K && place < n; ++q) {
+      if (q == k) continue;
+      int lo = 0, hi = n;                           // offers of beam q before this one: larger, or equal and of a lower beam
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const Key t = s_total[q][mid];
+        if (t > total || (t == total && q < k)) lo = mid + 1; else hi = mid;
+      }
+      place += lo;
+    }
+    if (place >= n) continue;
+    const int64_t o = (int64_t)b * n + place;
+    a.out_beam[o] = k;
+    a.out_token[o] = key_id(s_best[k][j]);
+    const unsigned long long bits = total >> 63 ? total & ~(1ull << 63) : ~total;
+    a.out_score[o] = (float)__longlong_as_double((long long)bits);
+  }
+  if (tid >= offers && tid < n) {
+    const int64_t o = (int64_t)b * n + tid;
+    a.out_beam[o] = -1;
+    a.out_token[o] = -1;
+    a.out_score[o] = -INFINITY;
+  }
+  if (tid == 0) a.counters[b] = 0u;
 }
 
 constexpr int SMS = 152;          // grids are sized for the whole GPU
 
 }  // namespace
 
-// Slices of a row: about eight CTAs an SM over all rows, a batch each at least.
+// Slices of a row: about six CTAs an SM over all rows, a batch of float32 values each at least.
 int beam_splits(int rows, int V) {
-  const int batches = (V + BATCH - 1) / BATCH;
-  return std::max(1, std::min(batches, (8 * SMS + rows - 1) / rows));
+  const int batches = (V + THREADS * PER - 1) / (THREADS * PER);
+  return std::max(1, std::min(batches, (6 * SMS + rows - 1) / rows));
 }
-int beam_parts_bound(int rows) { return 8 * SMS + rows; }
+int beam_parts_bound(int rows) { return 6 * SMS + rows; }
 
 cudaError_t launch_beam_select(const BeamArgs& a, kva_dtype dtype, cudaStream_t s) {
   const dim3 grid(a.splits, a.B * a.K);
