@@ -80,14 +80,34 @@ __device__ __forceinline__ Key insert(Key list, Key k, int lane) {      // k: th
 template <typename T> struct Batch {
   static constexpr int GROUPS = 4 / sizeof(T), WIDE = PER * GROUPS, WORDS = 16;     // WIDE: values
   uint32_t r[WORDS];
-  __device__ __forceinline__ void load(const T* row, int i, int V, bool aligned) {
-    if (aligned && i + WIDE <= V) {
+  // shift: the bytes of the row's start past a multiple of 16 (uniform over the CTA)
+  __device__ __forceinline__ void load(const T* row, int i, int V, int shift) {
+    if (shift == 0 && i + WIDE <= V) {
 #pragma unroll
       for (int e = 0; e < WORDS / 4; ++e) {
         const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i) + e);
         r[4 * e] = w.x; r[4 * e + 1] = w.y; r[4 * e + 2] = w.z; r[4 * e + 3] = w.w;
       }
-    } else {                                       // the row's end, or a row that is not aligned
+    } else if (shift != 0 && i > 0 && i + WIDE + 16 / (int)sizeof(T) <= V) {
+      // the aligned words around them, moved down by `shift` bytes
+      uint32_t w[WORDS + 4];
+      const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + i) - shift);
+#pragma unroll
+      for (int e = 0; e < WORDS / 4 + 1; ++e) {
+        const uint4 x = __ldg(at + e);
+        w[4 * e] = x.x; w[4 * e + 1] = x.y; w[4 * e + 2] = x.z; w[4 * e + 3] = x.w;
+      }
+      if (shift & 8) {
+#pragma unroll
+        for (int e = 0; e < WORDS + 2; ++e) w[e] = w[e + 2];
+      }
+      if (shift & 4) {
+#pragma unroll
+        for (int e = 0; e < WORDS + 1; ++e) w[e] = w[e + 1];
+      }
+#pragma unroll
+      for (int e = 0; e < WORDS; ++e) r[e] = sizeof(T) == 2 ? __funnelshift_r(w[e], w[e + 1], (shift & 2) * 8) : w[e];
+    } else {                                       // the row's ends
 #pragma unroll
       for (int e = 0; e < WORDS; ++e) {
         if constexpr (sizeof(T) == 2) {
@@ -152,7 +172,7 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
   const bool done = a.finished != nullptr && a.finished[row] != 0;
   if (!done && score > -INFINITY) {
     const T* z = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
-    const bool aligned = (reinterpret_cast<uintptr_t>(z) & 15u) == 0;
+    const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15u);
     using Part = Batch<T>;
     constexpr int BATCH = THREADS * Part::WIDE;
     const int batches = (a.V + BATCH - 1) / BATCH;
@@ -162,10 +182,10 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     float best = -INFINITY, second = -INFINITY;    // of the batches' maxima
     int best_at = b0;
     Part next;
-    if (b0 < b1) next.load(z, b0 * BATCH + tid * Part::WIDE, a.V, aligned);
+    if (b0 < b1) next.load(z, b0 * BATCH + tid * Part::WIDE, a.V, shift);
     for (int bt = b0; bt < b1; ++bt) {
       const Part now = next;
-      if (bt + 1 < b1) next.load(z, (bt + 1) * BATCH + tid * Part::WIDE, a.V, aligned);
+      if (bt + 1 < b1) next.load(z, (bt + 1) * BATCH + tid * Part::WIDE, a.V, shift);
       float high = -INFINITY;
 #pragma unroll
       for (int g = 0; g < Part::GROUPS; ++g) {
@@ -225,18 +245,18 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       const bool all = second >= bound && second > -INFINITY;
       for (int bt = all ? b0 : best_at; bt < (all ? b1 : best_at + 1); ++bt) {
         const int i0 = bt * BATCH + tid * Part::WIDE;
-        next.load(z, i0, a.V, aligned);
+        next.load(z, i0, a.V, shift);
+        uint32_t hits = 0u;
 #pragma unroll
         for (int g = 0; g < Part::GROUPS; ++g) {
           float x[PER];
           next.values(g, x);
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            if (x[e] >= bound && x[e] > -INFINITY) {
-              const int at = atomicAdd(&s_count, 1);
-              if (at < LIST) s_cand[at] = key_of(x[e], i0 + g * PER + e);
-            }
-          }
+          for (int e = 0; e < PER; ++e) hits |= (x[e] >= bound && x[e] > -INFINITY ? 1u : 0u) << (g * PER + e);
+        }
+        for (; hits; hits &= hits - 1) {
+          const int id = i0 + __ffs(hits) - 1, at = atomicAdd(&s_count, 1);
+          if (at < LIST) s_cand[at] = key_of(load1(z + id), id);
         }
       }
     }
@@ -251,7 +271,7 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     } else {
       for (int bt = b0; bt < b1; ++bt) {
         const int i0 = bt * BATCH + tid * Part::WIDE;
-        next.load(z, i0, a.V, aligned);
+        next.load(z, i0, a.V, shift);
 #pragma unroll 1
         for (int g = 0; g < Part::GROUPS; ++g) {
           float x[PER];
@@ -422,7 +442,8 @@ constexpr int SMS = 152;          // grids are sized for the whole GPU
 
 }  // namespace
 
-// Slices of a row: about six CTAs an SM over all rows, a batch of float32 values each at least.
+// Slices of a row: about six CTAs an SM over all rows, a batch of float32 values each at least.  A CTA spends about 7 us beside reading,
+// which others' reading should cover: 32 x 8 beams, 40% of them done, took 38 / 31 / 34 / 36 us with 3 / 6 / 8 / 12.
 int beam_splits(int rows, int V) {
   const int batches = (V + THREADS * PER - 1) / (THREADS * PER);
   return std::max(1, std::min(batches, (6 * SMS + rows - 1) / rows));
