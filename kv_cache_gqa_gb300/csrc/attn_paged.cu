@@ -43,10 +43,13 @@ Load load_of(const PagedArgs& a, const int32_t* lengths, const int32_t* start, i
   return w;
 }
 
-// As many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps.
+// As many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps.  A whole number of
+// runs a unit, where there are four of them or more: units of equal length (one sequence's heads) then begin with a run each
+// (one sequence of 768 slots: 13.0 us, so 10.5).
 int runs_of(const Load& w, int slots) {
   const int64_t most = std::min<int64_t>(slots, (int64_t)(2.0 * std::sqrt((double)w.steps * (double)w.units)));
-  return (int)std::max<int64_t>(1, std::min(most, w.steps));
+  const int64_t runs = std::max<int64_t>(1, std::min(most, w.steps));
+  return (int)(runs >= 4 * w.units ? runs / w.units * w.units : runs);
 }
 
 }  // namespace

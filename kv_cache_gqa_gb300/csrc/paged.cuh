@@ -100,12 +100,17 @@ struct Place {
   }
 };
 
+// Quotients of numbers that mostly fit 32 bits (a division of 64 takes some hundred cycles).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // All steps, their runs, and this CTA's run [x0, x1).
 struct Run {
   int64_t total, x0, x1;
   int runs;
-  __device__ __forceinline__ int64_t start_of(int c) const { return total * c / runs; }
-  __device__ __forceinline__ int of(int64_t x) const { return (int)(((x + 1) * runs - 1) / total); }
+  __device__ __forceinline__ int64_t start_of(int c) const { return divide(total * c, runs); }
+  __device__ __forceinline__ int of(int64_t x) const { return (int)divide((x + 1) * runs - 1, total); }
 };
 
 // This CTA's run and the place of its first step (none: x0 = x1).  Whole CTA; scratch: THREADS / 32 + 4 words.
@@ -114,10 +119,13 @@ __device__ __forceinline__ Run first_place(const PagedArgs& a, const C& c, int64
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // sum of all sequences, kept per thread for a batch of up to THREADS of them
+  __shared__ Seq s_seq;
   int64_t mine = 0, first = 0;
+  Seq kept{};
   for (int b = tid; b < a.B; b += THREADS) {
-    const int64_t n = c.head_steps(sequence(a, b)) * a.Hkv;
-    if (b == tid) first = n;
+    const Seq seq = sequence(a, b);
+    const int64_t n = c.head_steps(seq) * a.Hkv;
+    if (b == tid) { first = n; kept = seq; }
     mine += n;
   }
 #pragma unroll
@@ -143,7 +151,14 @@ __device__ __forceinline__ Run first_place(const PagedArgs& a, const C& c, int64
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + tid;
-    const int64_t n = b0 == 0 ? first : (b < a.B ? c.head_steps(sequence(a, b)) * a.Hkv : 0);
+    if (b0 > 0) {
+      first = 0;
+      if (b < a.B) {
+        kept = sequence(a, b);
+        first = c.head_steps(kept) * a.Hkv;
+      }
+    }
+    const int64_t n = first;
     int64_t upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -160,16 +175,16 @@ __device__ __forceinline__ Run first_place(const PagedArgs& a, const C& c, int64
       all += scratch[w];
     }
     const int64_t lo = before + upto - n;
-    if (b < a.B && x0 >= lo && x0 < lo + n) { scratch[W] = lo; scratch[W + 1] = b; }
+    if (b < a.B && x0 >= lo && x0 < lo + n) { scratch[W] = lo; scratch[W + 1] = b; s_seq = kept; }
     base = all;
     if (x0 < all) break;                          // uniform
   }
   __syncthreads();
   p->b = (int)scratch[W + 1];
-  p->s = sequence(a, p->b);
+  p->s = s_seq;
   p->n_tiles = c.tiles(p->s);
   const int64_t head = c.head_steps(p->s), in = x0 - scratch[W];
-  p->g = (int)(in / head);
+  p->g = (int)divide(in, head);
   int64_t rest = in - p->g * head;
   p->rt = 0;
   p->n_steps = c.steps(p->s, 0);
@@ -238,48 +253,76 @@ __device__ __forceinline__ void finish_unit(const PagedArgs& a, const Cut& cut, 
   }
   if (whole) return;
   const int c0 = run.of(p.at), c1 = run.of(p.at + p.n_steps - 1);
-  __threadfence();
-  __syncthreads();
+  __syncthreads();                                // the CTA's part is written; thread 0's fences cover all of it
   unsigned* counter = a.counters + c0;            // only the last unit of a run goes on into the next one
-  if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+  if (tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+    __threadfence();
+  }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   const int first = (c0 * 2 + (run.start_of(c0) >= p.at ? 0 : 1)) * R;   // the others' parts are their [0]
-  constexpr int BLOCK = SCRATCH / (R * 4) < 512 ? SCRATCH / (R * 4) : 512;    // parts whose weights fit
+  auto part = [&](int c) { return c == c0 ? first : 2 * R * c; };
+  constexpr int BLOCK = SCRATCH / (R * 8) < 512 ? SCRATCH / (R * 8) : 512;    // parts whose (maximum, sum) fit
+  float2* ml = reinterpret_cast<float2*>(sm);     // [R][BLOCK]; the maxima become weights
+  __shared__ float s_alpha[R];
   float acc[EPT];
 #pragma unroll
   for (int e = 0; e < EPT; ++e) acc[e] = 0.f;
-  if (tid < R) {                                  // the join's maximum first, then weights block by block
-    float M = M_NONE;
-    for (int c = c0; c <= c1 && tid < here; ++c)
-      M = fmaxf(M, __ldcg(a.part_ml + 2 * ((c == c0 ? first : 2 * R * c) + tid)));
-    s_M[tid] = M;
-    s_L[tid] = 0.f;
-  }
-  __syncthreads();
-  for (int cb = c0; cb <= c1; cb += BLOCK) {
+  if (tid < R) { s_M[tid] = M_NONE; s_L[tid] = 0.f; }
+  for (int cb = c0; cb <= c1; cb += BLOCK) {      // one pass, unless the unit has very many parts
     const int n = min(BLOCK, c1 + 1 - cb);
+    constexpr int U = EPT <= 8 ? 4 : 2;           // parts on their way, the first ones before the weights are known
+    float v[U][EPT];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* src = a.part_acc + (int64_t)part(cb + c + u) * DV;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e)
+          v[u][e] = c + u < n && (tid + e * THREADS) / DV < here ? __ldcg(src + tid + e * THREADS) : 0.f;
+      }
+    };
+    fetch(0);
+    __syncthreads();
     for (int i = tid; i < R * n; i += THREADS) {
-      const int c = cb + i / R, r = i % R;
-      sm[i] = r < here ? ex2(__ldcg(a.part_ml + 2 * ((c == c0 ? first : 2 * R * c) + r)) - s_M[r]) : 0.f;
+      const int c = i / R, r = i % R;
+      ml[r * BLOCK + c] = r < here ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + part(cb + c) + r) : make_float2(M_NONE, 0.f);
     }
     __syncthreads();
-    if (tid < here) {
-      float L = s_L[tid];
-      for (int c = 0; c < n; ++c)
-        L = fmaf(sm[c * R + tid], __ldcg(a.part_ml + 2 * ((cb + c == c0 ? first : 2 * R * (cb + c)) + tid) + 1), L);
-      s_L[tid] = L;
-    }
-    for (int c = 0; c < n; ++c) {
-      const float* src = a.part_acc + (int64_t)(cb + c == c0 ? first : 2 * R * (cb + c)) * DV;
+    const int lane = tid & 31;
+    for (int r = tid >> 5; r < R; r += W) {       // weights against the maximum so far
+      const float before = s_M[r];
+      float M = before, den = 0.f;
+      for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[r * BLOCK + c].x);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        const int idx = tid + e * THREADS;
-        if (idx / DV < here) acc[e] = fmaf(sm[c * R + idx / DV], __ldcg(src + idx), acc[e]);
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
+      for (int c = lane; c < n; c += 32) {
+        const float w = ex2(ml[r * BLOCK + c].x - M);
+        den = fmaf(w, ml[r * BLOCK + c].y, den);
+        ml[r * BLOCK + c].x = w;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(FULL_MASK, den, o);
+      __syncwarp();
+      if (lane == 0) {
+        s_alpha[r] = ex2(before - M);
+        s_L[r] = fmaf(s_L[r], s_alpha[r], den);
+        s_M[r] = M;
       }
     }
     __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) acc[e] *= s_alpha[(tid + e * THREADS) / DV];
+    for (int c = 0; c < n; c += U) {
+      if (c > 0) fetch(c);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < EPT; ++e)
+          if (c + u < n) acc[e] = fmaf(ml[(tid + e * THREADS) / DV * BLOCK + c + u].x, v[u][e], acc[e]);
+    }
   }
 #pragma unroll
   for (int e = 0; e < EPT; ++e) {
