@@ -38,9 +38,9 @@ __device__ __forceinline__ int sequence_of(const int32_t* start, int B, int t, i
 
 // ALIGNED: the rotated range and its halves (quarters for 2D) are multiples of 8 dims.
 template <typename InT, typename OutT, int SW, bool ALIGNED, int TOK>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(THREADS, 4)
 append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
-  constexpr int AHEAD = sizeof(InT) == 2 ? 4 : 2;       // sets of a warp on their way
+  constexpr int AHEAD = 2;                              // sets of a warp on their way
   constexpr int RPW = 32 / SW;                          // q or K rows a warp holds
   constexpr int WPT = WARPS / TOK;                      // warps per token
   constexpr int LD = SW * 8 + (RPW > 1 ? SW : 0);       // the rows of a warp start in different banks
