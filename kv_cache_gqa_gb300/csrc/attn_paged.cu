@@ -98,8 +98,10 @@ cudaError_t launch_attn_paged(const PagedArgs& args, int Dk, int Dv, kva_dtype d
   a.rows_lo = 0;
   a.rows_hi = INT32_MAX;
   if (dtype == KVA_F32) {
+    int rows = 0;
+    for (int b = 0; b < a.B; ++b) rows = std::max(rows, std::min(start[b + 1] - start[b], PAGED_ROWS) * G);
     const Load w = load_of(a, lengths, start, 0, INT32_MAX, PAGED_ROWS, 128);
-    e = launch_attn_paged_simt(a, Dk, dtype, runs_of(w, PAGED_SMS * 3), s);
+    e = launch_attn_paged_simt(a, Dk, rows, runs_of(w, PAGED_SMS * (Dk == 64 ? 2 : 1)), s);
     if (e == cudaSuccess) ++*n_launches;
     return e;
   }

@@ -1,10 +1,12 @@
 // Attention of new tokens over a paged cache on the CUDA cores (kv_attn_paged).
 //
-// A unit is 16 query rows (token, head of the group) of one KV head; a step is 128 slots, 32 for each of
+// A unit is ROWS (8 or 16) query rows (token, head of the group) of one KV head; a step is 128 slots, 32 for each of
 // the CTA's four warps, which keep their own running maximum, sum and output and join them at the unit's
-// end (paged.cuh).  A lane takes one key's scores against all rows (its K row from global memory, q rows
-// broadcast from shared memory), the weights go through shared memory, and then a lane takes DV/32 columns of
-// the output for all rows.  The reference maximum moves only when a score exceeds it by 2^8.
+// end (paged.cuh).  Each lane has the K row and the V row of its slot copied into the warp's shared memory (one bulk copy
+// each, whatever page the slot is in); K of the next 32 slots is on its way during the weights' product, V during the
+// scores.  A lane takes one key's scores against all rows (q rows broadcast from shared memory), the weights go
+// through shared memory, and then a lane takes DV/32 columns of the output for all rows.  The reference maximum moves only
+// when a score exceeds it by 2^8.
 //
 // Method: one pass over the keys with the running maximum and sum of the softmax; the visible prefix of a
 // token as in the decode and verify steps (Youtu-VL-4B ncnn port, step 8; HunyuanOCR v1.5 ncnn port, section
@@ -20,47 +22,39 @@ using paged::ex2;
 using paged::M_NONE;
 using paged::Place;
 
-constexpr int WARPS = 4, THREADS = WARPS * 32, R = 16, KT = 32;
-static_assert(R == PAGED_ROWS, "partial results");
+constexpr int WARPS = 4, THREADS = WARPS * 32, KT = 32;
 constexpr float RESCALE_LOG2 = 8.0f;
 
-template <int N> struct Cols { float v[N]; };
-template <typename T, int N>
-__device__ __forceinline__ Cols<N> load_cols(const T* p) {
-  Cols<N> c;
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (N == 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-      c.v[0] = x.x; c.v[1] = x.y; c.v[2] = x.z; c.v[3] = x.w;
-    } else {
-      const float2 x = __ldg(reinterpret_cast<const float2*>(p));
-      c.v[0] = x.x; c.v[1] = x.y;
-    }
-  } else {
-    if constexpr (N == 4) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-      c.v[0] = bf16_lo(x.x); c.v[1] = bf16_hi(x.x); c.v[2] = bf16_lo(x.y); c.v[3] = bf16_hi(x.y);
-    } else {
-      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p));
-      c.v[0] = bf16_lo(x); c.v[1] = bf16_hi(x);
-    }
-  }
-  return c;
-}
-
-template <int DK, int DV>
+template <int DK, int DV, int ROWS>
 struct Smem {
-  static constexpr int Q = R * DK, P = WARPS * KT * R, O = WARPS * R * DV, ML = 2 * WARPS * R;
-  static constexpr int BYTES = 4 * (Q + P > ML + O ? Q + P : ML + O);
+  static constexpr int LDK = DK + 4;              // floats of a K row: lanes that read a row each meet different banks
+  static constexpr int K = KT * LDK, V = KT * DV; // of a warp
+  static constexpr int TILES = WARPS * (K + V);
+  static constexpr int Q = ROWS * DK, P = WARPS * KT * ROWS, ML = 2 * WARPS * ROWS, O = WARPS * ROWS * DV;
+  static constexpr int REST = 4 * (Q + P > ML + O ? Q + P : ML + O);       // the join reuses q and the weights
+  static constexpr int BYTES = 4 * TILES + REST;
 };
 
-template <typename T, int DK, int DV>
+template <int DK, int DV, int ROWS>
 __global__ void __launch_bounds__(THREADS)
 attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int NC = DV / 32;
-  extern __shared__ __align__(16) float sm[];
+  using S = Smem<DK, DV, ROWS>;
+  constexpr int NC = DV / 32, R = ROWS;
+  extern __shared__ __align__(16) float smem[];
   __shared__ int64_t scratch[WARPS + 4];
+  __shared__ uint64_t s_bar[WARPS][2];            // a warp's K and V have landed
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* tile_k = smem + warp * (S::K + S::V);
+  float* tile_v = tile_k + S::K;
+  float* sm = smem + S::TILES;
+  float* sm_q = sm;
+  float* sm_p = sm + S::Q + warp * KT * R;
+  uint64_t* bar = s_bar[warp];
+  if (lane == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    fence_mbar_init();
+  }
   const Cut cut{R, KT * WARPS, a.Hq / a.Hkv, a.rows_lo, a.rows_hi};
   const int G = cut.G, page_mask = (1 << a.page_shift) - 1;
   griddep_wait();                               // inputs of this launch are complete from here on
@@ -68,69 +62,97 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   Place p;
   const paged::Run run = paged::first_place<THREADS>(a, cut, scratch, &p);
   if (run.x0 >= run.x1) return;
-  float* sm_q = sm;
-  float* sm_p = sm + R * DK + warp * KT * R;
+  uint32_t phase = 0;
+  bool ok = true;                               // no wait of this warp has given up
 
   for (; p.b < a.B && p.at < run.x1; p.next(a, cut)) {
     const int st0 = (int)max((int64_t)0, run.x0 - p.at), st1 = (int)min((int64_t)p.n_steps, run.x1 - p.at);
-    const int64_t rows = (int64_t)p.s.T * G;
-    __syncthreads();                            // the unit before is done with the shared memory
-    for (int i = tid; i < R * DK; i += THREADS) {
-      const int64_t row = (int64_t)p.rt * R + i / DK;
-      float x = 0.f;
-      if (row < rows)
-        x = load1(reinterpret_cast<const T*>(a.q) + ((p.s.t0 + row / G) * a.Hq + p.g * G + row % G) * DK + i % DK) *
-            a.scale_log2;
-      sm_q[i] = x;
+    const int rows = p.s.T * G;                 // the call's rows fit 32 bits
+    const int lim_all = cut.visible(p.s, p.rt); // slots that the tile's last row sees
+    const int32_t* pages = a.table + (int64_t)p.b * a.table_stride;
+    const int first = (st0 * WARPS + warp) * KT;                  // first key of this warp's first tile
+    const int n_mine = !ok ? 0 : max(0, min(st1 - st0, (lim_all - first + KT * WARPS - 1) / (KT * WARPS)));
+    // this lane's slot of tile u: its rows in K and V, -1 for none; a page outside the pool makes its scores NaN
+    int64_t at_k = -1, at_v = -1;
+    bool bad = false;
+    auto look_up = [&](int u) {
+      const int key = first + u * (KT * WARPS) + lane;
+      at_k = at_v = -1;
+      bad = false;
+      if (u >= n_mine || key >= lim_all) return;
+      const int page = pages[key >> a.page_shift];
+      bad = (unsigned)page >= (unsigned)a.n_pages;
+      const int64_t pg = bad ? 0 : page;
+      const int in = (p.g << a.page_shift) + (key & page_mask);
+      at_k = pg * a.page_stride + (int64_t)in * DK;
+      at_v = pg * a.page_stride_v + (int64_t)in * DV;
+    };
+    auto copy_k = [&]() {                       // whole warp
+      const int n = __popc(__ballot_sync(FULL_MASK, at_k >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&bar[0], n * DK * 4);
+      __syncwarp();
+      if (at_k >= 0) bulk_g2s(tile_k + lane * S::LDK, reinterpret_cast<const float*>(a.k) + at_k, DK * 4, &bar[0]);
+    };
+    auto copy_v = [&]() {
+      const int n = __popc(__ballot_sync(FULL_MASK, at_v >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&bar[1], n * DV * 4);
+      __syncwarp();
+      if (at_v >= 0) bulk_g2s(tile_v + lane * DV, reinterpret_cast<const float*>(a.v) + at_v, DV * 4, &bar[1]);
+    };
+    look_up(0);
+    if (n_mine > 0) { copy_k(); copy_v(); }
+    __syncthreads();                            // the unit before is done with q's place
+    for (int i = tid; i < R * DK / 4; i += THREADS) {
+      const int row = p.rt * R + i / (DK / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < rows) {
+        x = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) +
+                                                  ((int64_t)(p.s.t0 + row / G) * a.Hq + p.g * G + row % G) * DK) + i % (DK / 4));
+        x.x *= a.scale_log2; x.y *= a.scale_log2; x.z *= a.scale_log2; x.w *= a.scale_log2;
+      }
+      reinterpret_cast<float4*>(sm_q)[i] = x;
     }
     __syncthreads();
     float m[R], l[R], o[R][NC];
     int lim[R];                                 // slots that row r sees
-    int lim_all = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = M_NONE;
       l[r] = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[r][c] = 0.f;
-      const int64_t row = (int64_t)p.rt * R + r;
-      lim[r] = row < rows ? min(max(p.s.L - p.s.T + (int)(row / G) + 1, 0), p.s.L) : 0;
-      lim_all = max(lim_all, lim[r]);
+      const int row = p.rt * R + r;
+      lim[r] = row < rows ? min(max(p.s.L - p.s.T + row / G + 1, 0), p.s.L) : 0;
     }
-    const int32_t* pages = a.table + (int64_t)p.b * a.table_stride;
-    for (int st = st0; st < st1; ++st) {
-      const int ks = (st * WARPS + warp) * KT;
-      if (ks >= lim_all) break;
-      const int key = ks + lane;
-      bool bad = false;
-      int64_t at = 0, atv = 0;                  // the key's rows in K and V
-      if (key < lim_all) {
-        const int page = pages[key >> a.page_shift];
-        bad = (unsigned)page >= (unsigned)a.n_pages;
-        const int64_t pg = bad ? 0 : page;
-        const int in = (p.g << a.page_shift) + (key & page_mask);
-        at = pg * a.page_stride + (int64_t)in * DK;
-        atv = pg * a.page_stride_v + (int64_t)in * DV;
+    for (int u = 0; u < n_mine; ++u) {
+      const int ks = first + u * (KT * WARPS), key = ks + lane;
+      const bool wrong = bad;                   // of this tile's slot
+      if (!paged::warp_wait(&bar[0], phase)) {
+        ok = false;                             // gave up: the copy of V lands first (bounded)
+        (void)paged::warp_wait(&bar[1], phase);
+        break;
       }
       float s[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) s[r] = 0.f;
-      if (key < lim_all) {
-        const T* kp = reinterpret_cast<const T*>(a.k) + at;
 #pragma unroll 4
-        for (int d = 0; d < DK; d += 4) {
-          const Cols<4> kk = load_cols<T, 4>(kp + d);
+      for (int d = 0; d < DK; d += 4) {
+        const float4 kk = *reinterpret_cast<const float4*>(tile_k + lane * S::LDK + d);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float4 qv = *reinterpret_cast<const float4*>(sm_q + r * DK + d);
-            s[r] = fmaf(qv.x, kk.v[0], fmaf(qv.y, kk.v[1], fmaf(qv.z, kk.v[2], fmaf(qv.w, kk.v[3], s[r]))));
-          }
+        for (int r = 0; r < R; ++r) {
+          const float4 qv = *reinterpret_cast<const float4*>(sm_q + r * DK + d);
+          s[r] = fmaf(qv.x, kk.x, fmaf(qv.y, kk.y, fmaf(qv.z, kk.z, fmaf(qv.w, kk.w, s[r]))));
         }
+      }
+      __syncwarp();                             // K is read
+      if (u + 1 < n_mine) {
+        look_up(u + 1);
+        copy_k();
       }
       bool grow = false;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (bad) s[r] = NAN;
+        if (wrong) s[r] = NAN;
         if (key >= lim[r]) s[r] = -INFINITY;
         grow |= s[r] > m[r] + RESCALE_LOG2;
       }
@@ -158,24 +180,37 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
       for (int r = 0; r < R; r += 4)
         *reinterpret_cast<float4*>(sm_p + lane * R + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
       __syncwarp();
+      if (!paged::warp_wait(&bar[1], phase)) {
+        ok = false;                             // gave up: the next copy of K lands first (bounded)
+        if (u + 1 < n_mine) (void)paged::warp_wait(&bar[0], phase ^ 1);
+        break;
+      }
       const int n = min(KT, lim_all - ks);
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
-        const int64_t vj = __shfl_sync(FULL_MASK, atv, j);
-        const Cols<NC> vv = load_cols<T, NC>(reinterpret_cast<const T*>(a.v) + vj + lane * NC);
+        float vv[NC];
+        if constexpr (NC == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(tile_v + j * DV + lane * 4);
+          vv[0] = x.x; vv[1] = x.y; vv[2] = x.z; vv[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(tile_v + j * DV + lane * 2);
+          vv[0] = x.x; vv[1] = x.y;
+        }
 #pragma unroll
         for (int r = 0; r < R; r += 4) {
           const float4 w = *reinterpret_cast<const float4*>(sm_p + j * R + r);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            o[r][c] = fmaf(w.x, vv.v[c], o[r][c]);
-            o[r + 1][c] = fmaf(w.y, vv.v[c], o[r + 1][c]);
-            o[r + 2][c] = fmaf(w.z, vv.v[c], o[r + 2][c]);
-            o[r + 3][c] = fmaf(w.w, vv.v[c], o[r + 3][c]);
+            o[r][c] = fmaf(w.x, vv[c], o[r][c]);
+            o[r + 1][c] = fmaf(w.y, vv[c], o[r + 1][c]);
+            o[r + 2][c] = fmaf(w.z, vv[c], o[r + 2][c]);
+            o[r + 3][c] = fmaf(w.w, vv[c], o[r + 3][c]);
           }
         }
       }
-      __syncwarp();
+      __syncwarp();                             // V and the weights are read
+      if (u + 1 < n_mine) copy_v();
+      phase ^= 1;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -187,37 +222,37 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
     float* sm_o = sm + 2 * WARPS * R + warp * R * DV;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (lane == 0) { sm_m[warp * R + r] = m[r]; sm_l[warp * R + r] = l[r]; }
+      if (lane == 0) { sm_m[warp * R + r] = m[r]; sm_l[warp * R + r] = ok ? l[r] : NAN; }
 #pragma unroll
       for (int c = 0; c < NC; ++c) sm_o[r * DV + lane * NC + c] = o[r][c];
     }
-    paged::finish_unit<R, DV, WARPS, Smem<DK, DV>::BYTES>(a, cut, p, run, st0, st1, sm);
+    paged::finish_unit<R, DV, WARPS, S::REST>(a, cut, p, run, st0, st1, sm);
   }
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV, int ROWS>
 cudaError_t launch_t(const PagedArgs& a, int runs, cudaStream_t s) {
-  constexpr int smem = Smem<DK, DV>::BYTES;
+  constexpr int smem = Smem<DK, DV, ROWS>::BYTES;
   static DeviceOnce configured;
   if (!configured.done()) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_paged_simt_kernel<T, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_paged_simt_kernel<DK, DV, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured.mark();
   }
-  return launch_pdl(attn_paged_simt_kernel<T, DK, DV>, dim3(runs), dim3(THREADS), (size_t)smem, s, a);
+  return launch_pdl(attn_paged_simt_kernel<DK, DV, ROWS>, dim3(runs), dim3(THREADS), (size_t)smem, s, a);
 }
 
-template <typename T>
-cudaError_t launch_d(const PagedArgs& a, int Dk, int runs, cudaStream_t s) {
-  if (Dk == 64) return launch_t<T, 64, 64>(a, runs, s);
-  if (Dk == 128) return launch_t<T, 128, 128>(a, runs, s);
-  return launch_t<T, 192, 128>(a, runs, s);
+template <int DK, int DV>
+cudaError_t launch_d(const PagedArgs& a, int rows, int runs, cudaStream_t s) {
+  return rows <= 8 ? launch_t<DK, DV, 8>(a, runs, s) : launch_t<DK, DV, 16>(a, runs, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, kva_dtype dtype, int runs, cudaStream_t s) {
-  return dtype == KVA_F32 ? launch_d<float>(a, Dk, runs, s) : launch_d<bf16_t>(a, Dk, runs, s);
+cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, int rows, int runs, cudaStream_t s) {
+  if (Dk == 64) return launch_d<64, 64>(a, rows, runs, s);
+  if (Dk == 128) return launch_d<128, 128>(a, rows, runs, s);
+  return launch_d<192, 128>(a, rows, runs, s);
 }
 
 }  // namespace kva

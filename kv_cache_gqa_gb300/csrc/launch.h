@@ -317,7 +317,7 @@ cudaError_t launch_attn_paged_step(const PagedArgs& a, int Dk, int rows, int run
 cudaError_t paged_query_map(CUtensorMap* map, const PagedArgs& a, int width, int heads, int tokens);
 cudaError_t launch_attn_paged_chunk(const PagedArgs& a, int Dk, int Dv, int runs, cudaStream_t s, unsigned* n_launches);
 void attn_paged_chunk_load(int T, int L, int G, int64_t* steps, int64_t* units);
-cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, kva_dtype dtype, int runs, cudaStream_t s);
+cudaError_t launch_attn_paged_simt(const PagedArgs& a, int Dk, int rows, int runs, cudaStream_t s);
 
 struct AppendPagedArgs {
   const void* q;                      // [T, Hq, Dk], tokens q_stride elements apart (Hq = 0: no queries)
