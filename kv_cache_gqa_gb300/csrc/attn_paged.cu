@@ -43,11 +43,12 @@ Load load_of(const PagedArgs& a, const int32_t* lengths, const int32_t* start, i
   return w;
 }
 
-// As many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps.  A whole number of
+// As many runs as the GPU holds at once, and not so many that joining a unit's parts costs more than its steps: `worth` is the
+// square root of a step's time over a part's, doubled (one sequence of 768 slots in float32: 2 gives 18.9 us, 4 14.6).  A whole number of
 // runs a unit, where there are four of them or more: units of equal length (one sequence's heads) then begin with a run each
 // (one sequence of 768 slots: 13.0 us, so 10.5).
-int runs_of(const Load& w, int slots) {
-  const int64_t most = std::min<int64_t>(slots, (int64_t)(2.0 * std::sqrt((double)w.steps * (double)w.units)));
+int runs_of(const Load& w, int slots, double worth = 2.0) {
+  const int64_t most = std::min<int64_t>(slots, (int64_t)(worth * std::sqrt((double)w.steps * (double)w.units)));
   const int64_t runs = std::max<int64_t>(1, std::min(most, w.steps));
   return (int)(runs >= 4 * w.units ? runs / w.units * w.units : runs);
 }
@@ -101,7 +102,7 @@ cudaError_t launch_attn_paged(const PagedArgs& args, int Dk, int Dv, kva_dtype d
     int rows = 0;
     for (int b = 0; b < a.B; ++b) rows = std::max(rows, std::min(start[b + 1] - start[b], PAGED_ROWS) * G);
     const Load w = load_of(a, lengths, start, 0, INT32_MAX, PAGED_ROWS, 128);
-    e = launch_attn_paged_simt(a, Dk, rows, runs_of(w, PAGED_SMS * (Dk == 64 ? 2 : 1)), s);
+    e = launch_attn_paged_simt(a, Dk, rows, runs_of(w, PAGED_SMS * (Dk == 64 ? 2 : 1), 4.0), s);
     if (e == cudaSuccess) ++*n_launches;
     return e;
   }

@@ -8,6 +8,11 @@
 // through shared memory, and then a lane takes DV/32 columns of the output for all rows.  The reference maximum moves only
 // when a score exceeds it by 2^8.
 //
+// Bound: long chunks by shared-memory reads (each key's q values, 16 rows of them, beside 64 multiply-adds per 4 dims): 512
+// tokens behind 1536 slots at 16/8 heads of 128 take 368 us (14 TFLOP/s; lanes that read K and V from global
+// memory themselves took 530).  Small batches by latency: one 768-slot sequence 14.6 us (34 so), seven ragged sequences
+// 21 us (25 so).  64 single tokens over 500 to 4000 slots: 350 us, 3.6 TB/s, a tile of K and V at a time on its way.
+//
 // Method: one pass over the keys with the running maximum and sum of the softmax; the visible prefix of a
 // token as in the decode and verify steps (Youtu-VL-4B ncnn port, step 8; HunyuanOCR v1.5 ncnn port, section
 // 3.8).  The reference keeps fixed windows; a cache in pages has no counterpart there.
@@ -186,7 +191,7 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
         break;
       }
       const int n = min(KT, lim_all - ks);
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < n; ++j) {
         float vv[NC];
         if constexpr (NC == 4) {
