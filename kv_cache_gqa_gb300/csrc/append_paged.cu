@@ -7,6 +7,10 @@
 // sines and norm weights of its dims stay in registers.  The token's sequence is found by a search of 32 probes
 // at a time in token_start, its slot is L - T + i, and the table names the page; the rows' loads go out first.
 //
+// Bound: long appends by HBM in principle (24 chunks of 64 to 1024 tokens, 16/8 heads of 128, 149 MB: 47 us, 3.2 TB/s), in fact by
+// the instructions and the latency of a row (load, sum over its lanes, turn through shared memory) at 32 warps an SM.  There: 3 / 4 /
+// 5 / 6 CTAs an SM 53 / 47 / 59 / 67 us; 2 / 3 / 4 / 6 sets ahead 47 / 49 / 50 / 57; a CTA a token 83.  64 tokens: latency (4.5 us).
+//
 // Method: the append of the decode step (Youtu-VL-4B ncnn port, step 6) with per-head RMSNorm and rotate-half
 // RoPE (Penguin-VL ncnn port, sections 2.1 and 4.2; Youtu-VL-4B ncnn port, implementation difficulty 2).
 // The reference has no cache in pages and no scaled positions.

@@ -12,6 +12,10 @@
 // carries 16 bits at no cost.  EXACT (a float32 output) adds a third part, 24 bits, and keeps the tensor core's sums to one
 // tile, joined by float32 additions: it cuts sums off towards zero, which over a long run would show (7e-6).
 //
+// Bound: many long sequences by HBM (64 of 1k to 32k slots at 16/8 heads of 128: 637 us, 6.9 TB/s; 64 of 500 to 4000: 101 us, 5.9
+// TB/s; head dims 192/128 with float32 out: 142 us, 5.9 TB/s, its third part and short sums beside the loads); one sequence
+// by latency (768 slots 10 us, 8192 16 us: the plan, a table read, one ring's loads, the join of the parts).
+//
 // Method: one pass over the keys with the running maximum and sum of the softmax; GQA by repeat-interleave
 // grouping (Penguin-VL ncnn port, section 3), the visible prefix of decode and verify steps (Youtu-VL-4B ncnn
 // port, step 8; HunyuanOCR v1.5 ncnn port, section 3.8), bf16 storage with fp32 accumulation (section 3.7 there).
