@@ -40,8 +40,30 @@ __device__ __forceinline__ int sequence_of(const int32_t* start, int B, int t, i
   return lo;
 }
 
-// ALIGNED: the rotated range and its halves (quarters for 2D) are multiples of 8 dims.
-template <typename InT, typename OutT, int SW, bool ALIGNED, int TOK>
+// How a row's rotated pairs (d, d + half) lie in the lanes.  PAIRED: the whole row turns as one block, and a lane holds 4 dims
+// of each half, so pairs meet in its registers.  ALIGNED: the rotated range and its halves (quarters for 2D) are multiples of
+// 8 dims, the lane's 8 partners a piece of the row's copy in shared memory.  GENERAL: partners one by one.
+enum Turn { GENERAL, ALIGNED, PAIRED };
+
+// 4 elements at p and 4 at p + gap
+__device__ __forceinline__ void load_halves(Raw8<float>& x, const float* p, int gap) {
+  x.a = __ldg(reinterpret_cast<const float4*>(p));
+  x.b = __ldg(reinterpret_cast<const float4*>(p + gap));
+}
+__device__ __forceinline__ void load_halves(Raw8<bf16_t>& x, const bf16_t* p, int gap) {
+  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p)), hi = __ldg(reinterpret_cast<const uint2*>(p + gap));
+  x.a = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store_halves(float* p, int gap, const float (&y)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<float4*>(p + gap) = make_float4(y[4], y[5], y[6], y[7]);
+}
+__device__ __forceinline__ void store_halves(bf16_t* p, int gap, const float (&y)[8]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  *reinterpret_cast<uint2*>(p + gap) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+}
+
+template <typename InT, typename OutT, int SW, Turn TURN, int TOK>
 __global__ void __launch_bounds__(THREADS, 4)
 append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   constexpr int AHEAD = 2;                              // sets of a warp on their way
@@ -50,10 +72,10 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   constexpr int LD = SW * 8 + (RPW > 1 ? SW : 0);       // the rows of a warp start in different banks
   __shared__ __align__(16) float s_cos[TOK][MAX_ROPE_FREQ];
   __shared__ __align__(16) float s_sin[TOK][MAX_ROPE_FREQ];
-  __shared__ __align__(16) float s_row[WARPS][RPW][LD];
+  __shared__ __align__(16) float s_row[TURN == PAIRED ? 1 : WARPS][RPW][LD];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int sub = lane / SW, sl = lane % SW, e0 = sl * 8;
+  const int sub = lane / SW, sl = lane % SW, e0 = TURN == PAIRED ? sl * 4 : sl * 8;   // the lane's first dim
   const int tl = warp / WPT, t0 = blockIdx.x * TOK, t = t0 + tl;
   const int Dk = a.Dk, Dv = a.Dv, Hkv = a.Hkv, Hq = a.Hq;
   const int ro = a.rot_offset, rw = a.rot_dim, half = rw / 2, kind_r = a.rope.kind;
@@ -67,7 +89,7 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   const int sets_q = (Hq + RPW - 1) / RPW, sets_k = (Hkv + RPW - 1) / RPW, sets_v = (pieces + 31) / 32;
   auto units = [&](int kind) { return kind == 0 ? Hq : (kind == 1 ? Hkv : pieces); };
   auto sets = [&](int kind) { return kind == 0 ? sets_q : (kind == 1 ? sets_k : sets_v); };
-  const bool in_row = e0 < Dk;
+  const bool in_row = sl * 8 < Dk;
   // the walk that loads: kind, set, and this lane's unit and address in it
   struct Walk { int kind, set, unit; const InT* p; };
   auto enter = [&](Walk& w, int set) {          // the first set >= start of the walk's kind, or of a later one
@@ -85,7 +107,10 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   auto fetch = [&](Walk& w, Raw8<InT>& x) {      // the walk's set, then on to the next
     x.zero();
     if (w.kind > 2) return;
-    if (w.unit < units(w.kind) && (w.kind == 2 || in_row)) x.load(w.p);
+    if (w.unit < units(w.kind) && (w.kind == 2 || in_row)) {
+      if (TURN == PAIRED && w.kind < 2) load_halves(x, w.p, Dk / 2);
+      else x.load(w.p);
+    }
     w.set += step;
     if (w.set < sets(w.kind)) {
       const int by = step * (w.kind == 2 ? 32 : RPW);
@@ -135,7 +160,13 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   bool low = true;
   int partner = 0;
   uint64_t cs[4] = {}, sn[4] = {};
-  if (ALIGNED && turns) {
+  if (TURN == PAIRED && rotate && in_row) {
+    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_cos[tl][e0]), v = *reinterpret_cast<const ulonglong2*>(&s_sin[tl][e0]);
+    cs[0] = c.x; cs[1] = c.y;
+    sn[0] = v.x; sn[1] = v.y;
+    sn[2] = v.x ^ 0x8000000080000000ull; sn[3] = v.y ^ 0x8000000080000000ull;
+  }
+  if (TURN == ALIGNED && turns) {
     const int bi = d0 >= block ? 1 : 0, d = d0 - bi * block;
     low = d < hb;
     const int j0 = bi * hb + (low ? d : d - hb);
@@ -147,7 +178,7 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
       for (int i = 0; i < 4; ++i) sn[i] ^= 0x8000000080000000ull;
     }
   }
-  float* row = s_row[warp][sub];
+  float* row = s_row[TURN == PAIRED ? 0 : warp][sub];
   const float inv_d = 1.0f / (float)Dk;
   uint64_t x[4] = {}, wv[4] = {};
   auto mirror = [&]() {
@@ -168,8 +199,17 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
     for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(mul_f32x2(x[i], r2), wv[i]);
   };
   auto turn = [&]() {
+    if constexpr (TURN == PAIRED) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t lo = x[i], hi = x[2 + i];
+        x[i] = sum_of_products(lo, cs[i], hi, sn[2 + i]);
+        x[2 + i] = sum_of_products(hi, cs[i], lo, sn[i]);
+      }
+      return;
+    }
     mirror();
-    if constexpr (ALIGNED) {
+    if constexpr (TURN == ALIGNED) {
       if (turns) {
         if (kind_r == KVA_ROPE_INTERLEAVED) {           // inputs 2 j0 .. 2 j0 + 15 are 8 pairs
           uint64_t q[8];
@@ -221,7 +261,9 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
     const int per = qk ? RPW : 32;
     if (norm && qk && in_row && set < sets(kind)) {
       Raw8<float> w;
-      w.load((kind ? a.k_w : a.q_w) + e0);
+      const float* from = (kind ? a.k_w : a.q_w) + e0;
+      if constexpr (TURN == PAIRED) load_halves(w, from, Dk / 2);
+      else w.load(from);
       w.pairs(wv);
     }
     int unit = set * per + (qk ? sub : lane);
@@ -240,10 +282,14 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
       float y[8];
       unpack_pairs(x, y);
       if (kind == 0) {
-        store8(reinterpret_cast<OutT*>(a.q_out) + ((int64_t)t * Hq + unit) * Dk + e0, y);
+        OutT* to = reinterpret_cast<OutT*>(a.q_out) + ((int64_t)t * Hq + unit) * Dk + e0;
+        if constexpr (TURN == PAIRED) store_halves(to, Dk / 2, y);
+        else store8(to, y);
       } else if (at_k >= 0) {
         if (kind == 1) {
-          store8(reinterpret_cast<OutT*>(a.kc) + at_k + ((int64_t)unit << a.page_shift) * Dk + e0, y);
+          OutT* to = reinterpret_cast<OutT*>(a.kc) + at_k + ((int64_t)unit << a.page_shift) * Dk + e0;
+          if constexpr (TURN == PAIRED) store_halves(to, Dk / 2, y);
+          else store8(to, y);
         } else {
           const int head = unit / (Dv / 8), d = (unit - head * (Dv / 8)) * 8;
           store8(reinterpret_cast<OutT*>(a.vc) + at_v + ((int64_t)head << a.page_shift) * Dv + d, y);
@@ -257,7 +303,7 @@ append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
 
 constexpr int SMS = 152;          // grids are sized for the whole GPU; fewer SMs only take longer
 
-template <typename InT, typename OutT, bool ALIGNED, int TOK>
+template <typename InT, typename OutT, Turn TURN, int TOK>
 cudaError_t launch_t(const AppendPagedArgs& a, cudaStream_t s) {
   const int D = a.Dk, rpw = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
   const int64_t sets = (a.Hq + rpw - 1) / rpw + (int64_t)((a.Hkv + rpw - 1) / rpw) + ((int64_t)a.Hkv * a.Dv + 255) / 256;
@@ -265,21 +311,23 @@ cudaError_t launch_t(const AppendPagedArgs& a, cudaStream_t s) {
   const int64_t ctas = (a.T + TOK - 1) / TOK, most = (sets + WARPS / TOK - 1) / (WARPS / TOK);
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(most, 2 * SMS / ctas));
   const dim3 grid((unsigned)ctas, 1, groups);
-  if (D <= 64) return launch_pdl(append_paged_kernel<InT, OutT, 8, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
-  if (D <= 128) return launch_pdl(append_paged_kernel<InT, OutT, 16, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
-  return launch_pdl(append_paged_kernel<InT, OutT, 32, ALIGNED, TOK>, grid, dim3(THREADS), 0, s, a);
+  if (D <= 64) return launch_pdl(append_paged_kernel<InT, OutT, 8, TURN, TOK>, grid, dim3(THREADS), 0, s, a);
+  if (D <= 128) return launch_pdl(append_paged_kernel<InT, OutT, 16, TURN, TOK>, grid, dim3(THREADS), 0, s, a);
+  return launch_pdl(append_paged_kernel<InT, OutT, 32, TURN, TOK>, grid, dim3(THREADS), 0, s, a);
 }
 
 // A token per warp once that leaves four CTAs per SM.
-template <typename InT, typename OutT, bool ALIGNED>
+template <typename InT, typename OutT, Turn TURN>
 cudaError_t launch_w(const AppendPagedArgs& a, cudaStream_t s) {
-  return a.T >= 4 * TOKENS * SMS ? launch_t<InT, OutT, ALIGNED, TOKENS>(a, s) : launch_t<InT, OutT, ALIGNED, 1>(a, s);
+  return a.T >= 4 * TOKENS * SMS ? launch_t<InT, OutT, TURN, TOKENS>(a, s) : launch_t<InT, OutT, TURN, 1>(a, s);
 }
 
 template <typename InT, typename OutT>
 cudaError_t launch_a(const AppendPagedArgs& a, cudaStream_t s) {
+  const bool one_block = a.rope.kind != KVA_ROPE_2D && a.rope.kind != KVA_ROPE_INTERLEAVED;
+  if (one_block && a.rot_offset == 0 && a.rot_dim == a.Dk) return launch_w<InT, OutT, PAIRED>(a, s);
   const int unit = a.rope.kind == KVA_ROPE_2D ? 32 : 16;
-  return a.rot_offset % 8 == 0 && a.rot_dim % unit == 0 ? launch_w<InT, OutT, true>(a, s) : launch_w<InT, OutT, false>(a, s);
+  return a.rot_offset % 8 == 0 && a.rot_dim % unit == 0 ? launch_w<InT, OutT, ALIGNED>(a, s) : launch_w<InT, OutT, GENERAL>(a, s);
 }
 
 }  // namespace
