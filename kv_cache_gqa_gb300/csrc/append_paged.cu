@@ -2,14 +2,15 @@
 //
 // A CTA takes one token (few tokens: a part of its rows) or eight, a warp each (long appends), whose angles its
 // threads evaluate once.  A q or K row of D values belongs to SW lanes of a warp (SW = 8, 16 or 32 for rows up
-// to 64, 128 or 256 wide), 8 consecutive values a lane; V, which is only copied, goes 256 values a warp whatever the
-// row's width.  A warp walks its q, K and V sets in order with AHEAD of them on their way; the cosines,
+// to 64, 128 or 256 wide), 8 values a lane: 4 of each half where the whole row turns as one block, else 8 in a row.  V, which is
+// only copied, goes 256 values a warp whatever the row's width.  A warp walks its q, K and V sets in order with AHEAD of them on their way; the cosines,
 // sines and norm weights of its dims stay in registers.  The token's sequence is found by a search of 32 probes
 // at a time in token_start, its slot is L - T + i, and the table names the page; the rows' loads go out first.
 //
-// Bound: long appends by HBM in principle (24 chunks of 64 to 1024 tokens, 16/8 heads of 128, 149 MB: 47 us, 3.2 TB/s), in fact by
-// the instructions and the latency of a row (load, sum over its lanes, turn through shared memory) at 32 warps an SM.  There: 3 / 4 /
-// 5 / 6 CTAs an SM 53 / 47 / 59 / 67 us; 2 / 3 / 4 / 6 sets ahead 47 / 49 / 50 / 57; a CTA a token 83.  64 tokens: latency (4.5 us).
+// Bound: long appends by HBM in principle (24 chunks of 64 to 1024 tokens, 16/8 heads of 128, 149 MB: 45 us, 3.3 TB/s), in fact by
+// the instructions and the latency of a row (load, sum over its lanes, turn) at 32 warps an SM, and by a last round of CTAs that
+// is two thirds full.  There: 3 / 4 / 5 CTAs an SM 51 / 45 / 45 us, with the turn through shared memory 53 / 47 / 59 (and 2 / 3 /
+// 4 / 6 sets ahead 47 / 49 / 50 / 57; a CTA a token 83).  64 tokens: latency (4.5 us).
 //
 // Method: the append of the decode step (Youtu-VL-4B ncnn port, step 6) with per-head RMSNorm and rotate-half
 // RoPE (Penguin-VL ncnn port, sections 2.1 and 4.2; Youtu-VL-4B ncnn port, implementation difficulty 2).
