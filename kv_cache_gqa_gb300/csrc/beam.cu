@@ -10,10 +10,11 @@
 // (beams that are nearly even keep their order).
 // A beam that is done, or whose score is -infinity, is not read.
 //
-// Sums are float32 per thread and slice, 64 bits where they are joined.  Which thread takes an element depends on its index
-// alone, so equal rows give equal totals.  exp(x - m) is 2^(x log2 e - c), c = m log2 e rounded, with log2 e in two parts, and the sum is
-// put right for c's rounding at the end.  Slices hand over sums of 2^(x log2 e - k) with whole k, which join without an exponential:
-// 64-bit arithmetic is slow here (exp 2.6 us, log 1.2 us).
+// Sums are float32 per thread and slice, with what their additions round away where slices are joined.  Which thread takes an element
+// depends on its index alone, so equal rows give equal totals.  exp(x - m) is 2^((x - m) log2 e), the difference first: it is exact for
+// values near m whatever the size of both, so masked tokens at -1e10 or -1e30 are numbers like others (m log2 e, rounded before x log2 e
+// is taken from it, would be off by more than float32's exponents hold).  Slices hand over (maximum, sum).  Totals are 64-bit: the value
+// less the row's maximum, plus the score less the sum's logarithm (64-bit arithmetic is slow here: a logarithm takes 1.2 us).
 //
 // Bound: 32 x 8 beams over 151643 bf16 values by the reading's instructions and the slices' ends (31.5 us; 78 MB, 60% of them read, are
 // 7 us of HBM); one sequence's 4 beams over 151936 float32 values by latency (12.9 us: a slice's pass, its sort, the join).
@@ -155,8 +156,6 @@ __device__ __forceinline__ void warp_best(const float (&x)[PER], int i0, int n, 
 }
 
 constexpr int LIST = 1024;                       // candidates of a slice that are sorted at once
-constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;       // log2 e = HI + LO
-constexpr float HUGE_M = 1e30f;                  // beyond it m log2 e could overflow
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 4)
@@ -181,7 +180,7 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     const int batches = (a.V + BATCH - 1) / BATCH;
     const int b0 = (int)((int64_t)batches * split / gridDim.x), b1 = (int)((int64_t)batches * (split + 1) / gridDim.x);
     if (tid == 0) s_count = 0;
-    float m = LOW, c = 0.f, s = 0.f;               // s: sum of 2^(x log2 e - c), or of exp(x - m) where |m| >= HUGE_M
+    float m = LOW, s = 0.f;                        // the maximum, and the sum of exp(x - m)
     float best = -INFINITY, second = -INFINITY;    // of the batches' maxima
     int best_at = b0;
     Part next;
@@ -199,34 +198,26 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
         for (int e = 2; e < PER; e += 2) top = fmax3(top, x[e], x[e + 1]);
         high = fmaxf(high, top);
         if (top > m) {
-          const float to = top * L2E_HI;
-          s *= ex2(fabsf(m) < HUGE_M && fabsf(top) < HUGE_M ? c - to : (m - top) * L2E_HI);
+          s *= ex2((m - top) * LOG2E);
           m = top;
-          c = to;
         }
-        if (fabsf(m) < HUGE_M) {
-          const uint64_t hi2 = pack_f32x2(L2E_HI, L2E_HI), lo2 = pack_f32x2(L2E_LO, L2E_LO), c2 = pack_f32x2(-c, -c);
-          uint64_t sum = 0ull;
+        const uint64_t l2 = pack_f32x2(LOG2E, LOG2E), m2 = pack_f32x2(-m, -m);
+        uint64_t sum = 0ull;
 #pragma unroll
-          for (int e = 0; e < PER; e += 2) {
-            const uint64_t x2 = pack_f32x2(x[e], x[e + 1]), t = fma_f32x2(x2, lo2, fma_f32x2(x2, hi2, c2));
-            sum = add_f32x2(sum, pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t))));
-          }
-          s += f32x2_lo(sum) + f32x2_hi(sum);
-        } else {
-#pragma unroll
-          for (int e = 0; e < PER; ++e) s += ex2((x[e] - m) * L2E_HI);
+        for (int e = 0; e < PER; e += 2) {
+          const uint64_t t = mul_f32x2(add_f32x2(pack_f32x2(x[e], x[e + 1]), m2), l2);
+          sum = add_f32x2(sum, pack_f32x2(ex2(f32x2_lo(t)), ex2(f32x2_hi(t))));
         }
+        s += f32x2_lo(sum) + f32x2_hi(sum);
       }
       if (high > best) { second = best; best = high; best_at = bt; }
       else second = fmaxf(second, high);
     }
-    if (fabsf(m) < HUGE_M) s *= ex2(fmaf(-m, L2E_LO, fmaf(-m, L2E_HI, c)));    // now of exp(x - m)
     // the warp's sums, and its n-th best maximum of a thread
     float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-    s *= ex2((m - M) * L2E_HI);
+    s *= ex2((m - M) * LOG2E);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
     float ordered = best;
@@ -295,13 +286,9 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       if (lane == 0) {
         float CM = LOW, S = 0.f;
         for (int w = 0; w < WARPS; ++w) CM = fmaxf(CM, s_m[w]);
-        for (int w = 0; w < WARPS; ++w) S = fmaf(s_s[w], ex2((s_m[w] - CM) * L2E_HI), S);
-        // exp(CM) = 2^(CM log2 e): a whole power k, and the rest goes into the sum.  Huge values: the maximum as it is, and the
-        // sum with a minus.
-        const float k = rintf(CM * L2E_HI);
-        const bool plain = fabsf(CM) < HUGE_M;
-        a.part_stat[2 * part] = plain ? k : CM;
-        a.part_stat[2 * part + 1] = plain ? S * ex2(fmaf(CM, L2E_LO, fmaf(CM, L2E_HI, -k))) : -S;
+        for (int w = 0; w < WARPS; ++w) S = fmaf(s_s[w], ex2((s_m[w] - CM) * LOG2E), S);
+        a.part_stat[2 * part] = CM;
+        a.part_stat[2 * part + 1] = S;
       }
     }
   }
@@ -317,7 +304,8 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     const float sc = a.scores[r];
     const bool is_done = a.finished != nullptr && a.finished[r] != 0;
     Key list = 0, last = 0;
-    double base = NAN, top = 0.0;                    // an offer's total is (value - top) + base
+    double base = NAN;                               // an offer's total is (value - top) + base
+    float top = 0.f;
     if (is_done) {
       base = (double)sc;
       if (lane == 0) list = key_of(0.f, a.end_id);
@@ -334,21 +322,15 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
         }
       };
       fetch(0);
-      // the largest power of the slices, and the largest maximum of those of huge values, which count among themselves
-      float power = -INFINITY, huge = -INFINITY;
+      float M = -INFINITY;                           // the row's maximum
       bool odd = false;
       for (int i = lane; i < (int)gridDim.x; i += 32) {
         const float2 st = __ldcg(reinterpret_cast<const float2*>(a.part_stat) + part + i);
-        odd |= !(fabsf(st.y) < INFINITY);
-        if (st.y > 0.f) power = fmaxf(power, st.x);
-        if (st.y < 0.f) huge = fmaxf(huge, st.x);
+        odd |= !(st.y < INFINITY);
+        if (st.y > 0.f) M = fmaxf(M, st.x);          // a slice of -infinity alone has the sum 0
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        power = fmaxf(power, __shfl_xor_sync(FULL_MASK, power, o));
-        huge = fmaxf(huge, __shfl_xor_sync(FULL_MASK, huge, o));
-      }
-      const bool plain = !(huge > 0.f) && power > -INFINITY;
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
       float S = 0.f, rest = 0.f;                     // a sum and what its additions rounded away
       auto add = [&](float y, float more) {
         const float t = S + y, u = t - S;
@@ -357,17 +339,14 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
       };
       for (int i = lane; i < (int)gridDim.x; i += 32) {
         const float2 st = __ldcg(reinterpret_cast<const float2*>(a.part_stat) + part + i);
-        if (plain && st.y > 0.f) add(st.y * ex2(fmaxf(st.x - power, -120.f)), 0.f);      // a whole power: exact
-        if (!plain && st.y < 0.f && st.x == huge) add(-st.y, 0.f);
+        if (st.y > 0.f) add(st.y * ex2((st.x - M) * LOG2E), 0.f);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) add(__shfl_xor_sync(FULL_MASK, S, o), __shfl_xor_sync(FULL_MASK, rest, o));
       odd = __any_sync(FULL_MASK, odd);
       if (!odd && S > 0.f) {                         // neither a row of -infinity, nor one with NaN or +infinity
-        constexpr double LN2 = 0.69314718055994530942;
         base = (double)sc - log((double)S + (double)rest);
-        if (plain) base -= (double)power * LN2;
-        else top = (double)huge;
+        top = M;
         for (int i0 = 0; i0 < keys; i0 += 32 * KPL) {
           if (i0 > 0) fetch(i0);
           Key left = ~0ull;                          // keys below this one are not taken yet
@@ -392,7 +371,7 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     if (lane >= n) list = 0;
     Key total = 0;
     if (list != 0 && base == base) {
-      const double v = ((double)key_value(list) - top) + base;         // the difference first: both may be huge
+      const double v = ((double)key_value(list) - (double)top) + base;       // the difference first: both may be huge
       const unsigned long long bits = (unsigned long long)__double_as_longlong(v + 0.0);
       if (v > -INFINITY) total = bits >> 63 ? ~bits : bits | (1ull << 63);
     }
