@@ -586,8 +586,8 @@ size_t kva_paged_workspace_zero_bytes(void);
  *   Beam k of group b offers token v with the total scores[b,k] + z[b,k,v] - log sum_u exp(z[b,k,u]).  The n_out largest totals of a
  *   group, descending, equal ones toward the lower beam, then the lower token:
  *     out_beam, out_token [B,n_out] int32, out_score [B,n_out] float32.
- *   A finished beam offers one continuation, (end_id, its score unchanged).  A beam with score -infinity or NaN offers
- *   none, nor does one with a logit of NaN or +infinity; a token with logit -infinity is never offered.
+ *   A finished beam offers one continuation, (end_id, its score unchanged).  A beam whose score is infinite or NaN, finished
+ *   or not, offers none, nor does one with a logit of NaN or +infinity; a token with logit -infinity is never offered.
  *   Places that no offer fills hold beam -1, token -1 and score -infinity.
  *  logits     [B,K,V] of dtype (device), rows row_stride elements apart (0: V; more: a padded table; any alignment of dtype)
  *  scores     [B,K] float32 (device);  finished [B,K] int32 (device; nonzero: finished) or NULL

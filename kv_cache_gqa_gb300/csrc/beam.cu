@@ -8,7 +8,7 @@
 // sorted values), warps keep sorted lists over the whole slice instead.  The last CTA of a group joins the slices: a warp per
 // beam, then a thread per offer, which counts the offers of the other beams before its own (binary searches), by totals in 64 bits
 // (beams that are nearly even keep their order).
-// A beam that is done, or whose score is -infinity, is not read.
+// A beam that is done, or whose score is no finite number, is not read.
 //
 // Sums are float32 per thread and slice, with what their additions round away where slices are joined.  Which thread takes an element
 // depends on its index alone, so equal rows give equal totals.  exp(x - m) is 2^((x - m) log2 e), the difference first: it is exact for
@@ -172,7 +172,7 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
   griddep_launch_dependents();
   const float score = a.scores[row];
   const bool done = a.finished != nullptr && a.finished[row] != 0;
-  if (!done && score > -INFINITY) {
+  if (!done && fabsf(score) < INFINITY) {
     const T* z = reinterpret_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
     const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15u);
     using Part = Batch<T>;
@@ -306,10 +306,11 @@ beam_select_kernel(const __grid_constant__ BeamArgs a) {
     Key list = 0, last = 0;
     double base = NAN;                               // an offer's total is (value - top) + base
     float top = 0.f;
-    if (is_done) {
+    const bool finite = fabsf(sc) < INFINITY;        // else it offers nothing
+    if (finite && is_done) {
       base = (double)sc;
       if (lane == 0) list = key_of(0.f, a.end_id);
-    } else if (sc > -INFINITY) {
+    } else if (finite) {
       const int64_t part = (int64_t)r * gridDim.x;
       const int keys = (int)gridDim.x * n;
       constexpr int KPL = 12;                        // keys of a lane at a time

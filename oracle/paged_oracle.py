@@ -113,11 +113,11 @@ def beam_step(logits, scores, n, finished=None, end_id=0):
         for k in range(K):
             s = float(scores[b, k])
             if finished is not None and finished[b, k]:
-                if s > -math.inf:
+                if math.isfinite(s):
                     offers.append((-s, k, end_id))
                 continue
             z = np.asarray(logits[b, k], F64)
-            if not s > -math.inf or np.isnan(z).any() or (z == math.inf).any() or not (z > -math.inf).any():
+            if not math.isfinite(s) or np.isnan(z).any() or (z == math.inf).any() or not (z > -math.inf).any():
                 continue
             m = z.max()
             total = s + (z - m - math.log(np.exp(z - m).sum()))

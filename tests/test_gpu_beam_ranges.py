@@ -83,3 +83,21 @@ def test_rows_far_from_zero(K, at):  # noqa: F811
     z = (at + step * r.integers(-6, 7, (1, 3, V))).astype(np.float32)
     z[0, 2, : V // 2] -= np.float32(abs(at))                            # half of the row as far again
     run(K, z, -r.random((1, 3)).astype(np.float32), 32, "f32")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_scores_that_are_no_numbers(K, dt):  # noqa: F811
+    """+infinity, -infinity and NaN: such a beam offers nothing, finished or not; scores of the type's largest size are ordinary."""
+    r = np.random.default_rng(34)
+    t, z = given(r.standard_normal((3, 5, 700)), dt)
+    scores = -r.random((3, 5)).astype(np.float32)
+    scores[0, :3] = np.inf, -np.inf, np.nan
+    scores[1] = np.inf, np.inf, -np.inf, np.nan, np.inf
+    scores[2] = 3e38, -3e38, np.inf, 1e30, -1e30
+    for finished in (None, np.tile([True, True, True, False, False], (3, 1)), np.tile([False, False, False, True, True], (3, 1))):
+        beam, token, score = got = select(K, t, scores, 4, finished, 6)
+        want = P.beam_step(z, scores, 4, finished, 6)
+        check([x[:2] for x in got], want[:2])
+        assert (beam[1] == -1).all() and (token[1] == -1).all() and (score[1] == -np.inf).all()
+        first = [b for b, _, _ in want[2]]
+        assert beam[2].tolist() == first and np.allclose(score[2], [u for _, _, u in want[2]], rtol=2.0 ** -23)
