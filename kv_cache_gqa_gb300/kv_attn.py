@@ -218,6 +218,13 @@ def _stream(stream) -> Optional[int]:
     return s.cuda_stream
 
 
+def _keeping(struct, *held):
+    """A descriptor that keeps the tensors and host arrays whose addresses it holds, for the prepared calls made with it: what
+    it was built from may be assigned anew."""
+    struct.held = held
+    return struct
+
+
 @dataclasses.dataclass
 class KVCache:
     """N cache instances: k [N, Hkv, capacity, Dk] and v [N, Hkv, capacity, Dv] torch CUDA
@@ -245,7 +252,7 @@ class KVCache:
             raise KvaError(KVA_EINVAL, "cache tensors must be contiguous")
         N, Hkv, W, D = k.shape
         Dv = v.shape[3]
-        return _Cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), Hkv, D, W, Hkv * W * D, Dv, Hkv * W * Dv)
+        return _keeping(_Cache(k.data_ptr(), v.data_ptr(), _dtype_code(k), Hkv, D, W, Hkv * W * D, Dv, Hkv * W * Dv), k, v)
 
     @property
     def n_kv_heads(self):
@@ -311,8 +318,8 @@ class KVCacheQ4:
         if self.k.shape[:3] != self.v.shape[:3]:
             raise KvaError(KVA_EINVAL, "4-bit cache: k and v must have the same instances, heads and capacity")
         N, Hkv, W, half = self.k.shape
-        return _CacheQ4(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), Hkv, 2 * half, W,
-                        2 * self.v.shape[3], Hkv * W)
+        held = self.k, self.v, self.k_scale, self.v_scale
+        return _keeping(_CacheQ4(*map(_ptr, held), Hkv, 2 * half, W, 2 * self.v.shape[3], Hkv * W), *held)
 
     @property
     def n_kv_heads(self):
@@ -440,7 +447,8 @@ class PreparedCall:
     of tensors into pointers and descriptors is skipped.  The tensors and host arrays it was made
     from must stay alive and keep their storage (their contents may change between calls, which
     is how a decode loop advances its lengths), and the stream is the one current (or given)
-    when it was made."""
+    when it was made.  What a cache or batch held then is kept by the call, which goes on with it when
+    the cache or batch is given other tensors."""
     __slots__ = ("_fn", "_args", "_keep")
 
     def __init__(self, fn, args, keep):
@@ -771,7 +779,7 @@ class PagedKVCache:
                 raise KvaError(KVA_EINVAL, f"paged cache is on {t.device}, not on the current device")
         n, Hkv, page, D = k.shape[-4:]
         apart = lambda t: t.stride(-4) if n > 1 else 0  # noqa: E731
-        return _PagedCache(_ptr(k), _ptr(v), _dtype_code(k), Hkv, D, v.shape[-1], page, n, apart(k), apart(v))
+        return _keeping(_PagedCache(_ptr(k), _ptr(v), _dtype_code(k), Hkv, D, v.shape[-1], page, n, apart(k), apart(v)), k, v)
 
     @property
     def n_pages(self):
@@ -835,8 +843,8 @@ class PagedBatch:
         th, lh, sh = self.table_host, self.lengths_host, self.token_start_host
         if lh.shape != (B,) or sh.shape != (B + 1,) or (th is not None and th.shape != tuple(self.table.shape)):
             raise KvaError(KVA_EINVAL, "host mirrors must have the shapes of lengths, token_start and table")
-        return _PagedBatch(_ptr(self.table), self.table.shape[1], _ptr(self.lengths), _ptr(self.token_start), _ptr(th),
-                           _ptr(lh), _ptr(sh), B)
+        return _keeping(_PagedBatch(_ptr(self.table), self.table.shape[1], _ptr(self.lengths), _ptr(self.token_start), _ptr(th),
+                                    _ptr(lh), _ptr(sh), B), self.table, self.lengths, self.token_start, th, lh, sh)
 
 
 @dataclasses.dataclass(frozen=True)
