@@ -775,6 +775,10 @@ class PagedKVCache:
                 if t.shape[d] != 1 and t.stride(d) != want:
                     raise KvaError(KVA_EINVAL, "a page of the cache must be contiguous")
                 want *= t.shape[d]
+            for d in range(t.dim() - 3):             # 0 elements apart would mean packed pages to the C call
+                if t.shape[d] != 1 and t.stride(d) < want:
+                    raise KvaError(KVA_EINVAL, "the cache's pages overlap")
+        for t in (k, v):
             if _ptr(t) is None or t.device.index != _t().cuda.current_device():
                 raise KvaError(KVA_EINVAL, f"paged cache is on {t.device}, not on the current device")
         n, Hkv, page, D = k.shape[-4:]
