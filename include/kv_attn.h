@@ -567,8 +567,8 @@ kva_status kv_cache_append_paged(
  *  q    [T,Hq,Dk] of the cache's dtype, packed (device);  out [T,Hq,Dv] of out_dtype (device)
  *  A token that sees no slot (a sequence shorter than its new tokens) gives a row of zeros.  Slots at or beyond L are
  *  never used, whatever they hold.  A NaN or infinity in V of a slot that only later tokens of a sequence see may reach the earlier
- *  tokens of the same call.  bf16 caches: softmax weights meet V as bf16 for a bf16 out (as two bf16 parts, 16 bits, in batches
- *  whose sequences have at most 8 query rows a KV head) and as three parts (24 bits) for a float32 one; sums are float32.
+ *  tokens of the same call.  bf16 caches: softmax weights meet V as two bf16 parts (16 bits) for a bf16 out, as one (8 bits) in
+ *  sequences of more than 16 query rows a KV head, and as three (24 bits) for a float32 out; sums, the weights' own too, are float32.
  *  scale      <= 0 selects 1/sqrt(Dk)
  *  workspace  kva_paged_workspace_size(Hkv, Hq, Dv) bytes for calls of any batch; its first
  *             kva_paged_workspace_zero_bytes() bytes are zero before the first call and left so by every call.  Calls

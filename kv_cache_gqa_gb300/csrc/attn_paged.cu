@@ -89,7 +89,8 @@ cudaError_t paged_query_map(CUtensorMap* map, const PagedArgs& a, int width, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// float32 caches: CUDA cores.  bf16 caches: mma.sync tiles of 16 rows for sequences of up to 16 rows a KV head, and for all of
+// float32 caches: CUDA cores.  bf16 caches: mma.sync tiles of 16 rows for sequences of up to 16 rows a KV head (all of them with
+// the same bits, however many rows the batch's others have), and for all of
 // them where the output is float32 (the only form that holds its weights and sums to 24 bits); tcgen05 for the others.
 cudaError_t launch_attn_paged(const PagedArgs& args, int Dk, int Dv, kva_dtype dtype, const int32_t* lengths,
                               const int32_t* start, cudaStream_t s, unsigned* n_launches) {

@@ -8,9 +8,10 @@
 // the softmax keeps a reference maximum that moves only when a score exceeds it by 2^8, and P V follows with P
 // taken from the score registers.  All units' steps are cut into equal runs (paged.cuh), so ragged batches leave no CTA behind.
 //
-// Weights.  With at most 8 rows (ROWS = 8) the tile's other 8 rows hold what rounding a weight to bf16 left, so P
-// carries 16 bits at no cost.  EXACT (a float32 output) adds a third part, 24 bits, and keeps the tensor core's sums to one
-// tile, joined by float32 additions: it cuts sums off towards zero, which over a long run would show (7e-6).
+// Weights meet V as two bf16 parts, 16 bits: a bf16 output's own rounding then outweighs theirs, and a sequence keeps them whoever
+// shares its launch.  With at most 8 rows (ROWS = 8) the tile's other 8 rows hold the second part, at no cost.  EXACT (a float32
+// output) adds a third part, 24 bits, and keeps the tensor core's sums to one tile, joined by float32 additions: it cuts sums
+// off towards zero, which over a long run would show (7e-6).
 //
 // Bound: many long sequences by HBM (64 of 1k to 32k slots at 16/8 heads of 128: 637 us, 6.9 TB/s; 64 of 500 to 4000: 101 us, 5.9
 // TB/s; head dims 192/128 with float32 out: 142 us, 5.9 TB/s, its third part and short sums beside the loads); one sequence
@@ -239,14 +240,10 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
         for (int i = 0; i < 2; ++i) {
           const float p0 = ex2(w[h][2 * i] - m[h]), p1 = ex2(w[h][2 * i + 1] - m[h]);
           hi[h][i] = pack_bf16x2(p0, p1);
-          if constexpr (H == 1 || EXACT) {
-            l[h] += p0 + p1;
-            const float r0 = p0 - bf16_lo(hi[h][i]), r1 = p1 - bf16_hi(hi[h][i]);
-            mid[h][i] = pack_bf16x2(r0, r1);
-            if constexpr (EXACT) lo[h][i] = pack_bf16x2(r0 - bf16_lo(mid[h][i]), r1 - bf16_hi(mid[h][i]));
-          } else {
-            l[h] += bf16_lo(hi[h][i]) + bf16_hi(hi[h][i]);     // the weights that meet V
-          }
+          l[h] += p0 + p1;
+          const float r0 = p0 - bf16_lo(hi[h][i]), r1 = p1 - bf16_hi(hi[h][i]);
+          mid[h][i] = pack_bf16x2(r0, r1);
+          if constexpr (EXACT) lo[h][i] = pack_bf16x2(r0 - bf16_lo(mid[h][i]), r1 - bf16_hi(mid[h][i]));
         }
       // ---- O += P V ----
       {
@@ -275,6 +272,7 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
             } else if constexpr (H == 1) {
               mma16816(o[2 * nd + j], hi[0][0], mid[0][0], hi[0][1], mid[0][1], b0, b1);
             } else {
+              mma16816(o[2 * nd + j], mid[0][0], mid[H - 1][0], mid[0][1], mid[H - 1][1], b0, b1);
               mma16816(o[2 * nd + j], hi[0][0], hi[H - 1][0], hi[0][1], hi[H - 1][1], b0, b1);
             }
           }

@@ -155,3 +155,11 @@ def test_sums_over_a_long_run(K, Dk, Dv):
     want = (w @ v) / w.sum(1, keepdims=True)
     err = np.abs(host(o)[:, 0] - want) / want
     assert err.max() <= 4e-6 + PLAIN, err.max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Dk,Dv", DIMS)
+@pytest.mark.parametrize("new,G", [([1, 8, 1, 1], 2), ([1, 2, 1], 8), ([1] * 5 + [16], 1)])
+def test_a_neighbour_takes_no_bits(K, new, G, Dk, Dv):
+    """Sequences of up to 16 rows a KV head keep 16 bits, whoever shares their batch."""
+    check(K, new, G, "bf16", Dk, Dv)
