@@ -565,9 +565,9 @@ kva_status kv_cache_append_paged(
  *     o_i = softmax_j(q_i . K[g, j] * scale, j <= L - T + i) V[g, j]      (new token i of a sequence of T)
  *   One call takes any mix of single tokens, draft blocks and prompt chunks behind a cached prefix.
  *  q    [T,Hq,Dk] of the cache's dtype, packed (device);  out [T,Hq,Dv] of out_dtype (device)
- *  A token that sees no slot (a sequence shorter than its new tokens) gives a row of zeros.  Slots at or beyond L are
- *  never used, whatever they hold.  A NaN or infinity in V of a slot that only later tokens of a sequence see may reach the earlier
- *  tokens of the same call.  bf16 caches: softmax weights meet V as two bf16 parts (16 bits) for a bf16 out, as one (8 bits) in
+ *  A token that sees no slot (a sequence shorter than its new tokens) gives a row of zeros.  Slots that a token does not see,
+ *  later tokens' and those at or beyond L, never reach its output, whatever they hold; a NaN or infinity in V of one that it
+ *  sees gives NaN or infinities.  bf16 caches: softmax weights meet V as two bf16 parts (16 bits) for a bf16 out, as one (8 bits) in
  *  sequences of more than 16 query rows a KV head, and as three (24 bits) for a float32 out; sums, the weights' own too, are float32.
  *  scale      <= 0 selects 1/sqrt(Dk)
  *  workspace  kva_paged_workspace_size(Hkv, Hq, Dv) bytes for calls of any batch; its first

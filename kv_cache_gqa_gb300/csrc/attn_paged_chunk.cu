@@ -12,7 +12,8 @@
 //   0-3, 4-7  softmax of slots 0 and 1, a row a thread: scores from tensor memory, the row's limit, a lazily moved reference
 //             maximum (O is rescaled when a score exceeds it by 2^8), P = exp2(S - m) written back over S as bf16.
 //   8, 10     TMA of Q and K, and of V.  A key tile is a box for each page it touches; the warp holds the next page ids a lane
-//             each.  Slots of a tile at or beyond L are zeroed in V (they may hold anything, and 0 * NaN is NaN).
+//             each.  Slots of a tile at or beyond L are zeroed in V (they may hold anything, and 0 * NaN is NaN), and so are NaNs and
+//             infinities in slots that only some rows of the unit see; the rows that do see them get their NaN at the end.
 //   9, 11     issue the products of slots 0 and 1 from converged warps (one elected lane): O += P V for a tile, in two halves as
 //             the softmax hands them over, then S of the slot's next tile into the same columns.  One warp for both slots was busy
 //             all the time with its waits, descriptors and commits (4100 cycles a step; the products take 2048).
@@ -31,9 +32,12 @@ namespace kva {
 namespace {
 
 using paged::ex2;
+using paged::finite_pair;
 using paged::M_NONE;
 using paged::Place;
 using paged::Run;
+using paged::saw_odd;
+using paged::see_pair;
 using paged::Seq;
 
 constexpr int BM = 128, BN = 128;          // query rows of a slot, keys of a tile
@@ -78,6 +82,8 @@ struct CutPairs {
     return min(max(s.L - s.T + min(s.T, (rt + 1) * tpt), 0), s.L);
   }
   __device__ __forceinline__ int key_tiles(const Seq& s, int rt) const { return (visible(s, rt) + BN - 1) / BN; }
+  // slots that all rows of unit z see
+  __device__ __forceinline__ int common(const Seq& s, int z) const { return min(max(s.L - s.T + 2 * z * tpt + 1, 0), s.L); }
   __device__ __forceinline__ bool halves(const Seq& s, int z) const { return 2 * z + 1 >= row_tiles(s); }
   __device__ __forceinline__ int steps(const Seq& s, int z) const {
     return halves(s, z) ? max(1, (key_tiles(s, 2 * z) + 1) / 2) : max(1, key_tiles(s, 2 * z + 1));
@@ -96,6 +102,7 @@ struct Piece {
   int st0, st1, j0, n, c[2];
   bool halves, whole;
   int tail;                                  // entry of the tile that holds L (its slots from L on are zeroed in V), or -1
+  int clean;                                 // first entry with slots that not all rows see (V is cleaned there and in those behind it)
   __device__ __forceinline__ int entry(int s, int k) const { return halves ? 2 * k + s : k; }
 };
 __device__ __forceinline__ Piece piece_of(const CutPairs& cut, const Place& p, const Run& run) {
@@ -117,6 +124,7 @@ __device__ __forceinline__ Piece piece_of(const CutPairs& cut, const Place& p, c
   }
   const int at = p.s.L / BN - q.j0;
   q.tail = p.s.L % BN != 0 && at >= 0 && at < q.n ? at : -1;
+  q.clean = max(0, min(cut.common(p.s, p.rt) / BN - q.j0, q.n));
   return q;
 }
 
@@ -233,6 +241,60 @@ __device__ __noinline__ void nan_rows(Walk& w, const PagedArgs& a, const CutPair
   }
 }
 
+// What the cleaning of V took (NaNs and infinities) makes NaN of those columns in the rows that see it: all pieces of the CTA's run
+// again, for the row of this thread.  Whole warp; out of line: only where V holds such numbers.
+template <int DV>
+__device__ __noinline__ void odd_rows(Walk& w, const Place& begin, const PagedArgs& a, const CutPairs& cut, const Run& run, int s, int t) {
+  constexpr int PER = DV / 32;              // columns of a lane
+  const int lane = t & 31;
+  __syncwarp();
+  if (lane == 0) {
+    w.p = begin;
+    w.q = piece_of(cut, begin, run);
+  }
+  __syncwarp();
+  for (bool more = true; more; more = enter(w, a, cut, run, false, lane)) {
+    const Place& p = w.p;
+    const int token = (2 * p.rt + s) * cut.tpt + t / cut.G;
+    const int lim = t < cut.tpt * cut.G && token < p.s.T ? min(max(p.s.L - p.s.T + token + 1, 0), p.s.L) : 0;
+    const int tiles = w.q.halves ? (s == 0 ? w.q.n : 0) : w.q.c[s];     // slot 0 writes both slots' halves
+    const int from = max(cut.common(p.s, p.rt), w.q.j0 * BN);
+    const int to = min((w.q.j0 + tiles) * BN, lim), last = __reduce_max_sync(FULL_MASK, to);
+    for (int key = from; key < last; ++key) {
+      const int page = a.table[(int64_t)p.b * a.table_stride + (key >> a.page_shift)];
+      if ((unsigned)page >= (unsigned)a.n_pages) continue;
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v) + page * a.page_stride_v +
+                          (int64_t)((p.g << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * DV + lane * PER;
+      uint32_t odd = 0u;                    // this lane's columns
+#pragma unroll
+      for (int e = 0; e < PER; ++e) odd |= ((v[e] & 0x7f80u) == 0x7f80u ? 1u : 0u) << e;
+      for (unsigned hits = __ballot_sync(FULL_MASK, odd != 0u); hits; hits &= hits - 1) {
+        const int h = __ffs(hits) - 1;
+        for (uint32_t bits = __shfl_sync(FULL_MASK, odd, h); bits; bits &= bits - 1) {
+          const int d = h * PER + __ffs(bits) - 1;
+          if (key >= to) continue;
+          if (w.q.whole) {
+            reinterpret_cast<uint16_t*>(a.out)[((int64_t)(p.s.t0 + token) * a.Hq + p.g * cut.G + t % cut.G) * DV + d] = 0x7fc0;
+          } else {
+            const int64_t part = blockIdx.x * 2 + (run.x0 >= p.at ? 0 : 1);
+            a.part_acc[(((part * 2 + s) * (DV / 4) + d / 4) * BM + t) * 4 + d % 4] = NAN;
+          }
+        }
+      }
+    }
+  }
+}
+
+// NaNs and infinities of a lane's 16 bytes in rows r, r + 32 / W, .. below `to` become zeros.  Out of line, as above.
+template <int W>
+__device__ __noinline__ void clean_rows(uint8_t* at, int r, int to) {
+  for (; r < to; r += 32 / W) {
+    uint4* x = reinterpret_cast<uint4*>(at + r * 128);
+    const uint4 v = *x;
+    *x = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+  }
+}
+
 template <int D, int DV>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap tmK,
@@ -256,16 +318,18 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
   uint64_t* o_free = bars + 16;    // [slot] O copied out (by 4 warps)
   uint64_t* q_full = bars + 18;    // the piece's Q landed
   uint64_t* q_free = bars + 19;    // both slots' last Q K^T of the piece done
-  uint64_t* v_clean = bars + 20;   // [NV] the tile that holds L has its V cleaned
+  uint64_t* v_clean = bars + 20;   // [NV] a tile with slots that not all rows see has its V cleaned
   uint64_t* ml_full = bars + 22;   // slot 1's maxima and sums of a halves piece published (4 warps)
   uint64_t* ml_free = bars + 23;   // and read by slot 0 (4 warps)
   uint64_t* turn = bars + 24;      // [slot] the slot's products of a round have been issued
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 27);
   volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(bars + 28);   // pieces (modulo 32) with a page id outside the pool
+  volatile int* s_odd = reinterpret_cast<volatile int*>(bars + 29);             // the cleaning of V took something, now or before
   __shared__ int64_t scratch[THREADS / 32 + 4];
   __shared__ Run run;
   __shared__ Walk walks[THREADS / 32];
+  __shared__ Place run_begin;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
@@ -282,6 +346,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     mbar_init(ml_full, SOFTMAX_WARPS / 2); mbar_init(ml_free, SOFTMAX_WARPS / 2);
     *s_abort = 0;
     *s_bad = 0u;
+    *s_odd = 0;
     fence_mbar_init();
   }
   if (warp == K_WARP && lane == 0) { tc::tma_prefetch_desc(&tmK); tc::tma_prefetch_desc(&tmV); tc::tma_prefetch_desc(&tmQ); }
@@ -298,6 +363,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     if (lane == 0) walk.p = first;
     if (tid == 0) {
       run = mine;
+      run_begin = first;
       a.joins[blockIdx.x].last = -1;
     }
   }
@@ -351,16 +417,27 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           if (it >= NV && !warp_wait(&v_free[st], it / NV - 1)) { ok = false; break; }
           uint8_t* dst = sm + LY::V_OFF + st * NSUBV * SUB;
           load_tile<NSUBV>(a, &tmV, pg, pc.j0 + i, p.g, dst, &v_full[st], lane);
-          if (i == pc.tail) {
+          if (i >= pc.clean) {
             if (!warp_wait(&v_full[st], it / NV)) { ok = false; ++it; break; }
-            const int from = p.s.L % BN;
-            for (int x = lane; x < (BN - from) * 8 * NSUBV; x += 32) {
-              const int row = from + x / (8 * NSUBV), ch = x % (8 * NSUBV);
-              *reinterpret_cast<uint4*>(dst + (ch >> 3) * SUB + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+            constexpr int W = 8 * NSUBV;        // 16-byte pieces of a row: a lane takes the same one of every 32 / W-th row
+            const int to = i == pc.tail ? p.s.L % BN : BN, from = min(max(cut.common(p.s, p.rt) - (pc.j0 + i) * BN, 0), to);
+            uint8_t* at = dst + (lane % W >> 3) * SUB + (lane & 7) * 16;
+            uint32_t seen = 0u;
+#pragma unroll 2                                // what runs once a unit pays for its instructions' way here: 8 took longer
+            for (int r = from + lane / W; r < to; r += 32 / W) {
+              const uint4 v = *reinterpret_cast<const uint4*>(at + r * 128);
+              see_pair(seen, v.x); see_pair(seen, v.y); see_pair(seen, v.z); see_pair(seen, v.w);
             }
+#pragma unroll 1
+            for (int r = to + lane / W; r < BN; r += 32 / W) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
+            const bool odd = __any_sync(FULL_MASK, saw_odd(seen));
+            if (odd) clean_rows<W>(at, from + lane / W, to);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_clean[st]);
+            if (lane == 0) {
+              if (odd) *s_odd = 1;
+              mbar_arrive(&v_clean[st]);
+            }
           }
         }
         if (*s_abort) ok = false;
@@ -375,7 +452,8 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       const uint64_t v_desc = tc::desc_at(DESC_VMN, smem_u32(sm + LY::V_OFF));
       // descriptor start addresses advance by constant offsets (addresses stay below 2^18)
       constexpr uint64_t BOX = (uint64_t)SUB >> 4;
-      int tails[2] = {0, 0};                    // cleaned tiles of a V stage so far
+      static_assert(NV == 2, "cleaned tiles are counted by two stages");
+      int cleaned[2] = {0, 0};                  // tiles of a V stage so far
       int tiles = 0, used = 0;                  // the slot's tiles, and pieces with any, so far
       int rounds = 0;                           // turns taken so far
       for (bool first = true; ok && enter(walk, a, cut, run, first, lane); first = false, ++np) {
@@ -441,7 +519,7 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
           if (NK > 1 && k + 1 < c) wait_k(k + 1);
           pass_v(e);
           ok = ok && warp_wait(&v_full[st], e / NV);
-          if (e - it == pc.tail) ok = ok && warp_wait(&v_clean[st], tails[st]);
+          if (e - it >= pc.clean) ok = ok && warp_wait(&v_clean[st], cleaned[st] + ((e - it - pc.clean) >> 1));
           // the first P V of a piece overwrites O: the one before must have been read
           if (k == 0 && used > 0) ok = ok && warp_wait(&o_free[s], used - 1);
           if (!ok) break;
@@ -470,7 +548,9 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
         it += pc.n;
         pass_k(it);
         pass_v(it);
-        if (pc.tail >= 0) ++tails[(it - pc.n + pc.tail) % NV];
+        const int first_clean = (it - pc.n + pc.clean) & 1, clean = pc.n - pc.clean;
+        cleaned[0] += (clean + 1 - first_clean) >> 1;
+        cleaned[1] += (clean + first_clean) >> 1;
         tiles += c;
         used += c > 0;
         if (*s_abort) ok = false;
@@ -686,6 +766,8 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
     if (!ok) {
       *s_abort = 1;
       nan_rows<DV>(walk, a, cut, run, s, t);
+    } else if (pieces > 0 && __any_sync(FULL_MASK, *s_odd != 0)) {
+      odd_rows<DV>(walk, run_begin, a, cut, run, s, t);
     }
   }
   tc::fence_before_sync();

@@ -191,9 +191,7 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
         break;
       }
       const int n = min(KT, lim_all - ks);
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        float vv[NC];
+      auto value = [&](int j, float (&vv)[NC]) {
         if constexpr (NC == 4) {
           const float4 x = *reinterpret_cast<const float4*>(tile_v + j * DV + lane * 4);
           vv[0] = x.x; vv[1] = x.y; vv[2] = x.z; vv[3] = x.w;
@@ -201,6 +199,12 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
           const float2 x = *reinterpret_cast<const float2*>(tile_v + j * DV + lane * 2);
           vv[0] = x.x; vv[1] = x.y;
         }
+      };
+      const int common = max(0, min(n, lim[0] - ks));        // keys that all rows see (the first row sees the fewest)
+#pragma unroll 8
+      for (int j = 0; j < common; ++j) {
+        float vv[NC];
+        value(j, vv);
 #pragma unroll
         for (int r = 0; r < R; r += 4) {
           const float4 w = *reinterpret_cast<const float4*>(sm_p + j * R + r);
@@ -212,6 +216,19 @@ attn_paged_simt_kernel(const __grid_constant__ PagedArgs a) {
             o[r + 3][c] = fmaf(w.w, vv[c], o[r + 3][c]);
           }
         }
+      }
+      // The others, one less than the tile has tokens, meet only the rows that see them: a weight of 0 would make NaN of a NaN.
+#pragma unroll 1
+      for (int j = common; j < n; ++j) {
+        float vv[NC];
+        value(j, vv);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (ks + j < lim[r]) {
+            const float w = sm_p[j * R + r];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[r][c] = fmaf(w, vv[c], o[r][c]);
+          }
       }
       __syncwarp();                             // V and the weights are read
       if (u + 1 < n_mine) copy_v();

@@ -29,8 +29,11 @@ namespace {
 
 using paged::Cut;
 using paged::ex2;
+using paged::finite_pair;
 using paged::M_NONE;
 using paged::Place;
+using paged::saw_odd;
+using paged::see_pair;
 
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int KT = 16;                          // keys of a warp's tile
@@ -168,11 +171,40 @@ attn_paged_step_kernel(const __grid_constant__ PagedArgs a, const __grid_constan
       }
       unsigned char* stg = ring + slot * S::STAGE;
       const int ks = first + u * (KT * WARPS);
-      if (ks + KT > lim_all) {                  // keys that nobody sees: zero V so that 0 * V stays 0
-        const int nk = lim_all - ks;
+      if (ks + KT > lim_min) {                  // keys that some rows, or none, see: 0 times what they do not see must be 0
+        unsigned char* sv = stg + KB * BOX;
+        if (lim_min < lim_all) {
+          uint32_t seen = 0u;
+          for (int i = lane; i < KT * DV / 8; i += 32) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sv + i * 16);
+            see_pair(seen, x.x); see_pair(seen, x.y); see_pair(seen, x.z); see_pair(seen, x.w);
+          }
+          if (__builtin_expect(__any_sync(FULL_MASK, saw_odd(seen)), 0)) {
+#pragma unroll 1
+            for (int j = 0; j < KT; ++j)        // a NaN or infinity: NaN for the rows that see it,
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(sv + (n >> 3) * BOX + swz(j, n & 7) + 4 * t), odd = x ^ finite_pair(x);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                  if ((odd & 0xffffu) && ks + j < lim[h]) o[n][2 * h] = NAN;
+                  if ((odd >> 16) && ks + j < lim[h]) o[n][2 * h + 1] = NAN;
+                }
+              }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = lane; i < KT * DV / 8; i += 32) {           // and 0 for the products
+              uint4* x = reinterpret_cast<uint4*>(sv + i * 16);
+              const uint4 v = *x;
+              *x = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+            }
+            fence_proxy_async_smem();           // before the stage's next copies
+          }
+        }
+        const int nk = max(0, lim_all - ks);
         for (int i = lane; i < (KT - nk) * (DV / 8); i += 32) {
           const int key = nk + i / (DV / 8), ch = i % (DV / 8);
-          *reinterpret_cast<uint4*>(stg + (KB + ch / 8) * BOX + swz(key, ch % 8)) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sv + (ch / 8) * BOX + swz(key, ch % 8)) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
       }

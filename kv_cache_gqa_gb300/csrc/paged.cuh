@@ -17,6 +17,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A pair of bf16 numbers, its NaNs and infinities as zeros.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+// Notes in `seen` (0 at first) whether one of a pair is NaN or infinite: an exponent of ones carries into bit 15 or 31.
+__device__ __forceinline__ void see_pair(uint32_t& seen, uint32_t w) { seen |= (w & 0x7f807f80u) + 0x00800080u; }
+__device__ __forceinline__ bool saw_odd(uint32_t seen) { return (seen & 0x80008000u) != 0u; }
+
 // A whole warp waits for the phase of this parity, up to WAIT_LIMIT_NS; false if it gave up.  With a hint the hardware suspends
 // the warp for up to so many nanoseconds and wakes it when the phase ends.  Without, it looks again every few hundred cycles,
 // and the issue slots that takes were the softmax warps' (a 2048-token chunk behind 30000 slots: 821 us, with the hint 657).
