@@ -1,36 +1,11 @@
-// Steps of a q or K row that the quantising and the paged append share: the norm's sum, the rotation's
-// angles, and products of pairs.
+// Steps of a q or K row that the quantising and the paged append share: the rotation's angles and products of pairs.  (Their
+// norms differ: the quantising one's sum is strided over a copy in shared memory, the paged one's is over the lanes' registers.)
 #pragma once
 
 #include "common.cuh"
 
 namespace kva {
 namespace {
-
-// Sum of squares of a row of D values in shared memory, by its SW lanes: strided sums l, l + 32, ... (the
-// lanes read without bank conflicts), then pairs of neighbouring sums.
-template <int SW>
-__device__ __forceinline__ float sum_squares(const float* row, int D, int sl) {
-  constexpr int NL = 32 / SW;                             // strided sums a lane keeps
-  float v[NL];
-#pragma unroll
-  for (int j = 0; j < NL; ++j) {
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < D; i += 128)
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (i + 32 * m < D) {
-          const float x = row[i + 32 * m + sl + SW * j], q = __fmul_rn(x, x);
-          f[m] = i == 0 ? q : __fadd_rn(f[m], q);
-        }
-    v[j] = __fadd_rn(__fadd_rn(__fadd_rn(f[0], f[1]), f[2]), f[3]);
-#pragma unroll
-    for (int o = 1; o < SW; o <<= 1) v[j] = __fadd_rn(v[j], __shfl_xor_sync(FULL_MASK, v[j], o));
-  }
-  if constexpr (NL == 1) return v[0];
-  else if constexpr (NL == 2) return __fadd_rn(v[0], v[1]);
-  else return __fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3]));
-}
 
 // cos and sin of the angle p * inv (inv = ih + il) in float32, off by at most 3.5e-8 (half an ulp below 1 is
 // 3.0e-8; 1 in 400 is not the correctly rounded value).  For |p| < 2^20 the angle is a pair of floats, brought
