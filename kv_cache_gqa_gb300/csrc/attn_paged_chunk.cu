@@ -224,42 +224,36 @@ __device__ __forceinline__ bool enter(Walk& w, const PagedArgs& a, const CutPair
   return w.more != 0;
 }
 
-// A wait gave up: the rows of this thread from the walk's piece on become NaN.  Out of line: never in a healthy launch.
+// What is left to do to the row of this thread when something was wrong.  gave_up: a wait did, and the rows from the walk's piece on
+// become NaN.  Else the cleaning of V took NaNs or infinities, which make NaN of their columns in the rows that see them: all pieces
+// of the CTA's run again.  Whole warp.  Out of line, and one function: a second call in the kernel costs the softmax registers.
 template <int DV>
-__device__ __noinline__ void nan_rows(Walk& w, const PagedArgs& a, const CutPairs& cut, const Run& run, int s, int t) {
-  bool more = w.more != 0;
-  for (; more; more = enter(w, a, cut, run, false, t & 31)) {
-    const Place& p = w.p;
-    if (w.q.halves && s == 1) continue;
-    if (!w.q.whole)                                                    // a part: whoever joins it finds NaN
-      reinterpret_cast<float2*>(a.part_ml)[((int64_t)(blockIdx.x * 2 + (run.x0 >= p.at ? 0 : 1)) * 2 + s) * BM + t] =
-          make_float2(M_NONE, NAN);
-    const int token = (2 * p.rt + s) * cut.tpt + t / cut.G;
-    if (t >= cut.tpt * cut.G || token >= p.s.T) continue;
-    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)(p.s.t0 + token) * a.Hq + p.g * cut.G + t % cut.G) * DV;
-    for (int d = 0; d < DV; ++d) o[d] = 0x7fc0;
-  }
-}
-
-// What the cleaning of V took (NaNs and infinities) makes NaN of those columns in the rows that see it: all pieces of the CTA's run
-// again, for the row of this thread.  Whole warp; out of line: only where V holds such numbers.
-template <int DV>
-__device__ __noinline__ void odd_rows(Walk& w, const Place& begin, const PagedArgs& a, const CutPairs& cut, const Run& run, int s, int t) {
+__device__ __noinline__ void mend_rows(Walk& w, const Place& begin, const PagedArgs& a, const CutPairs& cut, const Run& run, int s, int t,
+                                       bool gave_up) {
   constexpr int PER = DV / 32;              // columns of a lane
   const int lane = t & 31;
   __syncwarp();
-  if (lane == 0) {
+  if (!gave_up && lane == 0) {
     w.p = begin;
-    w.q = piece_of(cut, begin, run);
+    w.more = begin.b < a.B && begin.at < run.x1;
+    if (w.more) w.q = piece_of(cut, begin, run);
   }
   __syncwarp();
-  for (bool more = true; more; more = enter(w, a, cut, run, false, lane)) {
+  for (bool more = w.more != 0; more; more = enter(w, a, cut, run, false, lane)) {
     const Place& p = w.p;
+    if (w.q.halves && s == 1) continue;     // slot 0 writes both slots' halves
     const int token = (2 * p.rt + s) * cut.tpt + t / cut.G;
-    const int lim = t < cut.tpt * cut.G && token < p.s.T ? min(max(p.s.L - p.s.T + token + 1, 0), p.s.L) : 0;
-    const int tiles = w.q.halves ? (s == 0 ? w.q.n : 0) : w.q.c[s];     // slot 0 writes both slots' halves
+    const bool row_ok = t < cut.tpt * cut.G && token < p.s.T;
+    const int64_t part = (int64_t)(blockIdx.x * 2 + (run.x0 >= p.at ? 0 : 1)) * 2 + s;
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)(p.s.t0 + token) * a.Hq + p.g * cut.G + t % cut.G) * DV;
+    if (gave_up) {
+      if (!w.q.whole) reinterpret_cast<float2*>(a.part_ml)[part * BM + t] = make_float2(M_NONE, NAN);   // whoever joins it finds NaN
+      for (int d = 0; row_ok && d < DV; ++d) out[d] = 0x7fc0;
+      continue;
+    }
+    const int lim = row_ok ? min(max(p.s.L - p.s.T + token + 1, 0), p.s.L) : 0;
     const int from = max(cut.common(p.s, p.rt), w.q.j0 * BN);
-    const int to = min((w.q.j0 + tiles) * BN, lim), last = __reduce_max_sync(FULL_MASK, to);
+    const int to = min((w.q.j0 + (w.q.halves ? w.q.n : w.q.c[s])) * BN, lim), last = __reduce_max_sync(FULL_MASK, to);
     for (int key = from; key < last; ++key) {
       const int page = a.table[(int64_t)p.b * a.table_stride + (key >> a.page_shift)];
       if ((unsigned)page >= (unsigned)a.n_pages) continue;
@@ -273,25 +267,11 @@ __device__ __noinline__ void odd_rows(Walk& w, const Place& begin, const PagedAr
         for (uint32_t bits = __shfl_sync(FULL_MASK, odd, h); bits; bits &= bits - 1) {
           const int d = h * PER + __ffs(bits) - 1;
           if (key >= to) continue;
-          if (w.q.whole) {
-            reinterpret_cast<uint16_t*>(a.out)[((int64_t)(p.s.t0 + token) * a.Hq + p.g * cut.G + t % cut.G) * DV + d] = 0x7fc0;
-          } else {
-            const int64_t part = blockIdx.x * 2 + (run.x0 >= p.at ? 0 : 1);
-            a.part_acc[(((part * 2 + s) * (DV / 4) + d / 4) * BM + t) * 4 + d % 4] = NAN;
-          }
+          if (w.q.whole) out[d] = 0x7fc0;
+          else a.part_acc[((part * (DV / 4) + d / 4) * BM + t) * 4 + d % 4] = NAN;
         }
       }
     }
-  }
-}
-
-// NaNs and infinities of a lane's 16 bytes in rows r, r + 32 / W, .. below `to` become zeros.  Out of line, as above.
-template <int W>
-__device__ __noinline__ void clean_rows(uint8_t* at, int r, int to) {
-  for (; r < to; r += 32 / W) {
-    uint4* x = reinterpret_cast<uint4*>(at + r * 128);
-    const uint4 v = *x;
-    *x = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
   }
 }
 
@@ -431,7 +411,13 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
 #pragma unroll 1
             for (int r = to + lane / W; r < BN; r += 32 / W) *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
             const bool odd = __any_sync(FULL_MASK, saw_odd(seen));
-            if (odd) clean_rows<W>(at, from + lane / W, to);
+            if (odd)
+#pragma unroll 1
+              for (int r = from + lane / W; r < to; r += 32 / W) {
+                uint4* x = reinterpret_cast<uint4*>(at + r * 128);
+                const uint4 v = *x;
+                *x = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+              }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -763,12 +749,8 @@ attn_paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_consta
       ++pieces;
       if (*s_abort) { ok = false; break; }      // (a piece that is through is written again: NaN)
     }
-    if (!ok) {
-      *s_abort = 1;
-      nan_rows<DV>(walk, a, cut, run, s, t);
-    } else if (pieces > 0 && __any_sync(FULL_MASK, *s_odd != 0)) {
-      odd_rows<DV>(walk, run_begin, a, cut, run, s, t);
-    }
+    if (!ok) *s_abort = 1;
+    if (!ok || __any_sync(FULL_MASK, *s_odd != 0)) mend_rows<DV>(walk, run_begin, a, cut, run, s, t, !ok);
   }
   tc::fence_before_sync();
   __syncthreads();
