@@ -593,7 +593,8 @@ size_t kva_paged_workspace_zero_bytes(void);
  *  scores     [B,K] float32 (device);  finished [B,K] int32 (device; nonzero: finished) or NULL
  *  end_id     0 <= end_id < V with `finished`, else not read
  *  workspace  kva_beam_workspace_size(B, K, V) bytes, which also serve smaller calls over the same V; its first
- *             kva_beam_workspace_zero_bytes() bytes are zero before the first call and left so by every call.
+ *             kva_beam_workspace_zero_bytes() bytes are zero before the first call and left so by every call.  Calls
+ *             sharing one workspace must not overlap on the GPU.
  *  1 <= K, n_out <= KVA_BEAM_MAX, n_out <= K * V, B <= 4096.  B == 0 is a no-op. */
 #define KVA_BEAM_MAX 32
 kva_status beam_select(

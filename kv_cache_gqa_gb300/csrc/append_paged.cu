@@ -8,9 +8,11 @@
 // at a time in token_start, its slot is L - T + i, and the table names the page; the rows' loads go out first.
 //
 // Bound: long appends by HBM in principle (24 chunks of 64 to 1024 tokens, 16/8 heads of 128, 149 MB: 45 us, 3.3 TB/s), in fact by
-// the instructions and the latency of a row (load, sum over its lanes, turn) at 32 warps an SM, and by a last round of CTAs that
-// is two thirds full.  There: 3 / 4 / 5 CTAs an SM 51 / 45 / 45 us, with the turn through shared memory 53 / 47 / 59 (and 2 / 3 /
-// 4 / 6 sets ahead 47 / 49 / 50 / 57; a CTA a token 83).  64 tokens: latency (4.5 us).
+// the instructions and the latency of a row (load, sum over its lanes, turn) at 32 warps an SM (55% of issue slots, a third of DRAM's
+// throughput), and by a last round of CTAs that is two thirds full.  There: 3 / 4 / 5 CTAs an SM 51 / 45 / 45 us, with the turn
+// through shared memory 53 / 47 / 59 (and 2 / 3 / 4 / 6 sets ahead 47 / 49 / 50 / 57; a CTA a token 83).  The same rows in other forms: no
+// turn 33.5 us, sections 45, 2D 47, the last 64 dims interleaved 43.5; float32 in and out (299 MB) 49, 57, 60 and 56 us.  64 tokens:
+// latency (4.4 us).
 //
 // Method: the append of the decode step (Youtu-VL-4B ncnn port, step 6) with per-head RMSNorm and rotate-half
 // RoPE (Penguin-VL ncnn port, sections 2.1 and 4.2; Youtu-VL-4B ncnn port, implementation difficulty 2).

@@ -9,9 +9,9 @@
 // when a score exceeds it by 2^8.
 //
 // Bound: long chunks by shared-memory reads (each key's q values, 16 rows of them, beside 64 multiply-adds per 4 dims): 512
-// tokens behind 1536 slots at 16/8 heads of 128 take 368 us (14 TFLOP/s; lanes that read K and V from global
-// memory themselves took 530).  Small batches by latency: one 768-slot sequence 14.6 us (34 so), seven ragged sequences
-// 21 us (25 so).  64 single tokens over 500 to 4000 slots: 350 us, 3.6 TB/s, a tile of K and V at a time on its way.
+// tokens behind 1536 slots at 16/8 heads of 128 take 370 us (20 TFLOP/s; lanes that read K and V from global
+// memory themselves took 530), 2000 from the first one 1108.  Small batches by latency: one 768-slot sequence 14.6 us (34 so), seven
+// ragged sequences 21.6 us (25 so).  64 single tokens over 500 to 4000 slots: 353 us, 3.6 TB/s, a tile of K and V at a time on its way.
 //
 // Method: one pass over the keys with the running maximum and sum of the softmax; the visible prefix of a
 // token as in the decode and verify steps (Youtu-VL-4B ncnn port, step 8; HunyuanOCR v1.5 ncnn port, section

@@ -13,9 +13,11 @@
 // output) adds a third part, 24 bits, and keeps the tensor core's sums to one tile, joined by float32 additions: it cuts sums
 // off towards zero, which over a long run would show (7e-6).
 //
-// Bound: many long sequences by HBM (64 of 1k to 32k slots at 16/8 heads of 128: 637 us, 6.9 TB/s; 64 of 500 to 4000: 101 us, 5.9
-// TB/s; head dims 192/128 with float32 out: 142 us, 5.9 TB/s, its third part and short sums beside the loads); one sequence
-// by latency (768 slots 10 us, 8192 16 us: the plan, a table read, one ring's loads, the join of the parts).
+// Bound: many long sequences by HBM (64 of 1k to 32k slots at 16/8 heads of 128, 4.7 GB: 673 us, 7.0 TB/s; 64 of 500 to 4000, 650 MB:
+// 108 us, 6.0 TB/s; 64 blocks of 4 and of 8 tokens over 2048 slots 90 and 96 us; 16 blocks of head dims 192/128 with float32 out, 892 MB:
+// 145 us, 6.1 TB/s, its third part and short sums beside the loads); one sequence by latency (768 slots 10.4 us: the plan, a table
+// read, one ring's loads, the join of the parts).  Chunks with float32 out read K and V again for every 16 rows: 512 tokens behind 1536
+// slots 95 us, 2048 behind 30000 at 32/8 heads 7.0 ms (the tcgen05 form's bf16 out: 0.74).
 //
 // Method: one pass over the keys with the running maximum and sum of the softmax; GQA by repeat-interleave
 // grouping (Penguin-VL ncnn port, section 3), the visible prefix of decode and verify steps (Youtu-VL-4B ncnn

@@ -16,8 +16,9 @@
 // is taken from it, would be off by more than float32's exponents hold).  Slices hand over (maximum, sum).  Totals are 64-bit: the value
 // less the row's maximum, plus the score less the sum's logarithm (64-bit arithmetic is slow here: a logarithm takes 1.2 us).
 //
-// Bound: 32 x 8 beams over 151643 bf16 values by the reading's instructions and the slices' ends (31.5 us; 78 MB, 60% of them read, are
-// 7 us of HBM); one sequence's 4 beams over 151936 float32 values by latency (12.9 us: a slice's pass, its sort, the join).
+// Bound: 32 x 8 beams over 151643 bf16 values by the slices' ends (30 us; 78 MB, 60% of them read, are 7 us of HBM, and the pass's
+// instructions about 5; 1024 CTAs on 608 places spend 7 us each beside reading, in sorts and barriers); one sequence's 4 beams over
+// 151936 float32 values by latency (12.7 us: a slice's pass, its sort, the join).
 //
 // The runtime's own options (HunyuanOCR v1.5 ncnn port, section 3.6) stop at top_k; it has no beams.
 #include <algorithm>

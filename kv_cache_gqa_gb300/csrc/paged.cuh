@@ -29,7 +29,7 @@ __device__ __forceinline__ bool saw_odd(uint32_t seen) { return (seen & 0x800080
 
 // A whole warp waits for the phase of this parity, up to WAIT_LIMIT_NS; false if it gave up.  With a hint the hardware suspends
 // the warp for up to so many nanoseconds and wakes it when the phase ends.  Without, it looks again every few hundred cycles,
-// and the issue slots that takes were the softmax warps' (a 2048-token chunk behind 30000 slots: 821 us, with the hint 657).
+// and the issue slots that takes were the softmax warps' (a 2048-token chunk behind 30000 slots: 821 us, with the hint 680).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   constexpr uint32_t HINT_NS = 1000000;
   uint64_t t0 = 0;
